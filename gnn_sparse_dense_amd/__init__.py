@@ -49,7 +49,30 @@ EXPORTED = (
     "spmm_coo_to_csr", "spmm_plan_transpose", "spmm_max_backward", "spmm_plan_features",
     "spmm_plan_reorder", "spmm_plan_permute", "spmm_set_mem_limit", "spmm_mem_stats",
     "spmm_coo_to_csr_noalloc",
+    "spmm_route_workspace", "spmm_route_build", "spmm_route_dispatch", "spmm_route_combine",
+    "spmm_route_combine_backward", "spmm_segment_product", "spmm_segment_product_dx", "spmm_segment_workspace",
+    "spmm_segment_product_dw", "spmm_layer_norm", "spmm_layer_norm_workspace", "spmm_layer_norm_backward",
 )
+
+SPMM_F32, SPMM_BF16, SPMM_F16 = 0, 1, 2
+
+# Row operators, from rows.py on first use (it defines autograd functions and
+# so needs torch, which this module imports only when a call does).
+_ROW_OPERATORS = (
+    "RowRoute", "dispatch", "combine", "segment_matmul", "layer_norm",
+    "spmm_route_build", "spmm_route_dispatch", "spmm_route_combine", "spmm_route_combine_backward",
+    "spmm_segment_product", "spmm_segment_product_dx", "spmm_segment_product_dw",
+    "spmm_layer_norm", "spmm_layer_norm_backward",
+)
+
+
+def __getattr__(name: str):
+    if name not in _ROW_OPERATORS:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    from . import rows
+    for n in _ROW_OPERATORS:
+        globals()[n] = getattr(rows, n)
+    return globals()[name]
 
 
 class SpmmError(RuntimeError):
@@ -141,6 +164,25 @@ def _load() -> ctypes.CDLL:
     lib.spmm_max_backward.restype = i32
     lib.spmm_coo_to_csr_noalloc.argtypes = [p, p, p, i64, i64, i64, p, p, p]
     lib.spmm_coo_to_csr_noalloc.restype = i32
+    pi64, f64 = ctypes.POINTER(ctypes.c_int64), ctypes.c_double
+    exchange = [p, p, i64, i64, i64, p, p, i32]
+    product = [p, p, p, p, i64, i64, i64, i64, i32]
+    for name, args in {
+        "spmm_route_workspace": [i64, i64, pi64],
+        "spmm_route_build": [p, i64, i64, p, p, p, p, i64, p],
+        "spmm_route_dispatch": exchange + [p, i64, i32, p],
+        "spmm_route_combine": exchange + [p, i64, i32, p],
+        "spmm_route_combine_backward": exchange + [p, p, p, i64, i32, p],
+        "spmm_segment_product": product + [p],
+        "spmm_segment_product_dx": product + [p],
+        "spmm_segment_workspace": [i64, i64, i64, i64, i32, pi64],
+        "spmm_segment_product_dw": product + [p, i64, p],
+        "spmm_layer_norm": [p, p, p, i32, p, p, p, i64, i64, f64, i32, p],
+        "spmm_layer_norm_workspace": [i64, i64, i32, pi64],
+        "spmm_layer_norm_backward": [p, p, p, i32, p, p, p, p, p, i64, i64, i32, p, i64, p],
+    }.items():
+        fn = getattr(lib, name)
+        fn.argtypes, fn.restype = args, i32
     lib.spmm_set_mem_limit.argtypes = [i64]
     lib.spmm_set_mem_limit.restype = i32
     lib.spmm_mem_stats.argtypes = [ctypes.POINTER(_MemStats)]

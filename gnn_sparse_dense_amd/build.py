@@ -34,6 +34,9 @@ SOURCES = [
     "reorder.hip",
     "merge_kernel.hip",
     "split_fused.hip",
+    "exchange.hip",
+    "layer_norm.hip",
+    "segment.hip",
 ]
 
 COMMON = [

@@ -7,11 +7,13 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <new>
 #include <vector>
 
 #include "alloc.h"
 #include "plan.h"
+#include "rows.h"
 
 #define SPMM_API extern "C" __attribute__((visibility("default")))
 
@@ -1648,4 +1650,381 @@ SPMM_API int spmm_max_backward(spmm_plan_t pt, const int64_t *argmax, const floa
     const hipError_t e = launch_maxgrad(a, reinterpret_cast<hipStream_t>(stream));
     if (e != hipSuccess) return fail_hip(e, "max backward launch");
     return succeed();
+}
+
+// ---- row operators (rows.h) ----
+
+namespace {
+
+// One array of a call: its first byte, size and element size; optional arrays
+// that are absent are left out of the list by passing bytes = 0.
+struct Array {
+    const char *name;
+    const void *p;
+    int64_t bytes;
+    size_t align;
+    bool out;
+};
+
+int64_t type_size(int type) { return type == SPMM_F32 ? 4 : 2; }
+
+bool is_type(int type) { return type == SPMM_F32 || type == SPMM_BF16 || type == SPMM_F16; }
+
+int check_types(int type, bool weighted, int weight_type) {
+    if (!is_type(type)) return fail(SPMM_E_INVALID_ARG, "unknown type %d", type);
+    if (weighted && weight_type != SPMM_F32 && weight_type != type)
+        return fail(SPMM_E_INVALID_ARG, "weights must be fp32 or of the rows' type (got %d)", weight_type);
+    return SPMM_OK;
+}
+
+// Every array is device memory of one device, aligned to its elements, and no
+// output overlaps another array.
+int check_arrays(std::initializer_list<Array> arrays, int *device) {
+    *device = -1;
+    for (const Array &a : arrays) {
+        if (a.bytes <= 0) continue;
+        hipPointerAttribute_t attr;
+        std::memset(&attr, 0, sizeof(attr));
+        bool ok = a.p != nullptr;
+        if (ok && hipPointerGetAttributes(&attr, a.p) != hipSuccess) {
+            (void)hipGetLastError();
+            ok = false;
+        }
+        if (!ok || (attr.type != hipMemoryTypeDevice && attr.type != hipMemoryTypeManaged))
+            return fail(SPMM_E_INVALID_ARG, "%s is NULL or not device memory", a.name);
+        if ((uintptr_t)a.p % a.align) return fail(SPMM_E_INVALID_ARG, "%s is not aligned to its elements", a.name);
+        if (*device < 0) *device = attr.device;
+        else if (*device != attr.device)
+            return fail(SPMM_E_INVALID_ARG, "%s is on device %d, another array on %d", a.name, attr.device, *device);
+    }
+    for (const Array &a : arrays)
+        if (a.out && a.bytes > 0)
+            for (const Array &b : arrays)
+                if (&a != &b && b.bytes > 0 && (uintptr_t)a.p < (uintptr_t)b.p + (uintptr_t)b.bytes &&
+                    (uintptr_t)b.p < (uintptr_t)a.p + (uintptr_t)a.bytes)
+                    return fail(SPMM_E_INVALID_ARG, "%s overlaps %s", a.name, b.name);
+    return SPMM_OK;
+}
+
+int check_route_sizes(int64_t pairs, int64_t E) {
+    if (pairs < 0) return fail(SPMM_E_INVALID_ARG, "negative size");
+    if (E < 1) return fail(SPMM_E_INVALID_ARG, "the number of experts must be positive (got %lld)", (long long)E);
+    if (pairs >= INT_MAX) return fail(SPMM_E_UNSUPPORTED, "pairs must be below 2^31 - 1");
+    if (E > kRouteMaxExperts)
+        return fail(SPMM_E_UNSUPPORTED, "at most %d experts (got %lld)", kRouteMaxExperts, (long long)E);
+    return SPMM_OK;
+}
+
+int check_exchange(int64_t T, int64_t k, int64_t E, int64_t N, int type, bool weighted, int weight_type) {
+    if (T < 0) return fail(SPMM_E_INVALID_ARG, "negative size");
+    if (k < 1) return fail(SPMM_E_INVALID_ARG, "k must be positive (got %lld)", (long long)k);
+    if (N < 1) return fail(SPMM_E_INVALID_ARG, "N must be positive (got %lld)", (long long)N);
+    if (T >= INT_MAX || k >= INT_MAX || N >= INT_MAX)
+        return fail(SPMM_E_UNSUPPORTED, "T, k and N must be below 2^31 - 1");
+    if (T * k >= (int64_t(1) << 59) / N) return fail(SPMM_E_UNSUPPORTED, "rows has too many elements");
+    if (const int st = check_route_sizes(T * k, E)) return st;
+    return check_types(type, weighted, weight_type);
+}
+
+int check_segment(int64_t R, int64_t E, int64_t I, int64_t O, int type) {
+    if (R < 0) return fail(SPMM_E_INVALID_ARG, "negative size");
+    if (E < 1 || I < 1 || O < 1) return fail(SPMM_E_INVALID_ARG, "E, I and O must be positive");
+    if (R >= INT_MAX || E >= (1 << 24) || I >= (1 << 24) || O >= (1 << 24))
+        return fail(SPMM_E_UNSUPPORTED, "R must be below 2^31 - 1, and E, I and O below 2^24");
+    if (E * I >= (int64_t(1) << 55) / O)
+        return fail(SPMM_E_UNSUPPORTED, "w has too many elements");
+    return check_types(type, false, 0);
+}
+
+int check_norm(int64_t R, int64_t N, int type, bool weighted, int weight_type) {
+    if (R < 0) return fail(SPMM_E_INVALID_ARG, "negative size");
+    if (N < 1) return fail(SPMM_E_INVALID_ARG, "N must be positive (got %lld)", (long long)N);
+    if (R >= INT_MAX || N >= INT_MAX) return fail(SPMM_E_UNSUPPORTED, "R and N must be below 2^31 - 1");
+    if (R >= (int64_t(1) << 59) / N) return fail(SPMM_E_UNSUPPORTED, "x has too many elements");
+    return check_types(type, weighted, weight_type);
+}
+
+int check_workspace(int64_t needed, int64_t given) {
+    if (given < needed)
+        return fail(SPMM_E_INVALID_ARG, "workspace of %lld bytes, %lld are needed", (long long)given,
+                    (long long)needed);
+    return SPMM_OK;
+}
+
+int launched(hipError_t e, const char *what) { return e == hipSuccess ? succeed() : fail_hip(e, what); }
+
+}  // namespace
+
+SPMM_API int spmm_route_workspace(int64_t pairs, int64_t E, int64_t *bytes) {
+    if (!bytes) return fail(SPMM_E_INVALID_ARG, "output is NULL");
+    if (const int st = check_route_sizes(pairs, E)) return st;
+    *bytes = route_workspace_ints(pairs, E) * (int64_t)sizeof(int);
+    return succeed();
+}
+
+SPMM_API int spmm_route_build(const int64_t *expert, int64_t pairs, int64_t E, int64_t *offsets, int32_t *order,
+                              int32_t *position, void *workspace, int64_t workspace_bytes, void *stream) {
+    if (const int st = check_route_sizes(pairs, E)) return st;
+    const int64_t need = route_workspace_ints(pairs, E) * (int64_t)sizeof(int);
+    if (const int st = check_workspace(need, workspace_bytes)) return st;
+    int device;
+    if (const int st = check_arrays({{"expert", expert, pairs * 8, 8, false},
+                                     {"offsets", offsets, (E + 1) * 8, 8, true},
+                                     {"order", order, pairs * 4, 4, true},
+                                     {"position", position, pairs * 4, 4, true},
+                                     {"workspace", workspace, need, 4, true}},
+                                    &device))
+        return st;
+    DeviceGuard dg(device);
+    RouteArgs a;
+    a.expert = expert;
+    a.pairs = pairs;
+    a.E = (int)E;
+    a.offsets = offsets;
+    a.order = order;
+    a.position = position;
+    a.workspace = static_cast<int *>(workspace);
+    return launched(launch_route(a, reinterpret_cast<hipStream_t>(stream)), "route launch");
+}
+
+SPMM_API int spmm_route_dispatch(const int64_t *offsets, const int32_t *position, int64_t T, int64_t k, int64_t E,
+                                 const void *x, const void *weight, int weight_type, void *xs, int64_t N, int type,
+                                 void *stream) {
+    if (const int st = check_exchange(T, k, E, N, type, weight != nullptr, weight_type)) return st;
+    if (T == 0) return succeed();
+    const int64_t size = type_size(type);
+    int device;
+    if (const int st = check_arrays(
+            {{"offsets", offsets, (E + 1) * 8, 8, false},
+             {"position", position, T * k * 4, 4, false},
+             {"x", x, T * N * size, (size_t)size, false},
+             {"weight", weight, weight ? T * k * type_size(weight_type) : 0, (size_t)type_size(weight_type), false},
+             {"xs", xs, T * k * N * size, (size_t)size, true}},
+            &device))
+        return st;
+    DeviceGuard dg(device);
+    ExchangeArgs a = {};
+    a.offsets = offsets;
+    a.position = position;
+    a.T = T;
+    a.k = k;
+    a.E = E;
+    a.N = N;
+    a.rows = x;
+    a.weight = weight;
+    a.weight_fp32 = weight_type == SPMM_F32;
+    a.out = xs;
+    return launched(launch_dispatch(a, type, reinterpret_cast<hipStream_t>(stream)), "dispatch launch");
+}
+
+SPMM_API int spmm_route_combine(const int64_t *offsets, const int32_t *position, int64_t T, int64_t k, int64_t E,
+                                const void *rows, const void *weight, int weight_type, void *out, int64_t N,
+                                int type, void *stream) {
+    if (const int st = check_exchange(T, k, E, N, type, weight != nullptr, weight_type)) return st;
+    if (T == 0) return succeed();
+    const int64_t size = type_size(type);
+    int device;
+    if (const int st = check_arrays(
+            {{"offsets", offsets, (E + 1) * 8, 8, false},
+             {"position", position, T * k * 4, 4, false},
+             {"rows", rows, T * k * N * size, (size_t)size, false},
+             {"weight", weight, weight ? T * k * type_size(weight_type) : 0, (size_t)type_size(weight_type), false},
+             {"out", out, T * N * size, (size_t)size, true}},
+            &device))
+        return st;
+    DeviceGuard dg(device);
+    ExchangeArgs a = {};
+    a.offsets = offsets;
+    a.position = position;
+    a.T = T;
+    a.k = k;
+    a.E = E;
+    a.N = N;
+    a.rows = rows;
+    a.weight = weight;
+    a.weight_fp32 = weight_type == SPMM_F32;
+    a.out = out;
+    return launched(launch_combine(a, type, reinterpret_cast<hipStream_t>(stream)), "combine launch");
+}
+
+SPMM_API int spmm_route_combine_backward(const int64_t *offsets, const int32_t *position, int64_t T, int64_t k,
+                                         int64_t E, const void *rows, const void *weight, int weight_type,
+                                         const void *dout, void *drows, void *dweight, int64_t N, int type,
+                                         void *stream) {
+    if (const int st = check_exchange(T, k, E, N, type, weight || dweight, weight_type)) return st;
+    if (T == 0) return succeed();
+    if (!drows && !dweight) return fail(SPMM_E_INVALID_ARG, "drows and dweight are both NULL");
+    const int64_t size = type_size(type), wsize = type_size(weight_type);
+    int device;
+    if (const int st = check_arrays({{"offsets", offsets, (E + 1) * 8, 8, false},
+                                     {"position", position, T * k * 4, 4, false},
+                                     {"rows", rows, dweight ? T * k * N * size : 0, (size_t)size, false},
+                                     {"weight", weight, weight ? T * k * wsize : 0, (size_t)wsize, false},
+                                     {"dout", dout, T * N * size, (size_t)size, false},
+                                     {"drows", drows, drows ? T * k * N * size : 0, (size_t)size, true},
+                                     {"dweight", dweight, dweight ? T * k * wsize : 0, (size_t)wsize, true}},
+                                    &device))
+        return st;
+    DeviceGuard dg(device);
+    ExchangeArgs a = {};
+    a.offsets = offsets;
+    a.position = position;
+    a.T = T;
+    a.k = k;
+    a.E = E;
+    a.N = N;
+    a.rows = rows;
+    a.weight = weight;
+    a.weight_fp32 = weight_type == SPMM_F32;
+    a.dout = dout;
+    a.drows = drows;
+    a.dweight = dweight;
+    return launched(launch_combine_backward(a, type, reinterpret_cast<hipStream_t>(stream)),
+                    "combine backward launch");
+}
+
+// The three segment products: `in` is x or dy, `out` y, dx or dw.
+static int segment_product(const void *x, const void *w, const void *dy, const int64_t *offsets, void *out,
+                           int64_t R, int64_t E, int64_t I, int64_t O, int type, void *workspace,
+                           int64_t workspace_bytes, void *stream) {
+    if (const int st = check_segment(R, E, I, O, type)) return st;
+    const bool dw = w == nullptr, transposed = x == nullptr;
+    const int64_t size = type_size(type);
+    const int64_t need = dw ? segment_workspace_floats(R, E, I, O, type) * (int64_t)sizeof(float) : 0;
+    if (const int st = check_workspace(need, workspace_bytes)) return st;
+    if (R == 0 && !dw) return succeed();
+    const int64_t out_bytes = (dw ? E * I * O : transposed ? R * I : R * O) * size;
+    int device;
+    if (const int st = check_arrays({{"offsets", offsets, (E + 1) * 8, 8, false},
+                                     {"x", x, transposed ? 0 : R * I * size, (size_t)size, false},
+                                     {"w", w, dw ? 0 : E * I * O * size, (size_t)size, false},
+                                     {"dy", dy, dw || transposed ? R * O * size : 0, (size_t)size, false},
+                                     {dw ? "dw" : transposed ? "dx" : "y", out, out_bytes, (size_t)size, true},
+                                     {"workspace", workspace, need, 4, true}},
+                                    &device))
+        return st;
+    DeviceGuard dg(device);
+    SegmentArgs a = {};
+    a.offsets = offsets;
+    a.R = R;
+    a.E = E;
+    a.I = I;
+    a.O = O;
+    a.x = x;
+    a.w = w;
+    a.dy = dy;
+    a.y = out;
+    a.partial = static_cast<float *>(workspace);
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    return launched(dw ? launch_segment_dw(a, type, s) : launch_segment(a, transposed, type, s),
+                    "segment product launch");
+}
+
+SPMM_API int spmm_segment_product(const void *x, const void *w, const int64_t *offsets, void *y, int64_t R, int64_t E,
+                                  int64_t I, int64_t O, int type, void *stream) {
+    if (R > 0 && (!x || !w)) return fail(SPMM_E_INVALID_ARG, "x / w are NULL");
+    static const char none = 0;
+    return segment_product(x ? x : &none, w ? w : &none, nullptr, offsets, y, R, E, I, O, type, nullptr, 0, stream);
+}
+
+SPMM_API int spmm_segment_product_dx(const void *dy, const void *w, const int64_t *offsets, void *dx, int64_t R,
+                                     int64_t E, int64_t I, int64_t O, int type, void *stream) {
+    if (R > 0 && (!dy || !w)) return fail(SPMM_E_INVALID_ARG, "dy / w are NULL");
+    static const char none = 0;
+    return segment_product(nullptr, w ? w : &none, dy, offsets, dx, R, E, I, O, type, nullptr, 0, stream);
+}
+
+SPMM_API int spmm_segment_workspace(int64_t R, int64_t E, int64_t I, int64_t O, int type, int64_t *bytes) {
+    if (!bytes) return fail(SPMM_E_INVALID_ARG, "output is NULL");
+    if (const int st = check_segment(R, E, I, O, type)) return st;
+    *bytes = segment_workspace_floats(R, E, I, O, type) * (int64_t)sizeof(float);
+    return succeed();
+}
+
+SPMM_API int spmm_segment_product_dw(const void *x, const void *dy, const int64_t *offsets, void *dw, int64_t R,
+                                     int64_t E, int64_t I, int64_t O, int type, void *workspace,
+                                     int64_t workspace_bytes, void *stream) {
+    if (R > 0 && (!x || !dy)) return fail(SPMM_E_INVALID_ARG, "x / dy are NULL");
+    static const char none = 0;
+    return segment_product(x ? x : &none, nullptr, dy, offsets, dw, R, E, I, O, type, workspace, workspace_bytes,
+                           stream);
+}
+
+SPMM_API int spmm_layer_norm(const void *x, const void *weight, const void *bias, int weight_type, void *y,
+                             float *mean, float *rstd, int64_t R, int64_t N, double eps, int type, void *stream) {
+    if (const int st = check_norm(R, N, type, weight || bias, weight_type)) return st;
+    if (!(eps >= 0.0)) return fail(SPMM_E_INVALID_ARG, "eps must be >= 0");
+    if (!mean != !rstd) return fail(SPMM_E_INVALID_ARG, "mean and rstd are written together");
+    if (R == 0) return succeed();
+    const int64_t size = type_size(type), wsize = type_size(weight_type);
+    int device;
+    if (const int st = check_arrays({{"x", x, R * N * size, (size_t)size, false},
+                                     {"weight", weight, weight ? N * wsize : 0, (size_t)wsize, false},
+                                     {"bias", bias, bias ? N * wsize : 0, (size_t)wsize, false},
+                                     {"y", y, R * N * size, (size_t)size, true},
+                                     {"mean", mean, mean ? R * 4 : 0, 4, true},
+                                     {"rstd", rstd, rstd ? R * 4 : 0, 4, true}},
+                                    &device))
+        return st;
+    DeviceGuard dg(device);
+    NormArgs a = {};
+    a.x = x;
+    a.weight = weight;
+    a.bias = bias;
+    a.weight_fp32 = weight_type == SPMM_F32;
+    a.eps = (float)eps;
+    a.R = R;
+    a.N = N;
+    a.y = y;
+    a.mean = mean;
+    a.rstd = rstd;
+    return launched(launch_norm(a, type, reinterpret_cast<hipStream_t>(stream)), "layer norm launch");
+}
+
+SPMM_API int spmm_layer_norm_workspace(int64_t R, int64_t N, int type, int64_t *bytes) {
+    if (!bytes) return fail(SPMM_E_INVALID_ARG, "output is NULL");
+    if (const int st = check_norm(R, N, type, false, 0)) return st;
+    *bytes = norm_workspace_floats(R, N, type) * (int64_t)sizeof(float);
+    return succeed();
+}
+
+SPMM_API int spmm_layer_norm_backward(const void *dy, const void *x, const void *weight, int weight_type,
+                                      const float *mean, const float *rstd, void *dx, void *dweight, void *dbias,
+                                      int64_t R, int64_t N, int type, void *workspace, int64_t workspace_bytes,
+                                      void *stream) {
+    const bool sums = dweight || dbias;
+    if (const int st = check_norm(R, N, type, weight || sums, weight_type)) return st;
+    if (R == 0 && !sums) return succeed();
+    if (!dx && !sums) return fail(SPMM_E_INVALID_ARG, "dx, dweight and dbias are all NULL");
+    const int64_t need = sums ? norm_workspace_floats(R, N, type) * (int64_t)sizeof(float) : 0;
+    if (const int st = check_workspace(need, workspace_bytes)) return st;
+    const int64_t size = type_size(type), wsize = type_size(weight_type);
+    int device;
+    if (const int st = check_arrays({{"dy", dy, R * N * size, (size_t)size, false},
+                                     {"x", x, R * N * size, (size_t)size, false},
+                                     {"weight", weight, weight ? N * wsize : 0, (size_t)wsize, false},
+                                     {"mean", mean, R * 4, 4, false},
+                                     {"rstd", rstd, R * 4, 4, false},
+                                     {"dx", dx, dx ? R * N * size : 0, (size_t)size, true},
+                                     {"dweight", dweight, dweight ? N * wsize : 0, (size_t)wsize, true},
+                                     {"dbias", dbias, dbias ? N * wsize : 0, (size_t)wsize, true},
+                                     {"workspace", workspace, need, 4, true}},
+                                    &device))
+        return st;
+    DeviceGuard dg(device);
+    NormArgs a = {};
+    a.x = x;
+    a.weight = weight;
+    a.weight_fp32 = weight_type == SPMM_F32;
+    a.R = R;
+    a.N = N;
+    a.mean = const_cast<float *>(mean);
+    a.rstd = const_cast<float *>(rstd);
+    a.dy = dy;
+    a.dx = dx;
+    a.dweight = dweight;
+    a.dbias = dbias;
+    a.partial = static_cast<float *>(workspace);
+    return launched(launch_norm_backward(a, type, reinterpret_cast<hipStream_t>(stream)),
+                    "layer norm backward launch");
 }

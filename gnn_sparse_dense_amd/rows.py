@@ -1,0 +1,425 @@
+"""Row operators: what a layer around the aggregation does with its rows when
+each row belongs to one or more experts (or node types), and the layer norm.
+
+    route = RowRoute(expert, E)              # expert [T, k] int64: each row's experts
+    xs = dispatch(route, x)                  # [T * k, N]: rows in expert order
+    h = segment_matmul(xs, w, route.offsets) # w [E, N, O]: each expert's product
+    out = combine(route, h, weight)          # [T, O]: summed back, weighted
+    y = layer_norm(out, gamma, beta)
+
+Rows are fp32, bf16 or fp16 matrices; sums are fp32 and outputs are rounded
+once.  All five run on torch's current stream of the tensors' device,
+allocate through torch and never wait for the GPU, so they can be captured
+into a graph.  dispatch, combine, segment_matmul and layer_norm are
+differentiable (once); the spmm_* functions are the C calls on caller's
+tensors.
+"""
+from __future__ import annotations
+
+import ctypes
+import functools
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import SPMM_BF16, SPMM_F16, SPMM_F32, _check, _current_stream, _lib
+
+_TYPES = {torch.float32: SPMM_F32, torch.bfloat16: SPMM_BF16, torch.float16: SPMM_F16}
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _check_tensor(name, t, dtypes, shape, device):
+    """t is what the library will read or write: it sees only the address."""
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d).replace('torch.', '') for d in dtypes)}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous (row-major)")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _check_rows_type(name, t, dim=2):
+    if t.dim() != dim:
+        raise ValueError(f"{name} has {t.dim()} dimensions, expected {dim}")
+    if t.dtype not in _TYPES:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
+    return _TYPES[t.dtype]
+
+
+def _stream(t, stream):
+    if stream is None:
+        return _current_stream(t)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+@functools.lru_cache(maxsize=256)
+def _workspace_bytes(call: str, *sizes: int) -> int:
+    n = ctypes.c_int64()
+    _check(getattr(_lib, call)(*sizes, ctypes.byref(n)))
+    return n.value
+
+
+def _workspace(device, call: str, *sizes: int):
+    """(tensor or None, address, bytes) of one call's scratch memory."""
+    n = _workspace_bytes(call, *sizes)
+    if n == 0:
+        return None, None, 0
+    t = torch.empty(n, dtype=torch.uint8, device=device)
+    return t, t.data_ptr(), n
+
+
+# ---------------------------------------------------------------- the C calls
+
+def spmm_route_build(expert, E: int, offsets, order, position, stream=None) -> None:
+    """Sort the pairs of expert (int64, any shape) by expert into offsets
+    int64 [E + 1], order and position int32 (expert's number of elements)."""
+    pairs, E = expert.numel(), int(E)
+    _check_tensor("expert", expert, (torch.int64,), expert.shape, offsets.device)
+    _check_tensor("offsets", offsets, (torch.int64,), (E + 1,), offsets.device)
+    _check_tensor("order", order, (torch.int32,), (pairs,), offsets.device)
+    _check_tensor("position", position, (torch.int32,), expert.shape, offsets.device)
+    _build(expert, pairs, E, offsets, order, position, _stream(offsets, stream))
+
+
+def _build(expert, pairs, E, offsets, order, position, stream):
+    ws, at, n = _workspace(offsets.device, "spmm_route_workspace", pairs, E)
+    _check(_lib.spmm_route_build(expert.data_ptr(), pairs, E, offsets.data_ptr(), order.data_ptr(),
+                                 position.data_ptr(), at, n, stream))
+
+
+def _check_exchange(route, name, rows, count, weight):
+    kind = _check_rows_type(name, rows)
+    _check_tensor(name, rows, (rows.dtype,), (count, rows.shape[1]), route.device)
+    if weight is None:
+        return kind, kind
+    _check_tensor("weight", weight, (torch.float32, rows.dtype), (route.T, route.k), route.device)
+    return kind, _TYPES[weight.dtype]
+
+
+def spmm_route_dispatch(route: "RowRoute", x, xs, weight=None, stream=None) -> None:
+    """xs [T * k, N] = rows of x [T, N] in expert order (times weight [T, k])."""
+    kind, wkind = _check_exchange(route, "x", x, route.T, weight)
+    _check_tensor("xs", xs, (x.dtype,), (route.T * route.k, x.shape[1]), route.device)
+    _check(_lib.spmm_route_dispatch(_ptr(route.offsets), _ptr(route.position), route.T, route.k, route.E, _ptr(x),
+                                    _ptr(weight), wkind, _ptr(xs), x.shape[1], kind, _stream(x, stream)))
+
+
+def spmm_route_combine(route: "RowRoute", rows, weight, out, stream=None) -> None:
+    """out [T, N] = the rows [T * k, N] summed back (weight [T, k] or None: 1)."""
+    kind, wkind = _check_exchange(route, "rows", rows, route.T * route.k, weight)
+    _check_tensor("out", out, (rows.dtype,), (route.T, rows.shape[1]), route.device)
+    _check(_lib.spmm_route_combine(_ptr(route.offsets), _ptr(route.position), route.T, route.k, route.E, _ptr(rows),
+                                   _ptr(weight), wkind, _ptr(out), rows.shape[1], kind, _stream(rows, stream)))
+
+
+def spmm_route_combine_backward(route: "RowRoute", rows, weight, dout, drows, dweight, stream=None) -> None:
+    """Gradients of combine: drows [T * k, N] and dweight [T, k], either may
+    be None (rows too, without dweight)."""
+    kind, wkind = _check_exchange(route, "dout", dout, route.T, weight)
+    pairs = (route.T * route.k, dout.shape[1])
+    if drows is not None:
+        _check_tensor("drows", drows, (dout.dtype,), pairs, route.device)
+    if dweight is not None:
+        if rows is None:
+            raise ValueError("rows are needed for dweight")
+        _check_tensor("rows", rows, (dout.dtype,), pairs, route.device)
+        types = (torch.float32, dout.dtype) if weight is None else (weight.dtype,)
+        _check_tensor("dweight", dweight, types, (route.T, route.k), route.device)
+        wkind = _TYPES[dweight.dtype]
+    _check(_lib.spmm_route_combine_backward(_ptr(route.offsets), _ptr(route.position), route.T, route.k, route.E,
+                                            _ptr(rows), _ptr(weight), wkind, _ptr(dout), _ptr(drows), _ptr(dweight),
+                                            dout.shape[1], kind, _stream(dout, stream)))
+
+
+def _check_segment(rows_name, rows, width, dtype, offsets, R, E, device):
+    _check_tensor(rows_name, rows, (dtype,), (R, width), device)
+    _check_tensor("offsets", offsets, (torch.int64,), (E + 1,), device)
+
+
+def spmm_segment_product(x, w, offsets, y, stream=None) -> None:
+    """y [R, O] = x [R, I] times w[e] [I, O] for the rows of each segment e."""
+    kind = _check_rows_type("x", x)
+    _check_rows_type("w", w, 3)
+    E, I, O = w.shape
+    _check_tensor("w", w, (x.dtype,), w.shape, x.device)
+    _check_segment("x", x, I, x.dtype, offsets, x.shape[0], E, x.device)
+    _check_tensor("y", y, (x.dtype,), (x.shape[0], O), x.device)
+    _check(_lib.spmm_segment_product(_ptr(x), _ptr(w), _ptr(offsets), _ptr(y), x.shape[0], E, I, O, kind,
+                                     _stream(x, stream)))
+
+
+def spmm_segment_product_dx(dy, w, offsets, dx, stream=None) -> None:
+    """dx [R, I] = dy [R, O] times the transpose of w[e] for each segment e."""
+    kind = _check_rows_type("dy", dy)
+    _check_rows_type("w", w, 3)
+    E, I, O = w.shape
+    _check_tensor("w", w, (dy.dtype,), w.shape, dy.device)
+    _check_segment("dy", dy, O, dy.dtype, offsets, dy.shape[0], E, dy.device)
+    _check_tensor("dx", dx, (dy.dtype,), (dy.shape[0], I), dy.device)
+    _check(_lib.spmm_segment_product_dx(_ptr(dy), _ptr(w), _ptr(offsets), _ptr(dx), dy.shape[0], E, I, O, kind,
+                                        _stream(dy, stream)))
+
+
+def spmm_segment_product_dw(x, dy, offsets, dw, stream=None) -> None:
+    """dw [E, I, O]: dw[e] = sum over the rows of segment e of x[r]^T dy[r]."""
+    kind = _check_rows_type("x", x)
+    _check_rows_type("dw", dw, 3)
+    E, I, O = dw.shape
+    _check_tensor("dw", dw, (x.dtype,), dw.shape, x.device)
+    _check_segment("x", x, I, x.dtype, offsets, x.shape[0], E, x.device)
+    _check_tensor("dy", dy, (x.dtype,), (x.shape[0], O), x.device)
+    ws, at, n = _workspace(x.device, "spmm_segment_workspace", x.shape[0], E, I, O, kind)
+    _check(_lib.spmm_segment_product_dw(_ptr(x), _ptr(dy), _ptr(offsets), _ptr(dw), x.shape[0], E, I, O, kind, at, n,
+                                        _stream(x, stream)))
+
+
+def _check_norm(x, weight, bias):
+    kind = _check_rows_type("x", x)
+    wkind = kind
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is not None:
+            _check_tensor(name, t, (torch.float32, x.dtype), (x.shape[1],), x.device)
+            wkind = _TYPES[t.dtype]
+    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+        raise TypeError(f"weight ({weight.dtype}) and bias ({bias.dtype}) must have one type")
+    _check_tensor("x", x, (x.dtype,), x.shape, x.device)
+    return kind, wkind
+
+
+def spmm_layer_norm(x, weight, bias, y, mean=None, rstd=None, eps: float = 1e-5, stream=None) -> None:
+    """y = layer norm of each row of x [R, N]; mean and rstd (fp32 [R]) are
+    what the backward pass reads."""
+    kind, wkind = _check_norm(x, weight, bias)
+    R, N = x.shape
+    _check_tensor("y", y, (x.dtype,), x.shape, x.device)
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        if t is not None:
+            _check_tensor(name, t, (torch.float32,), (R,), x.device)
+    _check(_lib.spmm_layer_norm(_ptr(x), _ptr(weight), _ptr(bias), wkind, _ptr(y), _ptr(mean), _ptr(rstd), R, N,
+                                float(eps), kind, _stream(x, stream)))
+
+
+def spmm_layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, stream=None) -> None:
+    """Gradients of the layer norm; any of dx [R, N], dweight and dbias [N]
+    may be None."""
+    kind, wkind = _check_norm(x, weight, None)
+    R, N = x.shape
+    _check_tensor("dy", dy, (x.dtype,), x.shape, x.device)
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        _check_tensor(name, t, (torch.float32,), (R,), x.device)
+    if dx is not None:
+        _check_tensor("dx", dx, (x.dtype,), x.shape, x.device)
+    types = (torch.float32, x.dtype) if weight is None else (weight.dtype,)
+    for name, t in (("dweight", dweight), ("dbias", dbias)):
+        if t is not None:
+            _check_tensor(name, t, types, (N,), x.device)
+            wkind = _TYPES[t.dtype]
+            types = (t.dtype,)
+    ws, at, n = None, None, 0
+    if dweight is not None or dbias is not None:
+        ws, at, n = _workspace(x.device, "spmm_layer_norm_workspace", R, N, kind)
+    _check(_lib.spmm_layer_norm_backward(_ptr(dy), _ptr(x), _ptr(weight), wkind, _ptr(mean), _ptr(rstd), _ptr(dx),
+                                         _ptr(dweight), _ptr(dbias), R, N, kind, at, n, _stream(x, stream)))
+
+
+# ------------------------------------------------------- differentiable calls
+
+def _wants_grad(*tensors) -> bool:
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+
+
+class RowRoute:
+    """Rows sorted by expert, built once per routing and applied many times.
+
+    expert: int64 [T, k] (or [T]: one expert per row, such as a node's type)
+    on the GPU; an id outside [0, num_experts) means no expert.  The pairs
+    (row, choice) are sorted by expert, stably, those without an expert last:
+
+    offsets : int64 [E + 1], places of each expert's pairs
+    order   : int32 [T * k], the pair t * k + j at each place
+    position: int32 [T, k], the place of each pair
+    """
+
+    def __init__(self, expert, num_experts: int):
+        if expert.dtype != torch.int64:
+            raise TypeError(f"expert must be int64, got {expert.dtype}")
+        if expert.dim() not in (1, 2):
+            raise ValueError(f"expert has {expert.dim()} dimensions, expected 1 or 2")
+        if not expert.is_cuda:
+            raise ValueError("expert must be a GPU tensor")
+        self.T = int(expert.shape[0])
+        self.k = int(expert.shape[1]) if expert.dim() == 2 else 1
+        if self.k < 1:
+            raise ValueError("expert must have at least one choice per row")
+        self.E = int(num_experts)
+        self.device = expert.device
+        pairs = self.T * self.k
+        _workspace_bytes("spmm_route_workspace", pairs, self.E)      # refuses sizes before any allocation
+        self.offsets = torch.empty(self.E + 1, dtype=torch.int64, device=self.device)
+        self.order = torch.empty(pairs, dtype=torch.int32, device=self.device)
+        self.position = torch.empty((self.T, self.k), dtype=torch.int32, device=self.device)
+        _build(expert.contiguous(), pairs, self.E, self.offsets, self.order, self.position,
+               _current_stream(self.offsets))
+
+
+class _Dispatch(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, route):
+        ctx.route = route
+        xs = x.new_empty((route.T * route.k, x.shape[1]))
+        spmm_route_dispatch(route, x.contiguous(), xs)
+        return xs
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dxs):
+        route = ctx.route
+        dx = dxs.new_empty((route.T, dxs.shape[1]))
+        spmm_route_combine(route, dxs.contiguous(), None, dx)
+        return dx, None
+
+
+def dispatch(route: RowRoute, x):
+    """Rows of x [T, N] in expert order: [T * k, N], row route.position[t, j]
+    = x[t]; rows from route.offsets[E] on (pairs without an expert) are zero.
+    Differentiable in x."""
+    _check_rows_type("x", x)
+    if _wants_grad(x):
+        return _Dispatch.apply(x, route)
+    xs = x.new_empty((route.T * route.k, x.shape[1]))
+    spmm_route_dispatch(route, x.contiguous(), xs)
+    return xs
+
+
+class _Combine(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, rows, weight, route):
+        rows = rows.contiguous()
+        weight = None if weight is None else weight.contiguous()
+        ctx.route = route
+        # rows are read again only for the weights' gradient
+        ctx.save_for_backward(rows if ctx.needs_input_grad[1] else None, weight)
+        out = rows.new_empty((route.T, rows.shape[1]))
+        spmm_route_combine(route, rows, weight, out)
+        return out
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dout):
+        route = ctx.route
+        rows, weight = ctx.saved_tensors
+        dout = dout.contiguous()
+        drows = dweight = None
+        if ctx.needs_input_grad[0]:
+            drows = dout.new_empty((route.T * route.k, dout.shape[1]))
+        if ctx.needs_input_grad[1]:
+            dweight = torch.empty_like(weight)
+            spmm_route_combine_backward(route, rows, weight, dout, drows, dweight)
+        elif drows is not None:
+            spmm_route_dispatch(route, dout, drows, weight)
+        return drows, dweight, None
+
+
+def combine(route: RowRoute, rows, weight=None):
+    """out [T, N]: out[t] = sum over j of weight[t, j] * rows[position[t, j]],
+    with rows [T * k, N] in expert order and weight [T, k] in fp32 or the
+    rows' type (None: 1); pairs without an expert do not enter.
+    Differentiable in rows and weight."""
+    _check_rows_type("rows", rows)
+    if _wants_grad(rows, weight):
+        return _Combine.apply(rows, weight, route)
+    out = rows.new_empty((route.T, rows.shape[1]))
+    spmm_route_combine(route, rows.contiguous(), None if weight is None else weight.contiguous(), out)
+    return out
+
+
+class _SegmentMatmul(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, offsets):
+        x, w, offsets = x.contiguous(), w.contiguous(), offsets.contiguous()
+        need_x, need_w = ctx.needs_input_grad[:2]
+        ctx.save_for_backward(x if need_w else None, w if need_x else None, offsets)
+        ctx.shape = w.shape
+        y = x.new_empty((x.shape[0], w.shape[2]))
+        spmm_segment_product(x, w, offsets, y)
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        x, w, offsets = ctx.saved_tensors
+        dy = dy.contiguous()
+        dx = dw = None
+        if ctx.needs_input_grad[0]:
+            dx = dy.new_empty((dy.shape[0], ctx.shape[1]))
+            spmm_segment_product_dx(dy, w, offsets, dx)
+        if ctx.needs_input_grad[1]:
+            dw = dy.new_empty(ctx.shape)
+            spmm_segment_product_dw(x, dy, offsets, dw)
+        return dx, dw, None
+
+
+def segment_matmul(x, w, offsets):
+    """y [R, O]: y[r] = x[r] . w[e] for the rows offsets[e] <= r <
+    offsets[e + 1] of x [R, I], with w [E, I, O] of x's type and offsets int64
+    [E + 1] on the GPU (a RowRoute's, or the bounds of rows sorted by type);
+    rows outside the segments are zero.  Differentiable in x and w."""
+    _check_rows_type("x", x)
+    _check_rows_type("w", w, 3)
+    if _wants_grad(x, w):
+        return _SegmentMatmul.apply(x, w, offsets)
+    y = x.new_empty((x.shape[0], w.shape[2]))
+    spmm_segment_product(x.contiguous(), w.contiguous(), offsets.contiguous(), y)
+    return y
+
+
+class _LayerNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, eps):
+        x = x.contiguous()
+        weight = None if weight is None else weight.contiguous()
+        bias = None if bias is None else bias.contiguous()
+        y = torch.empty_like(x)
+        mean = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
+        rstd = torch.empty_like(mean)
+        spmm_layer_norm(x, weight, bias, y, mean, rstd, eps)
+        ctx.save_for_backward(x, weight, mean, rstd)
+        ctx.bias_dtype = None if bias is None else bias.dtype
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        x, weight, mean, rstd = ctx.saved_tensors
+        need_x, need_w, need_b = ctx.needs_input_grad[:3]
+        dx = torch.empty_like(x) if need_x else None
+        dweight = torch.empty_like(weight) if need_w else None
+        dbias = torch.empty(x.shape[1], dtype=ctx.bias_dtype, device=x.device) if need_b else None
+        spmm_layer_norm_backward(dy.contiguous(), x, weight, mean, rstd, dx, dweight, dbias)
+        return dx, dweight, dbias, None
+
+
+def layer_norm(x, weight=None, bias=None, eps: float = 1e-5):
+    """Layer norm over the last dimension of x [..., N]: (x - mean) /
+    sqrt(var + eps) * weight + bias with the biased variance; weight and bias
+    [N] in fp32 or x's type (None: 1 and 0).  Differentiable in all three."""
+    if x.dim() < 1:
+        raise ValueError("x must have at least one dimension")
+    shape = x.shape
+    if x.dim() != 2:
+        x = x.reshape(-1, shape[-1]) if shape[-1] else x.reshape(0, 0)
+    if _wants_grad(x, weight, bias):
+        y = _LayerNorm.apply(x, weight, bias, eps)
+    else:
+        x = x.contiguous()
+        y = torch.empty_like(x)
+        spmm_layer_norm(x, None if weight is None else weight.contiguous(),
+                        None if bias is None else bias.contiguous(), y, None, None, eps)
+    return y if y.shape == shape else y.reshape(shape)

@@ -456,6 +456,100 @@ int spmm_plan_reorder(spmm_plan_t plan, int method, int64_t *perm);
  */
 spmm_plan_t spmm_plan_permute(spmm_plan_t plan, const int64_t *perm);
 
+/*
+ * Row operators: what a layer around the aggregation does with its rows when
+ * each row belongs to one or more experts (or node types): sorting rows by
+ * expert and back, a product per expert, and the layer norm.
+ *
+ * Rows are packed row-major matrices of one element type (enum spmm_type);
+ * sums are fp32 and every output element is rounded once.  Weights are fp32
+ * or of the rows' type (`weight_type`).  All pointers are device memory of one
+ * device, aligned to their elements; outputs overlap nothing else.  The calls
+ * enqueue kernels only, on `stream`, allocate nothing and read no size back,
+ * so they can be captured into a HIP graph; a workspace (from the matching
+ * _workspace call, which touches no device) belongs to one call at a time.
+ * No atomics decide a result: runs are bitwise reproducible.
+ * Returns OK, INVALID_ARG (NULL / host / misaligned / overlapping pointer,
+ * bad size or type, workspace too small), UNSUPPORTED (size limits) or HIP.
+ */
+enum spmm_type { SPMM_F32 = 0, SPMM_BF16 = 1, SPMM_F16 = 2 };
+
+/*
+ * Route: `pairs` = T * k pairs (row t, choice j) in row-major order, pair
+ * p = t * k + j with the expert id expert[p].  Pairs are sorted by expert,
+ * pairs of one expert in pair order; an id outside [0, E) means no expert and
+ * sorts behind all others.
+ *   offsets  : int64 [E + 1], pairs of expert e take the places
+ *              [offsets[e], offsets[e + 1]); places from offsets[E] on belong
+ *              to no expert
+ *   order    : int32 [pairs], the pair at each place
+ *   position : int32 [pairs], the place of each pair (inverse of order)
+ * pairs < 2^31 - 1, 1 <= E <= 2048.
+ */
+int spmm_route_workspace(int64_t pairs, int64_t E, int64_t *bytes);
+int spmm_route_build(const int64_t *expert, int64_t pairs, int64_t E, int64_t *offsets, int32_t *order,
+                     int32_t *position, void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * Dispatch: xs [T * k, N], xs[position[t, j]] = x[t] (times weight[t, j] when
+ * weight != NULL); rows from offsets[E] on are zero.
+ * Combine: out [T, N], out[t] = sum over j, ascending, of weight[t, j] *
+ * rows[position[t, j]] (weight 1 when NULL), one fused multiply-add per term;
+ * pairs of no expert are skipped (their rows and weights are not read into
+ * the sum), a row without experts is zero.
+ * Each is the other's gradient: d x = combine(d xs, no weight), and with
+ * d out = gradient of out: drows[position[t, j]] = weight[t, j] * dout[t]
+ * (zero from offsets[E] on) and dweight[t, j] = <rows[position[t, j]],
+ * dout[t]> (zero for pairs of no expert), both from
+ * spmm_route_combine_backward; either output may be NULL, `rows` too when
+ * dweight is.  dweight has weight_type.
+ */
+int spmm_route_dispatch(const int64_t *offsets, const int32_t *position, int64_t T, int64_t k, int64_t E,
+                        const void *x, const void *weight, int weight_type, void *xs, int64_t N, int type,
+                        void *stream);
+int spmm_route_combine(const int64_t *offsets, const int32_t *position, int64_t T, int64_t k, int64_t E,
+                       const void *rows, const void *weight, int weight_type, void *out, int64_t N, int type,
+                       void *stream);
+int spmm_route_combine_backward(const int64_t *offsets, const int32_t *position, int64_t T, int64_t k, int64_t E,
+                                const void *rows, const void *weight, int weight_type, const void *dout, void *drows,
+                                void *dweight, int64_t N, int type, void *stream);
+
+/*
+ * Segment product: rows sorted by expert times that expert's matrix.  For
+ * rows r of segment e, offsets[e] <= r < offsets[e + 1] (int64 [E + 1] on the
+ * device, non-decreasing, inside [0, R]; bounds outside are clamped, and a
+ * decreasing list leaves rows unwritten but touches nothing outside):
+ *   spmm_segment_product      : y [R, O], y[r] = x[r] . w[e]
+ *   spmm_segment_product_dx   : dx [R, I], dx[r] = dy[r] . w[e]^T
+ *   spmm_segment_product_dw   : dw [E, I, O], dw[e] = sum of x[r]^T dy[r]
+ * with x [R, I], w [E, I, O], dy [R, O].  Rows outside the segments give zero
+ * rows of y and dx and do not enter dw; an empty segment gives dw[e] = 0.
+ * R < 2^31 - 1, 1 <= E, I, O < 2^24.
+ */
+int spmm_segment_product(const void *x, const void *w, const int64_t *offsets, void *y, int64_t R, int64_t E,
+                         int64_t I, int64_t O, int type, void *stream);
+int spmm_segment_product_dx(const void *dy, const void *w, const int64_t *offsets, void *dx, int64_t R, int64_t E,
+                            int64_t I, int64_t O, int type, void *stream);
+int spmm_segment_workspace(int64_t R, int64_t E, int64_t I, int64_t O, int type, int64_t *bytes);
+int spmm_segment_product_dw(const void *x, const void *dy, const int64_t *offsets, void *dw, int64_t R, int64_t E,
+                            int64_t I, int64_t O, int type, void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * Layer norm of each row of x [R, N]: u = (x - mean) / sqrt(var + eps) with
+ * the biased variance, y = u * weight + bias (1 and 0 when NULL; both of
+ * weight_type).  mean and rstd (fp32 [R], both or neither) are kept for
+ *   spmm_layer_norm_backward: dx = rstd * (g - mean(g) - u * mean(g * u)),
+ *   g = dy * weight; dweight = sum of dy * u, dbias = sum of dy over the rows
+ *   (weight_type); any of the three may be NULL.
+ * R < 2^31 - 1, 1 <= N < 2^31 - 1.
+ */
+int spmm_layer_norm(const void *x, const void *weight, const void *bias, int weight_type, void *y, float *mean,
+                    float *rstd, int64_t R, int64_t N, double eps, int type, void *stream);
+int spmm_layer_norm_workspace(int64_t R, int64_t N, int type, int64_t *bytes);
+int spmm_layer_norm_backward(const void *dy, const void *x, const void *weight, int weight_type, const float *mean,
+                             const float *rstd, void *dx, void *dweight, void *dbias, int64_t R, int64_t N, int type,
+                             void *workspace, int64_t workspace_bytes, void *stream);
+
 /* The calling thread's last status; copies its message (NUL-terminated,
  * truncated to cap bytes) into buf when buf != NULL and cap > 0. */
 int spmm_last_error(char *buf, int64_t cap);
