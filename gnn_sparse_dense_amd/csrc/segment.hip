@@ -10,11 +10,12 @@
 // the summed index contiguously (x, dy in the first two, w in dx) and which
 // hold it as the row (w in y, both in dw).  Products accumulate in fp32.
 //
-// A block of 4 waves computes a 128 x 128 tile, each wave 64 x 64, with steps
-// of 128 bytes of the summed index (64 16-bit or 32 fp32 elements).  Both
-// operands' steps are staged in LDS, double buffered, in the orientation they
-// have in memory; operands whose rows are the summed index are turned by the
-// transposing LDS read (16-bit) or read element by element (fp32).
+// A block computes one tile of the output, in steps of 64 bytes of the summed
+// index (32 16-bit or 16 fp32 elements).  Both operands' steps are copied
+// straight into LDS in the orientation they have in memory, four steps ahead
+// of the matrix instructions; operands whose rows are the summed index are
+// turned by the transposing LDS read (16-bit) or read element by element
+// (fp32).
 //
 // The row operands' tiles come from the segment bounds on the device: tile
 // number -> segment by a wave-wide scan over the segments' tile counts, so no
@@ -28,7 +29,10 @@ namespace gspmm {
 namespace {
 
 constexpr int kWave = 64;
-constexpr int kStepBytes = 128;              // of the summed index, per row of a tile
+constexpr int kStepBytes = 64;               // of the summed index, per row of a tile
+constexpr int kChunks = kStepBytes / 16;     // 16-byte chunks of them
+constexpr int kParts = kStepBytes / 32;      // matrix steps of them
+constexpr int kStages = 4;                   // steps held in LDS
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -37,6 +41,22 @@ typedef short i16x4 __attribute__((ext_vector_type(4)));
 
 template <typename T>
 constexpr int kStep = kStepBytes / (int)sizeof(T);
+
+// LDS addresses keep their address space, and with it the name of the array
+// they point into (see Stages).
+typedef __attribute__((address_space(3))) char LdsByte;
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x2 __attribute__((ext_vector_type(2)));
+
+template <typename V>
+__device__ inline V lds_load(LdsByte *p) {
+    return __builtin_bit_cast(V, *(__attribute__((address_space(3))) i32x4 *)p);
+}
+
+template <typename V>
+__device__ inline void lds_store(LdsByte *p, const V &v) {
+    *(__attribute__((address_space(3))) i32x4 *)p = __builtin_bit_cast(i32x4, v);
+}
 
 __device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
@@ -57,16 +77,16 @@ using Medium = Shape<128, 128, 2, 2>;
 
 // ---- LDS layout of one operand's step, B rows of the tile ----
 //
-// KC (summed index contiguous): B rows of 128 bytes; chunk c of row r at
-// c ^ (r & 7), so that the 32 lanes that read one chunk column spread over
-// the banks.
-// KS (summed index = row), 16-bit: 64 rows of 2 B bytes; the 32-byte piece c
+// KC (summed index contiguous): B rows of 64 bytes; chunk c of row r at
+// c ^ (r / 4 & 3), so that 16 lanes that read one chunk column of 16 rows
+// cover all 64 banks once.
+// KS (summed index = row), 16-bit: 32 rows of 2 B bytes; the 32-byte piece c
 // of row k at c ^ 2 (k & 3), so that the four rows a 16-lane transposing read
-// touches lie in different banks.  fp32: 32 rows of 4 B bytes, as they are.
+// touches lie in different banks.  fp32: 16 rows of 4 B bytes, as they are.
 
 template <typename T, bool KC, int B>
 __device__ inline int chunk_offset(int outer, int chunk) {
-    if constexpr (KC) return outer * kStepBytes + ((chunk ^ (outer & 7)) << 4);
+    if constexpr (KC) return outer * kStepBytes + ((chunk ^ (outer >> 2 & 3)) << 4);
     else if constexpr (sizeof(T) == 4) return outer * B * 4 + (chunk << 4);
     else return outer * B * 2 + (((chunk >> 1) ^ ((outer & 3) << 1)) << 5) + ((chunk & 1) << 4);
 }
@@ -92,7 +112,7 @@ struct Operand {
 template <typename T, bool KC, int B, int WAVES>
 struct Copy {
     static constexpr int kCopies = B * kStepBytes / 1024 / WAVES;
-    static constexpr int kRowsPerCopy = KC ? 8 * WAVES : 1024 * WAVES / (B * (int)sizeof(T));
+    static constexpr int kRowsPerCopy = KC ? 1024 / kStepBytes * WAVES : 1024 * WAVES / (B * (int)sizeof(T));
 
     const char *base;
     int64_t bytes;          // from base to the end of the array
@@ -108,7 +128,7 @@ struct Copy {
         bytes = uniform((int64_t)((const char *)o.end - (const char *)o.ptr));
         next_copy = kRowsPerCopy * row_bytes;
         if constexpr (KC) {
-            const int row = byte / kStepBytes, chunk = (byte / 16 % 8) ^ (row & 7);
+            const int row = byte / kStepBytes, chunk = (byte / 16 % kChunks) ^ (row >> 2 & 3);
             first = chunk * kPack<T>;
             left = uniform((int)o.inner);
             step_bytes = kStepBytes;
@@ -125,7 +145,7 @@ struct Copy {
         }
     }
 
-    __device__ inline void step(char *lds, int wave) {
+    __device__ inline void step(LdsByte *lds, int wave) {
         const int records = (int)max(int64_t(0), min(bytes, int64_t(0x7fffffff)));
         const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)base, 0, records, 0x00020000);
 #pragma unroll
@@ -143,10 +163,10 @@ struct Copy {
 
 // The same through registers, at any width and alignment.
 template <typename T, bool KC, int B, int WAVES>
-__device__ inline void fetch(const Operand<T> &o, int64_t k0, Pack<T> (&r)[B * 8 / (WAVES * kWave)]) {
+__device__ inline void fetch(const Operand<T> &o, int64_t k0, Pack<T> (&r)[B * kChunks / (WAVES * kWave)]) {
     constexpr int kPerRow = KC ? kStepBytes / 16 : B * (int)sizeof(T) / 16;
 #pragma unroll
-    for (int i = 0; i < B * 8 / (WAVES * kWave); ++i) {
+    for (int i = 0; i < B * kChunks / (WAVES * kWave); ++i) {
         const int idx = threadIdx.x + i * WAVES * kWave, row = idx / kPerRow, c = idx % kPerRow * kPack<T>;
         const int64_t out = KC ? row : k0 + row, in = KC ? k0 + c : c;
         const int64_t n = out < o.outer ? o.inner - in : 0;
@@ -155,46 +175,71 @@ __device__ inline void fetch(const Operand<T> &o, int64_t k0, Pack<T> (&r)[B * 8
 }
 
 template <typename T, bool KC, int B, int WAVES>
-__device__ inline void put(char *lds, const Pack<T> (&r)[B * 8 / (WAVES * kWave)]) {
+__device__ inline void put(LdsByte *lds, const Pack<T> (&r)[B * kChunks / (WAVES * kWave)]) {
     constexpr int kPerRow = KC ? kStepBytes / 16 : B * (int)sizeof(T) / 16;
 #pragma unroll
-    for (int i = 0; i < B * 8 / (WAVES * kWave); ++i) {
+    for (int i = 0; i < B * kChunks / (WAVES * kWave); ++i) {
         const int idx = threadIdx.x + i * WAVES * kWave;
-        *reinterpret_cast<Pack<T> *>(lds + chunk_offset<T, KC, B>(idx / kPerRow, idx % kPerRow)) = r[i];
+        lds_store(lds + chunk_offset<T, KC, B>(idx / kPerRow, idx % kPerRow), r[i]);
     }
 }
 
-// The lane's operand values of matrix step ks for the 32 tile rows from m0:
-// row m0 + lane % 32; 16-bit: summed elements ks * 16 + lane / 32 * 8 + 0..7,
-// fp32: ks * 8 + lane / 32 * 4 + 0..3.
-template <typename T, bool KC, int B>
-__device__ inline Pack<T> frag(const char *lds, int m0, int ks) {
-    const int lane = threadIdx.x & (kWave - 1), half = lane >> 5, m = m0 + (lane & 31);
-    if constexpr (KC) {
-        return *reinterpret_cast<const Pack<T> *>(lds + chunk_offset<T, true, B>(m, 2 * ks + half));
-    } else if constexpr (sizeof(T) == 4) {
-        Pack<T> r;
+// The lane's operand values of matrix step ks for the 32 tile rows from
+// m0 + 32 i: row m0 + 32 i + lane % 32; 16-bit: summed elements ks * 16 +
+// lane / 32 * 8 + 0..7, fp32: ks * 8 + lane / 32 * 4 + 0..3.
+//
+// Offsets that depend on the lane are computed once and hidden from the
+// optimiser, so that an address is a stage, a lane's offset and a constant:
+// longer chains lose the stage's name (see Stages).
+template <typename T, bool KC, int B, int COUNT>
+struct Reader {
+    static constexpr bool kTurned = !KC && sizeof(T) == 2;
+    int at[KC ? kParts : kTurned ? COUNT : 1];
+
+    __device__ inline Reader(int m0) {
+        const int lane = threadIdx.x & (kWave - 1), half = lane >> 5, m = m0 + (lane & 31);
+        if constexpr (KC) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            r.v[j] = *reinterpret_cast<const float *>(lds + (ks * 8 + half * 4 + j) * B * 4 + m * 4);
-        return r;
-    } else {
-        // lane l of a 16-lane group points at 4 elements of summed row l / 4
-        // and receives element l of the rows 0..3
-        const int l = lane & 15, piece = (m0 >> 4) + ((lane >> 4) & 1);
-        struct {
-            i16x4 lo, hi;
-        } both;
+            for (int ks = 0; ks < kParts; ++ks) at[ks] = chunk_offset<T, true, B>(m, 2 * ks + half);
+        } else if constexpr (kTurned) {
+            // lane l of a 16-lane group points at 4 elements of summed row
+            // l / 4 and receives element l of the rows 0..3
+            const int l = lane & 15, k = half * 8 + (l >> 2);
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const int k = ks * 16 + half * 8 + q * 4 + (l >> 2);
-            const int at = k * B * 2 + ((piece ^ ((k & 3) << 1)) << 5) + ((l & 3) << 3);
-            auto *p = (__attribute__((address_space(3))) i16x4 *)(lds + at);
-            (q ? both.hi : both.lo) = __builtin_amdgcn_ds_read_tr16_b64_v4i16(p);
+            for (int i = 0; i < COUNT; ++i) {
+                const int piece = (m0 >> 4) + 2 * i + ((lane >> 4) & 1);
+                at[i] = k * B * 2 + ((piece ^ ((k & 3) << 1)) << 5) + ((l & 3) << 3);
+            }
+        } else {
+            at[0] = half * 4 * B * 4 + m * 4;
         }
-        return __builtin_bit_cast(Pack<T>, both);
+#pragma unroll
+        for (int &o : at) asm volatile("" : "+v"(o));
     }
-}
+
+    template <int BASE>
+    __device__ inline Pack<T> read(LdsByte *stage, int i, int ks) const {
+        if constexpr (KC) {
+            return lds_load<Pack<T>>(stage + at[ks] + (BASE + i * 32 * kStepBytes));
+        } else if constexpr (kTurned) {
+            struct {
+                i16x4 lo, hi;
+            } both;
+            typedef __attribute__((address_space(3))) i16x4 LdsFour;
+            LdsByte *p = stage + at[i] + (BASE + ks * 16 * B * 2);
+            both.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsFour *)p);
+            both.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsFour *)(p + 4 * B * 2));
+            return __builtin_bit_cast(Pack<T>, both);
+        } else {
+            Pack<T> r;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                r.v[j] = *(__attribute__((address_space(3))) float *)(stage + at[0] +
+                                                                      (BASE + (ks * 8 + j) * B * 4 + i * 32 * 4));
+            return r;
+        }
+    }
+};
 
 // acc += a . b with a's 32 rows in the lanes and b's 32 rows in the registers
 // (operands exchanged): lane l holds row l % 32 of a against rows
@@ -213,110 +258,171 @@ __device__ inline void multiply(const Pack<T> &a, const Pack<T> &b, f32x16 &acc)
     }
 }
 
+// Waits until at most N of the wave's copies are in flight and its LDS reads
+// are back, then for the block; LDS accesses stay on their side of it.
+template <int N>
+__device__ inline void wait_copies() {
+    __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4) << 14 | 0x0070);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+}
+
+// The stages of a block.  Each is an array of its own, named at compile time
+// by the unrolled loop below: a read of one stage then does not wait for the
+// copies into the others.
+struct Stages {
+    LdsByte *at[kStages];
+};
+
+#define SEGMENT_STAGES(name, bytes)                                                                 \
+    __shared__ __attribute__((aligned(1024))) char name##0[bytes];                                  \
+    __shared__ __attribute__((aligned(1024))) char name##1[bytes];                                  \
+    __shared__ __attribute__((aligned(1024))) char name##2[bytes];                                  \
+    __shared__ __attribute__((aligned(1024))) char name##3[bytes];                                  \
+    const Stages name = {{(LdsByte *)name##0, (LdsByte *)name##1, (LdsByte *)name##2, (LdsByte *)name##3}}
+
 // out[0..rows) x [0..cols) of a tile = A . B over K summed elements.
 template <typename T, typename OUT, typename S, bool AKC, bool BKC, bool DIRECT>
-__device__ inline void tile_product(char *lds, const Operand<T> &a, const Operand<T> &b, int64_t K, OUT *out,
+__device__ inline void tile_product(const Stages &lds, const Operand<T> &a, const Operand<T> &b, int64_t K, OUT *out,
                                     int64_t ldo, int64_t rows, int64_t cols) {
     constexpr int MI = S::MI, NI = S::NI, kA = S::BM * kStepBytes;
-    const int wave = uniform((int)threadIdx.x / kWave), lane = threadIdx.x & (kWave - 1);
+    const int wave = uniform((int)threadIdx.x / kWave);
     const int m0 = wave / S::WC * (MI * 32), n0 = wave % S::WC * (NI * 32);
     f32x16 acc[MI][NI] = {};
     const int steps = (int)((K + kStep<T> - 1) / kStep<T>);
-    Pack<T> fa[4][MI], fb[4][NI];
-    auto multiply_part = [&](int ks) {
-#pragma unroll
-        for (int i = 0; i < MI; ++i)
-#pragma unroll
-            for (int j = 0; j < NI; ++j) multiply<T>(fa[ks][i], fb[ks][j], acc[i][j]);
+    struct Operands {
+        Pack<T> a[kParts][MI], b[kParts][NI];
     };
-    auto read_part = [&](const char *cur, int ks) {
+    const Reader<T, AKC, S::BM, MI> read_a(m0);
+    const Reader<T, BKC, S::BN, NI> read_b(n0);
+    auto read_step = [&](LdsByte *from, Operands &to) {
 #pragma unroll
-        for (int i = 0; i < MI; ++i) fa[ks][i] = frag<T, AKC, S::BM>(cur, m0 + i * 32, ks);
+        for (int ks = 0; ks < kParts; ++ks) {
 #pragma unroll
-        for (int j = 0; j < NI; ++j) fb[ks][j] = frag<T, BKC, S::BN>(cur + kA, n0 + j * 32, ks);
+            for (int j = 0; j < NI; ++j) to.b[ks][j] = read_b.template read<kA>(from, j, ks);
+#pragma unroll
+            for (int i = 0; i < MI; ++i) to.a[ks][i] = read_a.template read<0>(from, i, ks);
+        }
+    };
+    auto multiply_step = [&](const Operands &o) {
+#pragma unroll
+        for (int ks = 0; ks < kParts; ++ks)
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+                for (int j = 0; j < NI; ++j) multiply<T>(o.a[ks][i], o.b[ks][j], acc[i][j]);
     };
     if constexpr (DIRECT) {
+        // In step t the matrix instructions work on registers read in step
+        // t - 1, stage t + 1 is read, and the copies of step t + 4 go into
+        // stage t.  Copies behind the last step read nothing and write zeros,
+        // so that every step waits for the same number of them; the loop body
+        // has no branch, so that a read waits for the copies of its own stage.
         Copy<T, AKC, S::BM, S::kWaves> ca(a, wave);
         Copy<T, BKC, S::BN, S::kWaves> cb(b, wave);
-        if (steps > 0) {
-            ca.step(lds, wave);
-            cb.step(lds + kA, wave);
-        }
-        __syncthreads();
-        for (int t = 0; t < steps; ++t) {
-            const char *cur = lds + (t & 1) * S::kStageBytes;
-            char *next = lds + ((t + 1) & 1) * S::kStageBytes;
-            // every read of this step goes out before the next step's copies
-            // (an LDS read behind a copy would wait for it); the last of them
-            // take the registers of the first part's operands
-            read_part(cur, 0);
-            read_part(cur, 1);
-            read_part(cur, 2);
+        constexpr int kCopies = decltype(ca)::kCopies + decltype(cb)::kCopies;
+        Operands set[2];
+        auto copy_step = [&](LdsByte *to) {
+            ca.step(to, wave);
+            cb.step(to + kA, wave);
+        };
+        auto one_step = [&](int u) {
+            wait_copies<(kStages - 2) * kCopies>();
+            copy_step(lds.at[u]);
+            read_step(lds.at[(u + 1) % kStages], set[(u + 1) & 1]);
+            multiply_step(set[u & 1]);
             __builtin_amdgcn_sched_barrier(0);
-            multiply_part(0);
-            read_part(cur, 3);
-            __builtin_amdgcn_sched_barrier(0);
-            if (t + 1 < steps) {
-                ca.step(next, wave);
-                cb.step(next + kA, wave);
-            }
-            __builtin_amdgcn_sched_barrier(0);
-            multiply_part(1);
-            multiply_part(2);
-            multiply_part(3);
-            __builtin_amdgcn_sched_barrier(0);       // the barrier's wait for the copies stays behind them
-            __syncthreads();
-        }
-    } else {
-        constexpr int kRegA = S::BM * 8 / S::kThreads, kRegB = S::BN * 8 / S::kThreads;
-        Pack<T> ra[kRegA], rb[kRegB];
-        if (steps > 0) {
-            fetch<T, AKC, S::BM, S::kWaves>(a, 0, ra);
-            fetch<T, BKC, S::BN, S::kWaves>(b, 0, rb);
-            put<T, AKC, S::BM, S::kWaves>(lds, ra);
-            put<T, BKC, S::BN, S::kWaves>(lds + kA, rb);
-        }
-        __syncthreads();
-        for (int t = 0; t < steps; ++t) {
-            const char *cur = lds + (t & 1) * S::kStageBytes;
-            char *next = lds + ((t + 1) & 1) * S::kStageBytes;
-            if (t + 1 < steps) {
-                fetch<T, AKC, S::BM, S::kWaves>(a, (int64_t)(t + 1) * kStep<T>, ra);
-                fetch<T, BKC, S::BN, S::kWaves>(b, (int64_t)(t + 1) * kStep<T>, rb);
-            }
+        };
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks) {
-                read_part(cur, ks);
-                multiply_part(ks);
+        for (int u = 0; u < kStages; ++u) copy_step(lds.at[u]);
+        wait_copies<(kStages - 1) * kCopies>();
+        read_step(lds.at[0], set[0]);
+        int t = steps;
+        for (; t >= kStages; t -= kStages) {
+#pragma unroll
+            for (int u = 0; u < kStages; ++u) one_step(u);
+        }
+        if (t > 0) {
+            one_step(0);
+            if (t > 1) {
+                one_step(1);
+                if (t > 2) one_step(2);
             }
-            if (t + 1 < steps) {
-                put<T, AKC, S::BM, S::kWaves>(next, ra);
-                put<T, BKC, S::BN, S::kWaves>(next + kA, rb);
+        }
+        wait_copies<0>();
+    } else {
+        constexpr int kRegA = S::BM * kChunks / S::kThreads, kRegB = S::BN * kChunks / S::kThreads;
+        Pack<T> ra[kRegA], rb[kRegB];
+        Operands set;
+        auto fetch_step = [&](int t) {
+            fetch<T, AKC, S::BM, S::kWaves>(a, (int64_t)t * kStep<T>, ra);
+            fetch<T, BKC, S::BN, S::kWaves>(b, (int64_t)t * kStep<T>, rb);
+        };
+        auto put_step = [&](LdsByte *to) {
+            put<T, AKC, S::BM, S::kWaves>(to, ra);
+            put<T, BKC, S::BN, S::kWaves>(to + kA, rb);
+        };
+        if (steps > 0) {
+            fetch_step(0);
+            put_step(lds.at[0]);
+        }
+        __syncthreads();
+        for (int t = 0; t < steps; t += 2) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                if (t + u < steps) {
+                    const bool more = t + u + 1 < steps;
+                    if (more) fetch_step(t + u + 1);
+                    read_step(lds.at[u], set);
+                    multiply_step(set);
+                    if (more) put_step(lds.at[1 - u]);
+                    __syncthreads();
+                }
             }
-            __syncthreads();
         }
     }
+    // The outputs go through LDS (the stages, read out by now) so that a store
+    // covers whole rows of the tile: a lane holds 4 columns of one row, and 32
+    // rows to a store would reach the L2 as 16-byte pieces.  Chunk c of row r
+    // stands at c ^ r.
+    constexpr int kRow = S::BN * (int)sizeof(OUT), kRowChunks = kRow / 16, kStageRows = S::kStageBytes / kRow;
+    static_assert(kStages * kStageRows >= S::BM && kStageRows % 32 == 0, "the stages hold the tile");
+    int thread = threadIdx.x;
+    asm volatile("" : "+v"(thread));                 // addresses of the stores are not kept through the loop
+    const int lane = thread & (kWave - 1);
 #pragma unroll
-    for (int i = 0; i < MI; ++i) {
-        const int64_t r = m0 + i * 32 + (lane & 31);
-        if (r >= rows) continue;
+    for (int wr = 0; wr < S::WR; ++wr) {             // the stage is known at compile time
+        if (wave / S::WC != wr) continue;
 #pragma unroll
-        for (int j = 0; j < NI; ++j)
+        for (int i = 0; i < MI; ++i) {
+            const int r0 = (wr * MI + i) * 32, r = r0 + (lane & 31);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int64_t c = n0 + j * 32 + q * 8 + (lane >> 5) * 4;
-                struct {
-                    OUT v[4];
-                } o;
+            for (int j = 0; j < NI; ++j)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o.v[e] = (OUT)acc[i][j][q * 4 + e];
-                OUT *p = out + r * ldo + c;
-                if (c + 4 <= cols) __builtin_memcpy(p, &o, sizeof(o));
-                else
+                for (int q = 0; q < 4; ++q) {
+                    const int byte = (n0 + j * 32 + q * 8 + (lane >> 5) * 4) * (int)sizeof(OUT);
+                    struct alignas(4 * sizeof(OUT)) Four {
+                        OUT v[4];
+                    } o;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (c + e < cols) p[e] = o.v[e];
-            }
+                    for (int e = 0; e < 4; ++e) o.v[e] = (OUT)acc[i][j][q * 4 + e];
+                    LdsByte *p = lds.at[r0 / kStageRows] + r % kStageRows * kRow +
+                                 (((byte >> 4) ^ (r & (kRowChunks - 1))) << 4) + (byte & 15);
+                    if constexpr (sizeof(OUT) == 4) lds_store(p, o);
+                    else *(__attribute__((address_space(3))) i32x2 *)p = __builtin_bit_cast(i32x2, o);
+                }
+        }
+    }
+    __syncthreads();
+    constexpr int kRowsPerPass = S::kThreads / kRowChunks;
+    const int chunk = thread % kRowChunks, c = chunk * kPack<OUT>;
+#pragma unroll
+    for (int r0 = 0; r0 < S::BM; r0 += kRowsPerPass) {
+        const int r = r0 + thread / kRowChunks;
+        const auto o = lds_load<Pack<OUT>>(lds.at[r0 / kStageRows] + r % kStageRows * kRow +
+                                           ((chunk ^ (r & (kRowChunks - 1))) << 4));
+        if (r < rows) store_pack(out + r * ldo + c, o, cols - c);
     }
 }
 
@@ -335,16 +441,20 @@ __device__ inline int64_t run_bound(const SegmentArgs &a, int64_t i) {
     return b < 0 ? 0 : b > a.R ? a.R : b;
 }
 
-// Run and first row of row tile `tile`; run < 0: there is no such tile.
+// Tile number `tile` of the runs [v0, v1), each cut into tiles of `len` rows:
+// its run, first row, and end of the run; run < 0: there is no such tile.
 // Every wave finds it by itself: 64 runs at a time, a scan of their tiles.
-template <int BM>
-__device__ inline void find_tile(const SegmentArgs &a, int64_t tile, int64_t *run, int64_t *row, int64_t *end) {
+struct RowTile {
+    int64_t run, row, end;
+};
+
+__device__ inline RowTile find_tile(const SegmentArgs &a, int64_t v0, int64_t v1, int64_t len, int64_t tile) {
     const int lane = threadIdx.x & (kWave - 1);
-    *run = -1;
-    for (int64_t v0 = 0; v0 < a.E + 2; v0 += kWave) {
+    RowTile t = {-1, 0, 0};
+    for (; v0 < v1; v0 += kWave) {
         const int64_t v = v0 + lane;
-        const int64_t lo = v < a.E + 2 ? run_bound(a, v) : 0, hi = v < a.E + 2 ? run_bound(a, v + 1) : 0;
-        const int64_t mine = hi > lo ? (hi - lo + BM - 1) / BM : 0;
+        const int64_t lo = v < v1 ? run_bound(a, v) : 0, hi = v < v1 ? run_bound(a, v + 1) : 0;
+        const int mine = hi > lo ? (int)((uint32_t)(hi - lo + len - 1) / (uint32_t)len) : 0;
         int64_t incl = mine;
 #pragma unroll
         for (int o = 1; o < kWave; o <<= 1) {
@@ -354,14 +464,29 @@ __device__ inline void find_tile(const SegmentArgs &a, int64_t tile, int64_t *ru
         const uint64_t past = __ballot(incl > tile);
         if (past) {
             const int at = __ffsll((unsigned long long)past) - 1;
-            const int64_t before = __shfl(incl - mine, at, kWave);
-            *run = v0 + at;
-            *row = __shfl(lo, at, kWave) + (tile - before) * BM;
-            *end = __shfl(hi, at, kWave);
-            return;
+            t.run = v0 + at;
+            t.row = __shfl(lo, at, kWave) + (tile - __shfl(incl - mine, at, kWave)) * len;
+            t.end = __shfl(hi, at, kWave);
+            break;
         }
         tile -= __shfl(incl, kWave - 1, kWave);
     }
+    t.run = uniform(t.run);
+    t.row = uniform(t.row);
+    t.end = uniform(t.end);
+    return t;
+}
+
+// Tiles of the runs [v0, v1) together.
+__device__ inline int64_t count_tiles(const SegmentArgs &a, int64_t v0, int64_t v1, int64_t len) {
+    int64_t sum = 0;
+    for (int64_t v = v0 + (threadIdx.x & (kWave - 1)); v < v1; v += kWave) {
+        const int64_t lo = run_bound(a, v), hi = run_bound(a, v + 1);
+        if (hi > lo) sum += (hi - lo + len - 1) / len;
+    }
+#pragma unroll
+    for (int o = kWave / 2; o > 0; o >>= 1) sum += __shfl_xor(sum, o, kWave);
+    return uniform(sum);
 }
 
 // Blocks are dealt to the 8 XCDs in turn: give each XCD a run of consecutive
@@ -373,19 +498,16 @@ __device__ inline int64_t xcd_order(int64_t id, int64_t total) {
 
 template <typename T, typename S, bool TRANSPOSED, bool DIRECT>
 __global__ __launch_bounds__(S::kThreads) void segment_kernel(SegmentArgs a, int64_t col_tiles, int64_t total) {
-    __shared__ __attribute__((aligned(1024))) char lds[2 * S::kStageBytes];
+    SEGMENT_STAGES(lds, S::kStageBytes);
     const int64_t K = TRANSPOSED ? a.O : a.I, N = TRANSPOSED ? a.I : a.O;
     const T *in = (const T *)(TRANSPOSED ? a.dy : a.x), *w = (const T *)a.w;
     for (int64_t id = blockIdx.x; id < total; id += gridDim.x) {
         const int64_t t = xcd_order(id, total), n0 = t % col_tiles * S::BN;
-        int64_t run, row, end;
-        find_tile<S::BM>(a, t / col_tiles, &run, &row, &end);
-        run = uniform(run);
-        if (run < 0) continue;
-        row = uniform(row);
-        end = uniform(end);
+        const RowTile rt = find_tile(a, 0, a.E + 2, S::BM, t / col_tiles);
+        if (rt.run < 0) continue;
+        const int64_t run = rt.run, row = rt.row;
         T *out = (T *)a.y + row * N + n0;
-        const int64_t rows = end - row;
+        const int64_t rows = rt.end - row;
         if (run == 0 || run > a.E) {
             tile_zero<T, S>(out, N, rows, N - n0);
             continue;
@@ -414,50 +536,76 @@ __global__ __launch_bounds__(S::kThreads) void segment_kernel(SegmentArgs a, int
     }
 }
 
-// dw: tile (segment, split of its rows, tile of [I, O]); splits > 1 write fp32
-// partial sums [splits][E][I][O].
+// Segment whose length is the `rank`-th largest (ties by number), for up to 64.
+__device__ inline int64_t segment_by_length(const SegmentArgs &a, int rank) {
+    const int lane = threadIdx.x & (kWave - 1);
+    const int64_t len = lane < a.E ? run_bound(a, lane + 2) - run_bound(a, lane + 1) : INT64_MIN;
+    int before = 0;
+    for (int e = 0; e < (int)a.E; ++e) {
+        const int64_t other = __shfl(len, e, kWave);
+        before += other > len || (other == len && e < lane);
+    }
+    return uniform((int)__ffsll((unsigned long long)__ballot(lane < a.E && before == rank)) - 1);
+}
+
+// dw.  chunk == 0: tile (segment, tile of [I, O]) over all rows of the
+// segment; the longest segments start first.  chunk > 0: tile (chunk of a
+// segment's rows, tile of [I, O]) into fp32 partial sums, one [I, O] for each
+// chunk in the order of the segments.
 template <typename T, typename OUT, typename S, bool DIRECT>
 __global__ __launch_bounds__(S::kThreads) void segment_dw_kernel(SegmentArgs a, OUT *dst, int64_t row_tiles,
-                                                                 int64_t col_tiles, int64_t splits, int64_t total) {
-    __shared__ __attribute__((aligned(1024))) char lds[2 * S::kStageBytes];
+                                                                 int64_t col_tiles, int64_t chunk, int64_t total) {
+    SEGMENT_STAGES(lds, S::kStageBytes);
     for (int64_t id = blockIdx.x; id < total; id += gridDim.x) {
-        int64_t t = xcd_order(id, total);
+        int64_t t = chunk ? xcd_order(id, total) : id;
         const int64_t n0 = t % col_tiles * S::BN;
         t /= col_tiles;
         const int64_t m0 = t % row_tiles * S::BM;
         t /= row_tiles;
-        const int64_t s = t % splits, e = t / splits;
-        const int64_t lo = run_bound(a, e + 1);
-        int64_t len = run_bound(a, e + 2) - lo;
-        if (len < 0) len = 0;
-        const int64_t steps = (len + kStep<T> - 1) / kStep<T>, per = (steps + splits - 1) / splits * kStep<T>;
-        const int64_t k0 = min(len, s * per), k1 = min(len, k0 + per);
+        int64_t row, end;
+        if (chunk) {
+            const RowTile rt = find_tile(a, 1, a.E + 1, chunk, t);
+            if (rt.run < 0) continue;
+            row = rt.row;
+            end = min(rt.end, row + chunk);
+        } else {
+            if (a.E <= kWave) t = max(int64_t(0), segment_by_length(a, (int)t));
+            row = run_bound(a, t + 1);
+            end = max(row, run_bound(a, t + 2));
+        }
         Operand<T> A, B;
-        A.ptr = (const T *)a.x + (lo + k0) * a.I + m0;
+        A.ptr = (const T *)a.x + row * a.I + m0;
         A.ld = a.I;
-        A.outer = k1 - k0;
+        A.outer = end - row;
         A.inner = a.I - m0;
         A.end = (const T *)a.x + a.R * a.I;
-        B.ptr = (const T *)a.dy + (lo + k0) * a.O + n0;
+        B.ptr = (const T *)a.dy + row * a.O + n0;
         B.ld = a.O;
-        B.outer = k1 - k0;
+        B.outer = end - row;
         B.inner = a.O - n0;
         B.end = (const T *)a.dy + a.R * a.O;
         __syncthreads();
-        tile_product<T, OUT, S, false, false, DIRECT>(lds, A, B, k1 - k0, dst + ((s * a.E + e) * a.I + m0) * a.O + n0,
-                                                      a.O, a.I - m0, a.O - n0);
+        tile_product<T, OUT, S, false, false, DIRECT>(lds, A, B, end - row, dst + (t * a.I + m0) * a.O + n0, a.O,
+                                                      a.I - m0, a.O - n0);
     }
 }
 
 constexpr int kFoldThreads = 256;
 
+// Adds a segment's partial sums in the order of its chunks.
 template <typename T>
-__global__ __launch_bounds__(kFoldThreads) void segment_fold_kernel(const float *partial, T *out, int64_t n,
-                                                                    int64_t splits) {
-    for (int64_t i = (int64_t)blockIdx.x * kFoldThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kFoldThreads) {
-        float t = 0.0f;
-        for (int64_t s = 0; s < splits; ++s) t += partial[s * n + i];
-        out[i] = (T)t;
+__global__ __launch_bounds__(kFoldThreads) void segment_fold_kernel(SegmentArgs a, int64_t chunk) {
+    const int64_t n = a.I * a.O;
+    for (int64_t e = blockIdx.y; e < a.E; e += gridDim.y) {
+        const int64_t first = count_tiles(a, 1, e + 1, chunk), parts = count_tiles(a, e + 1, e + 2, chunk);
+        const float *from = a.partial + first * n;
+        for (int64_t i = (int64_t)blockIdx.x * kFoldThreads + threadIdx.x; i < n;
+             i += (int64_t)gridDim.x * kFoldThreads) {
+            float t = 0.0f;
+#pragma unroll 8
+            for (int64_t p = 0; p < parts; ++p) t += from[p * n + i];
+            ((T *)a.y)[e * n + i] = (T)t;
+        }
     }
 }
 
@@ -475,11 +623,13 @@ bool direct_rows(const void *p, int64_t width, int size) {
 // 256 x 256 tiles when there are enough of them to fill the chip.
 bool large_tiles(int64_t tiles, int size, bool direct) { return direct && size == 2 && tiles >= 2 * kUnits; }
 
-// Splits of each segment's rows in dw: enough tiles to fill the chip, but at
-// least 8 steps of rows on average in each.
+// dw: whole segments when their tiles fill the chip twice; else chunks of
+// rows, about four tiles of work for each compute unit and at least 256
+// elements of the summed index, so that unequal segments cost no balance.
 struct DwShape {
     bool large;
-    int64_t row_tiles, col_tiles, splits;
+    int64_t row_tiles, col_tiles;
+    int64_t chunk, chunks;       // rows of a chunk (0: whole segments) and the most chunks there can be
 };
 
 DwShape dw_shape(int64_t R, int64_t E, int64_t I, int64_t O, int size, bool direct) {
@@ -488,9 +638,12 @@ DwShape dw_shape(int64_t R, int64_t E, int64_t I, int64_t O, int size, bool dire
     const int tile = d.large ? 256 : 128;
     d.row_tiles = tiles_of(I, tile);
     d.col_tiles = tiles_of(O, tile);
-    const int64_t tiles = E * d.row_tiles * d.col_tiles;
-    const int64_t want = (4 * kUnits + tiles - 1) / tiles, most = std::max<int64_t>(1, R / E / (8 * kStepBytes / size));
-    d.splits = d.large ? 1 : std::max<int64_t>(1, std::min(want, most));
+    const int64_t tiles = d.row_tiles * d.col_tiles, want = std::max<int64_t>(1, 4 * kUnits / tiles);
+    d.chunk = d.chunks = 0;
+    if (E * tiles >= 2 * kUnits || R <= 256) return d;
+    d.chunk = std::max<int64_t>(256, (R + want - 1) / want);
+    d.chunk = (d.chunk + 31) / 32 * 32;
+    d.chunks = R / d.chunk + E;
     return d;
 }
 
@@ -519,21 +672,21 @@ hipError_t segment(const SegmentArgs &a, bool transposed, hipStream_t s) {
 
 template <typename T, typename OUT>
 hipError_t segment_dw_launch(const SegmentArgs &a, OUT *dst, const DwShape &d, bool direct, hipStream_t s) {
-    const int64_t total = a.E * d.splits * d.row_tiles * d.col_tiles;
+    const int64_t total = (d.chunk ? d.chunks : a.E) * d.row_tiles * d.col_tiles;
     const unsigned blocks = (unsigned)std::min(total, kMaxBlocks);
-    if constexpr (sizeof(T) == 2) {
+    if constexpr (sizeof(T) == 2 && __is_same(T, OUT)) {       // large tiles take whole segments
         if (d.large) {
             segment_dw_kernel<T, OUT, Large, true><<<blocks, Large::kThreads, 0, s>>>(a, dst, d.row_tiles, d.col_tiles,
-                                                                                     d.splits, total);
+                                                                                     d.chunk, total);
             return hipGetLastError();
         }
     }
     if (direct)
         segment_dw_kernel<T, OUT, Medium, true><<<blocks, Medium::kThreads, 0, s>>>(a, dst, d.row_tiles, d.col_tiles,
-                                                                                   d.splits, total);
+                                                                                   d.chunk, total);
     else
         segment_dw_kernel<T, OUT, Medium, false><<<blocks, Medium::kThreads, 0, s>>>(a, dst, d.row_tiles, d.col_tiles,
-                                                                                    d.splits, total);
+                                                                                    d.chunk, total);
     return hipGetLastError();
 }
 
@@ -541,11 +694,12 @@ template <typename T>
 hipError_t segment_dw(const SegmentArgs &a, hipStream_t s) {
     const bool direct = direct_rows(a.x, a.I, sizeof(T)) && direct_rows(a.dy, a.O, sizeof(T));
     const DwShape d = dw_shape(a.R, a.E, a.I, a.O, sizeof(T), direct);
-    if (d.splits == 1) return segment_dw_launch<T, T>(a, (T *)a.y, d, direct, s);
+    if (d.chunk == 0) return segment_dw_launch<T, T>(a, (T *)a.y, d, direct, s);
     if (const hipError_t e = segment_dw_launch<T, float>(a, a.partial, d, direct, s)) return e;
-    const int64_t n = a.E * a.I * a.O;
-    segment_fold_kernel<T><<<(unsigned)std::min((n + kFoldThreads - 1) / kFoldThreads, kMaxBlocks), kFoldThreads, 0,
-                             s>>>(a.partial, (T *)a.y, n, d.splits);
+    const int64_t n = a.I * a.O;
+    const dim3 grid((unsigned)std::min<int64_t>((n + kFoldThreads - 1) / kFoldThreads, 1 << 16),
+                    (unsigned)std::min<int64_t>(a.E, 1 << 14));
+    segment_fold_kernel<T><<<grid, kFoldThreads, 0, s>>>(a, d.chunk);
     return hipGetLastError();
 }
 
@@ -553,10 +707,10 @@ hipError_t segment_dw(const SegmentArgs &a, hipStream_t s) {
 
 int64_t segment_workspace_floats(int64_t R, int64_t E, int64_t I, int64_t O, int type) {
     // the addresses are not known here: what either way of staging needs
-    int64_t splits = 1;
+    int64_t chunks = 0;
     for (const bool direct : {false, true})
-        splits = std::max(splits, dw_shape(R, E, I, O, type == SPMM_F32 ? 4 : 2, direct).splits);
-    return splits == 1 ? 0 : splits * E * I * O;
+        chunks = std::max(chunks, dw_shape(R, E, I, O, type == SPMM_F32 ? 4 : 2, direct).chunks);
+    return chunks * I * O;
 }
 
 hipError_t launch_segment(const SegmentArgs &a, bool transposed, int type, hipStream_t s) {
