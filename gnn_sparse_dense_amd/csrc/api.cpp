@@ -1787,7 +1787,7 @@ SPMM_API int spmm_route_build(const int64_t *expert, int64_t pairs, int64_t E, i
     return launched(launch_route(a, reinterpret_cast<hipStream_t>(stream)), "route launch");
 }
 
-SPMM_API int spmm_route_dispatch(const int64_t *offsets, const int32_t *position, int64_t T, int64_t k, int64_t E,
+SPMM_API int spmm_route_dispatch(const int64_t *offsets, const int32_t *order, int64_t T, int64_t k, int64_t E,
                                  const void *x, const void *weight, int weight_type, void *xs, int64_t N, int type,
                                  void *stream) {
     if (const int st = check_exchange(T, k, E, N, type, weight != nullptr, weight_type)) return st;
@@ -1796,7 +1796,7 @@ SPMM_API int spmm_route_dispatch(const int64_t *offsets, const int32_t *position
     int device;
     if (const int st = check_arrays(
             {{"offsets", offsets, (E + 1) * 8, 8, false},
-             {"position", position, T * k * 4, 4, false},
+             {"order", order, T * k * 4, 4, false},
              {"x", x, T * N * size, (size_t)size, false},
              {"weight", weight, weight ? T * k * type_size(weight_type) : 0, (size_t)type_size(weight_type), false},
              {"xs", xs, T * k * N * size, (size_t)size, true}},
@@ -1805,7 +1805,7 @@ SPMM_API int spmm_route_dispatch(const int64_t *offsets, const int32_t *position
     DeviceGuard dg(device);
     ExchangeArgs a = {};
     a.offsets = offsets;
-    a.position = position;
+    a.order = order;
     a.T = T;
     a.k = k;
     a.E = E;
@@ -1847,7 +1847,7 @@ SPMM_API int spmm_route_combine(const int64_t *offsets, const int32_t *position,
     return launched(launch_combine(a, type, reinterpret_cast<hipStream_t>(stream)), "combine launch");
 }
 
-SPMM_API int spmm_route_combine_backward(const int64_t *offsets, const int32_t *position, int64_t T, int64_t k,
+SPMM_API int spmm_route_combine_backward(const int64_t *offsets, const int32_t *order, int64_t T, int64_t k,
                                          int64_t E, const void *rows, const void *weight, int weight_type,
                                          const void *dout, void *drows, void *dweight, int64_t N, int type,
                                          void *stream) {
@@ -1857,7 +1857,7 @@ SPMM_API int spmm_route_combine_backward(const int64_t *offsets, const int32_t *
     const int64_t size = type_size(type), wsize = type_size(weight_type);
     int device;
     if (const int st = check_arrays({{"offsets", offsets, (E + 1) * 8, 8, false},
-                                     {"position", position, T * k * 4, 4, false},
+                                     {"order", order, T * k * 4, 4, false},
                                      {"rows", rows, dweight ? T * k * N * size : 0, (size_t)size, false},
                                      {"weight", weight, weight ? T * k * wsize : 0, (size_t)wsize, false},
                                      {"dout", dout, T * N * size, (size_t)size, false},
@@ -1868,7 +1868,7 @@ SPMM_API int spmm_route_combine_backward(const int64_t *offsets, const int32_t *
     DeviceGuard dg(device);
     ExchangeArgs a = {};
     a.offsets = offsets;
-    a.position = position;
+    a.order = order;
     a.T = T;
     a.k = k;
     a.E = E;

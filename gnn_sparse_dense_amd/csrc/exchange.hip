@@ -7,13 +7,26 @@
 //    waves) + (its rank inside its wave).  The rank comes from ballots: the
 //    lanes of a wave that hold the same key are found with one ballot per key
 //    bit, so equal keys keep their order and no atomic decides a place.
-//  * Dispatch: out[position[t, j]] = x[t].  Rows are walked by source, so
-//    every row of x is read once and written k times.
+//  * Dispatch: row p of the output is x[order[p] / k].  The output is one
+//    contiguous array, written in order in aligned 16-byte packs; the k copies
+//    of a row of x are read at different times, mostly from the Infinity Cache.
 //  * Combine: out[t] = sum_j weight[t, j] * rows[position[t, j]], j ascending,
 //    one fused multiply-add per term.  With no weights it is dispatch's
 //    gradient.
-//  * Combine's gradients: drows[position[t, j]] = weight[t, j] * dout[t] and
-//    dweight[t, j] = <rows[position[t, j]], dout[t]>, one pass over both.
+//  * Combine's gradients: drows[p] = weight[q] * dout[q / k] and dweight[q] =
+//    <rows[p], dout[q / k]> for the pair q = order[p], one pass over both.
+//
+// All three move bytes and nothing else.  Calls that move more than half of
+// the 256 MB Infinity Cache use non-temporal stores, and non-temporal loads
+// for rows that are read once when rows are whole 16-byte groups (lanes of
+// other rows share cache lines).  Measured: 16,384 x 2048 bf16 rows, k = 4:
+// dispatch walked by source row 118 us, with non-temporal stores 92 us, by
+// output row with them 77 us (4.3 TB/s of x once and the output); combine 77
+// us with plain, 72 us with non-temporal stores, 69 us with loads as well (4.9
+// TB/s); gradients by source row 134 us, by output row 118 us (5.1 TB/s).
+// 50,021 x 1433 fp16 rows, k = 3: dispatch by source row 239 us, by output
+// row in packs of one row 218 us, in aligned packs 190 us (3.0 TB/s; at width
+// 1432, with aligned loads, 143 us); combine 143, 136 and 147 us.
 #include "rows.h"
 
 #include <algorithm>
@@ -223,41 +236,48 @@ bool route_in_one_block(int64_t pairs, int64_t E) { return pairs <= 16 * 1024 &&
 // --------------------------------------------------------------- exchange
 
 constexpr int kThreads = 256;
+constexpr int64_t kMaxBlocks = 1 << 20;
+constexpr int64_t kStreamBytes = int64_t(128) << 20;     // half of the Infinity Cache
 
-// A launch's work as a flat list of (row, pack) items, 256 to a block.
-struct Items {
-    int64_t packs;      // packs of a row
-    int64_t total;      // rows * packs
-};
+// How a call's accesses go: plain, non-temporal stores, non-temporal loads of
+// what is read once as well.
+enum Access { kPlain, kStores, kBoth };
 
-__host__ __device__ inline int64_t packs_of(int64_t N, int pack) { return (N + pack - 1) / pack; }
+template <int ACCESS, typename T>
+__device__ inline Pack<T> load_once(const T *p, int64_t n) {
+    if constexpr (ACCESS == kBoth) return load_pack_stream(p, n);
+    else return load_pack(p, n);
+}
 
-// Row and pack of the thread's item.  The block's first item is split with
-// one division in 32 bits where the launch fits them, the thread's with a
-// comparison or a 32-bit division.
-__device__ inline bool item_of(int64_t block, int64_t packs, int64_t total, int64_t *row, int64_t *pack) {
-    const int64_t b0 = block * kThreads;
-    int64_t r, v;
-    if (total <= 0xffffffffLL) {
-        r = (uint32_t)b0 / (uint32_t)packs;
-        v = (uint32_t)b0 % (uint32_t)packs;
-    } else {
-        r = b0 / packs;
-        v = b0 % packs;
-    }
-    v += threadIdx.x;
-    if (packs >= kThreads) {
-        if (v >= packs) {
-            v -= packs;
-            ++r;
+template <int ACCESS, typename T>
+__device__ inline void store_out(T *p, const Pack<T> &r, int64_t n) {
+    if constexpr (ACCESS == kPlain) store_pack(p, r, n);
+    else store_pack_stream(p, r, n);
+}
+
+// a = a * n + b for a position `b` behind the start of row `a` of rows of n, b < n + 2^13.
+__device__ inline void carry(int64_t &row, uint32_t &col, uint32_t n) {
+    if (n >= 8192) {
+        if (col >= n) {
+            col -= n;
+            ++row;
         }
     } else {
-        r += (uint32_t)v / (uint32_t)packs;
-        v = (uint32_t)v % (uint32_t)packs;
+        row += col / n;
+        col %= n;
     }
-    *row = r;
-    *pack = v;
-    return b0 + threadIdx.x < total;
+}
+
+// Row and column of element `at` of rows of n, for a position that is the
+// same for the whole block.
+__device__ inline void split(int64_t at, uint32_t n, int64_t *row, uint32_t *col) {
+    if (at <= 0xffffffffLL) {
+        *row = (uint32_t)at / n;
+        *col = (uint32_t)at % n;
+    } else {
+        *row = at / n;
+        *col = (uint32_t)(at % n);
+    }
 }
 
 __device__ inline int64_t live_rows(const ExchangeArgs &a) {
@@ -265,38 +285,103 @@ __device__ inline int64_t live_rows(const ExchangeArgs &a) {
     return kept < 0 ? 0 : kept < rows ? kept : rows;
 }
 
+// Pair at place p, or -1 where the row is zero.
+__device__ inline int pair_at(const ExchangeArgs &a, int64_t p, int64_t kept) {
+    if (p >= kept) return -1;
+    const int q = a.order[p];
+    return q >= 0 && q < a.T * a.k ? q : -1;
+}
+
+// Element c of the output row that pair q fills (q < 0: zero).
 template <typename T>
-__global__ __launch_bounds__(kThreads) void dispatch_kernel(ExchangeArgs a, int64_t packs, int64_t total,
-                                                            int64_t blocks) {
-    const int64_t kept = live_rows(a), rows = a.T * a.k;
+__device__ inline T dispatched(const ExchangeArgs &a, int q, uint32_t c) {
+    if (q < 0) return (T)0.0f;
+    const T v = ((const T *)a.rows)[(int64_t)((uint32_t)q / (uint32_t)a.k) * a.N + c];
+    return a.weight ? (T)(load_weight<T>(a.weight, q, a.weight_fp32) * (float)v) : v;
+}
+
+// Pack number i of the output holds its elements [i * P - lead, i * P - lead
+// + P): packs are aligned in memory, the first and last may be partial, and a
+// pack may hold the end of one row and the start of the next.  A thread takes
+// U packs, kThreads apart, so that their loads are in flight together.
+template <typename T, int U, int ACCESS>
+__global__ __launch_bounds__(kThreads) void dispatch_kernel(ExchangeArgs a, int lead, int64_t blocks) {
+    constexpr int P = kPack<T>;
+    const int64_t kept = live_rows(a), rows = a.T * a.k, end = rows * a.N;
+    const uint32_t N = (uint32_t)a.N, k = (uint32_t)a.k;
     for (int64_t b = blockIdx.x; b < blocks; b += gridDim.x) {
-        int64_t t, v;
-        if (!item_of(b, packs, total, &t, &v)) continue;
-        const int64_t c = v * kPack<T>, n = a.N - c;
-        const Pack<T> x = load_pack((const T *)a.rows + t * a.N + c, n);
-        const Pack<T> zero = {};
-        for (int64_t j = 0; j < a.k; ++j) {
-            const int64_t p = a.position[t * a.k + j];
-            if (p < 0 || p >= rows) continue;
-            Pack<T> r = x;
-            if (a.weight) {
-                const float w = load_weight<T>(a.weight, t * a.k + j, a.weight_fp32);
+        const int64_t first = b * (kThreads * U * P) - lead;    // below 0 in block 0 only
+        int64_t p0;
+        uint32_t c0;
+        split(max(first, int64_t(0)), N, &p0, &c0);
+        Pack<T> r[U], tail[U];
+        int64_t at[U], p[U];
+        uint32_t c[U];
+        int q[U];
+        bool whole[U], two[U];
 #pragma unroll
-                for (int i = 0; i < kPack<T>; ++i) r.v[i] = (T)(w * (float)x.v[i]);
+        for (int u = 0; u < U; ++u) {
+            at[u] = first + (threadIdx.x + u * kThreads) * P;
+            p[u] = p0;
+            c[u] = c0 + (uint32_t)(max(at[u], int64_t(0)) - max(first, int64_t(0)));
+            if (at[u] < end) carry(p[u], c[u], N);
+            q[u] = at[u] < end ? pair_at(a, p[u], kept) : -1;
+            whole[u] = at[u] >= 0 && at[u] + P <= end && c[u] + P <= N;
+            two[u] = false;
+            r[u] = {};
+            if (whole[u]) {
+                if (q[u] >= 0) r[u] = load_pack((const T *)a.rows + (int64_t)((uint32_t)q[u] / k) * a.N + c[u]);
+            } else if (at[u] >= 0 && at[u] + P <= end && N >= P && !a.weight) {
+                // the end of one row and the start of the next: the packs of
+                // x around them, where both lie inside x
+                const int q1 = pair_at(a, p[u] + 1, kept);
+                const int64_t from = (int64_t)((uint32_t)max(q[u], 0) / k) * a.N + c[u];
+                const int64_t next = (int64_t)((uint32_t)max(q1, 0) / k) * a.N - (N - c[u]);
+                two[u] = (q[u] < 0 || from + P <= a.T * a.N) && (q1 < 0 || next >= 0);
+                tail[u] = {};
+                if (two[u] && q[u] >= 0) r[u] = load_pack((const T *)a.rows + from);
+                if (two[u] && q1 >= 0) tail[u] = load_pack((const T *)a.rows + next);
             }
-            store_pack((T *)a.out + p * a.N + c, p < kept ? r : zero, n);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (whole[u]) {
+                if (a.weight && q[u] >= 0) {
+                    const float w = load_weight<T>(a.weight, q[u], a.weight_fp32);
+#pragma unroll
+                    for (int i = 0; i < P; ++i) r[u].v[i] = (T)(w * (float)r[u].v[i]);
+                }
+                store_out<ACCESS>((T *)a.out + at[u], r[u], P);
+            } else if (two[u]) {
+#pragma unroll
+                for (uint32_t i = 0; i < P; ++i)
+                    if (i >= N - c[u]) r[u].v[i] = tail[u].v[i];
+                store_out<ACCESS>((T *)a.out + at[u], r[u], P);
+            } else if (at[u] < end) {                               // the ends, and rows below a pack
+                for (int64_t i = max(at[u], int64_t(0)); i < min(at[u] + P, end); ++i) {
+                    ((T *)a.out)[i] = dispatched<T>(a, q[u], c[u]);
+                    if (++c[u] == N) {
+                        c[u] = 0;
+                        q[u] = ++p[u] < rows ? pair_at(a, p[u], kept) : -1;
+                    }
+                }
+            }
         }
     }
 }
 
-template <typename T>
+template <typename T, int ACCESS>
 __global__ __launch_bounds__(kThreads) void combine_kernel(ExchangeArgs a, int64_t packs, int64_t total,
                                                            int64_t blocks) {
     const int64_t kept = live_rows(a);
     for (int64_t b = blockIdx.x; b < blocks; b += gridDim.x) {
-        int64_t t, v;
-        if (!item_of(b, packs, total, &t, &v)) continue;
-        const int64_t c = v * kPack<T>, n = a.N - c;
+        if (b * kThreads + threadIdx.x >= total) continue;
+        int64_t t;
+        uint32_t v;
+        split(b * kThreads, (uint32_t)packs, &t, &v);
+        v += threadIdx.x;
+        carry(t, v, (uint32_t)packs);
+        const int64_t c = (int64_t)v * kPack<T>, n = a.N - c;
         float acc[kPack<T>] = {};
         for (int64_t j0 = 0; j0 < a.k; j0 += 4) {
             Pack<T> r[4];
@@ -309,7 +394,7 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(ExchangeArgs a, int64
                 live[u] = p >= 0 && p < kept;
                 w[u] = 1.0f;
                 if (live[u]) {
-                    r[u] = load_pack((const T *)a.rows + p * a.N + c, n);
+                    r[u] = load_once<ACCESS>((const T *)a.rows + p * a.N + c, n);
                     if (a.weight) w[u] = load_weight<T>(a.weight, t * a.k + j, a.weight_fp32);
                 }
             }
@@ -323,79 +408,104 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(ExchangeArgs a, int64
         Pack<T> o;
 #pragma unroll
         for (int i = 0; i < kPack<T>; ++i) o.v[i] = (T)acc[i];
-        store_pack((T *)a.out + t * a.N + c, o, n);
+        store_out<ACCESS>((T *)a.out + t * a.N + c, o, n);
     }
 }
 
-// A group of G lanes takes one pair: it walks the row of dout and the pair's
-// row once, writes the row's gradient and sums the dot product over the group.
-template <typename T, int G>
-__global__ __launch_bounds__(kThreads) void combine_backward_kernel(ExchangeArgs a, int64_t packs, int64_t tasks) {
+// A group of G lanes takes one place: it walks its row and the row of dout
+// once, writes the row's gradient and sums the dot product over the group.
+template <typename T, int G, int ACCESS>
+__global__ __launch_bounds__(kThreads) void combine_backward_kernel(ExchangeArgs a, int64_t packs) {
     const int64_t kept = live_rows(a), rows = a.T * a.k;
     const int lane = threadIdx.x % G;
     const Pack<T> zero = {};
-    for (int64_t task0 = (int64_t)blockIdx.x * (kThreads / G); task0 < tasks;
-         task0 += (int64_t)gridDim.x * (kThreads / G)) {
-        const int64_t task = task0 + threadIdx.x / G;
+    for (int64_t p0 = (int64_t)blockIdx.x * (kThreads / G); p0 < rows; p0 += (int64_t)gridDim.x * (kThreads / G)) {
+        const int64_t p = p0 + threadIdx.x / G;
+        int q = -1;
+        bool live = false;
         float dot = 0.0f;
-        if (task < tasks) {
-            const int64_t t = task / a.k, p = a.position[task];
-            const bool live = p >= 0 && p < kept;
-            const float w = a.weight ? load_weight<T>(a.weight, task, a.weight_fp32) : 1.0f;
+        if (p < rows) {
+            q = a.order[p];
+            if (q < 0 || q >= rows) q = -1;
+            live = q >= 0 && p < kept;
+            const float w = live && a.weight ? load_weight<T>(a.weight, q, a.weight_fp32) : 1.0f;
+            const T *dout = (const T *)a.dout + (int64_t)((uint32_t)max(q, 0) / (uint32_t)a.k) * a.N;
             for (int64_t v = lane; v < packs; v += G) {
                 const int64_t c = v * kPack<T>, n = a.N - c;
+                Pack<T> o = zero;
                 if (live) {
-                    const Pack<T> d = load_pack((const T *)a.dout + t * a.N + c, n);
+                    const Pack<T> d = load_pack(dout + c, n);
                     if (a.dweight) {
-                        const Pack<T> r = load_pack((const T *)a.rows + p * a.N + c, n);
+                        const Pack<T> r = load_once<ACCESS>((const T *)a.rows + p * a.N + c, n);
 #pragma unroll
                         for (int i = 0; i < kPack<T>; ++i) dot = fmaf((float)r.v[i], (float)d.v[i], dot);
                     }
-                    if (a.drows) {
-                        Pack<T> o;
 #pragma unroll
-                        for (int i = 0; i < kPack<T>; ++i) o.v[i] = (T)(w * (float)d.v[i]);
-                        store_pack((T *)a.drows + p * a.N + c, o, n);
-                    }
-                } else if (a.drows && p >= 0 && p < rows) {
-                    store_pack((T *)a.drows + p * a.N + c, zero, n);
+                    for (int i = 0; i < kPack<T>; ++i) o.v[i] = (T)(w * (float)d.v[i]);
                 }
+                if (a.drows) store_out<ACCESS>((T *)a.drows + p * a.N + c, o, n);
             }
         }
         if (a.dweight) {
 #pragma unroll
             for (int o = G / 2; o > 0; o >>= 1) dot += __shfl_xor(dot, o, kWave);
-            if (lane == 0 && task < tasks) store_weight<T>(a.dweight, task, a.weight_fp32, dot);
+            if (lane == 0 && q >= 0) store_weight<T>(a.dweight, q, a.weight_fp32, dot);
         }
     }
 }
 
-constexpr int64_t kMaxBlocks = 1 << 20;
+// Access of a call that moves `bytes`, and of its rows that are read once.
+template <typename T>
+int access_of(const ExchangeArgs &a, int64_t bytes) {
+    if (bytes <= kStreamBytes) return kPlain;
+    return a.N % kPack<T> == 0 && (uintptr_t)a.rows % 16 == 0 ? kBoth : kStores;
+}
 
 template <typename T>
-hipError_t flat(void (*kernel)(ExchangeArgs, int64_t, int64_t, int64_t), const ExchangeArgs &a, hipStream_t s) {
-    const int64_t packs = packs_of(a.N, kPack<T>), total = a.T * packs;
+hipError_t dispatch(const ExchangeArgs &a, hipStream_t s) {
+    constexpr int P = kPack<T>;
+    const int lead = (int)((uintptr_t)a.out % 16 / sizeof(T));
+    const int64_t total = (a.T * a.k * a.N + lead + P - 1) / P;
+    const bool plain = access_of<T>(a, (a.k + 1) * a.T * a.N * (int)sizeof(T)) == kPlain;
+    // two packs to a thread once that still leaves every unit eight blocks
+    const int per = total >= int64_t(256) * 8 * 2 * kThreads ? 2 : 1;
+    const int64_t blocks = (total + kThreads * per - 1) / (kThreads * per);
+    const unsigned grid = (unsigned)std::min(blocks, kMaxBlocks);
+    if (per == 1) dispatch_kernel<T, 1, kPlain><<<grid, kThreads, 0, s>>>(a, lead, blocks);
+    else if (plain) dispatch_kernel<T, 2, kPlain><<<grid, kThreads, 0, s>>>(a, lead, blocks);
+    else dispatch_kernel<T, 2, kStores><<<grid, kThreads, 0, s>>>(a, lead, blocks);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t combine(const ExchangeArgs &a, hipStream_t s) {
+    const int64_t packs = (a.N + kPack<T> - 1) / kPack<T>, total = a.T * packs;
     const int64_t blocks = (total + kThreads - 1) / kThreads;
-    if (blocks == 0) return hipSuccess;
-    kernel<<<(unsigned)std::min(blocks, kMaxBlocks), kThreads, 0, s>>>(a, packs, total, blocks);
+    const unsigned grid = (unsigned)std::min(blocks, kMaxBlocks);
+    const int access = access_of<T>(a, (a.k + 1) * a.T * a.N * (int)sizeof(T));
+    if (access == kPlain) combine_kernel<T, kPlain><<<grid, kThreads, 0, s>>>(a, packs, total, blocks);
+    else if (access == kStores) combine_kernel<T, kStores><<<grid, kThreads, 0, s>>>(a, packs, total, blocks);
+    else combine_kernel<T, kBoth><<<grid, kThreads, 0, s>>>(a, packs, total, blocks);
     return hipGetLastError();
 }
 
 template <typename T, int G>
-hipError_t grouped(const ExchangeArgs &a, hipStream_t s) {
-    const int64_t tasks = a.T * a.k, blocks = (tasks + kThreads / G - 1) / (kThreads / G);
-    if (blocks == 0) return hipSuccess;
-    combine_backward_kernel<T, G><<<(unsigned)std::min(blocks, kMaxBlocks), kThreads, 0, s>>>(
-        a, packs_of(a.N, kPack<T>), tasks);
+hipError_t combine_backward_groups(const ExchangeArgs &a, int64_t packs, hipStream_t s) {
+    const int64_t rows = a.T * a.k, blocks = (rows + kThreads / G - 1) / (kThreads / G);
+    const unsigned grid = (unsigned)std::min(blocks, kMaxBlocks);
+    const int access = access_of<T>(a, (2 * a.k + 1) * a.T * a.N * (int)sizeof(T));
+    if (access == kPlain) combine_backward_kernel<T, G, kPlain><<<grid, kThreads, 0, s>>>(a, packs);
+    else if (access == kStores) combine_backward_kernel<T, G, kStores><<<grid, kThreads, 0, s>>>(a, packs);
+    else combine_backward_kernel<T, G, kBoth><<<grid, kThreads, 0, s>>>(a, packs);
     return hipGetLastError();
 }
 
 template <typename T>
 hipError_t combine_backward(const ExchangeArgs &a, hipStream_t s) {
-    const int64_t packs = packs_of(a.N, kPack<T>);
-    if (packs <= 4) return grouped<T, 4>(a, s);
-    if (packs <= 16) return grouped<T, 16>(a, s);
-    return grouped<T, 64>(a, s);
+    const int64_t packs = (a.N + kPack<T> - 1) / kPack<T>;
+    if (packs <= 4) return combine_backward_groups<T, 4>(a, packs, s);
+    if (packs <= 16) return combine_backward_groups<T, 16>(a, packs, s);
+    return combine_backward_groups<T, 64>(a, packs, s);
 }
 
 }  // namespace
@@ -426,15 +536,15 @@ hipError_t launch_route(const RouteArgs &a, hipStream_t s) {
 }
 
 hipError_t launch_dispatch(const ExchangeArgs &a, int type, hipStream_t s) {
-    if (type == SPMM_F32) return flat<float>(dispatch_kernel<float>, a, s);
-    if (type == SPMM_BF16) return flat<__bf16>(dispatch_kernel<__bf16>, a, s);
-    return flat<_Float16>(dispatch_kernel<_Float16>, a, s);
+    if (type == SPMM_F32) return dispatch<float>(a, s);
+    if (type == SPMM_BF16) return dispatch<__bf16>(a, s);
+    return dispatch<_Float16>(a, s);
 }
 
 hipError_t launch_combine(const ExchangeArgs &a, int type, hipStream_t s) {
-    if (type == SPMM_F32) return flat<float>(combine_kernel<float>, a, s);
-    if (type == SPMM_BF16) return flat<__bf16>(combine_kernel<__bf16>, a, s);
-    return flat<_Float16>(combine_kernel<_Float16>, a, s);
+    if (type == SPMM_F32) return combine<float>(a, s);
+    if (type == SPMM_BF16) return combine<__bf16>(a, s);
+    return combine<_Float16>(a, s);
 }
 
 hipError_t launch_combine_backward(const ExchangeArgs &a, int type, hipStream_t s) {

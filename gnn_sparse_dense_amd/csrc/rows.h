@@ -51,6 +51,33 @@ __device__ inline void store_pack(T *p, const Pack<T> &r, int64_t n) {
         if (i < n) p[i] = r.v[i];
 }
 
+// Streaming accesses: non-temporal, so that what is written once (or read
+// once) does not displace what is read again from the 256 MB Infinity Cache.
+template <int ALIGN>
+struct Stream;
+template <>
+struct Stream<2> {
+    typedef int V __attribute__((ext_vector_type(4), aligned(2)));
+};
+template <>
+struct Stream<4> {
+    typedef int V __attribute__((ext_vector_type(4), aligned(4)));
+};
+
+template <typename T>
+__device__ inline Pack<T> load_pack_stream(const T *p, int64_t n) {
+    typedef typename Stream<sizeof(T)>::V V;
+    if (n >= kPack<T>) return __builtin_bit_cast(Pack<T>, __builtin_nontemporal_load((const V *)p));
+    return load_pack(p, n);
+}
+
+template <typename T>
+__device__ inline void store_pack_stream(T *p, const Pack<T> &r, int64_t n) {
+    typedef typename Stream<sizeof(T)>::V V;
+    if (n >= kPack<T>) __builtin_nontemporal_store(__builtin_bit_cast(V, r), (V *)p);
+    else store_pack(p, r, n);
+}
+
 // A weight stored in fp32 or in the rows' own type.
 template <typename T>
 __device__ inline float load_weight(const void *w, int64_t i, bool fp32) {
@@ -81,7 +108,8 @@ hipError_t launch_route(const RouteArgs &a, hipStream_t s);
 
 struct ExchangeArgs {
     const int64_t *offsets;  // [E + 1]; rows from offsets[E] on belong to no expert
-    const int *position;     // [T, k]
+    const int *position;     // [T, k] (combine)
+    const int *order;        // [T * k] (dispatch, combine's gradients)
     int64_t T;
     int64_t k;
     int64_t E;

@@ -107,7 +107,7 @@ def spmm_route_dispatch(route: "RowRoute", x, xs, weight=None, stream=None) -> N
     """xs [T * k, N] = rows of x [T, N] in expert order (times weight [T, k])."""
     kind, wkind = _check_exchange(route, "x", x, route.T, weight)
     _check_tensor("xs", xs, (x.dtype,), (route.T * route.k, x.shape[1]), route.device)
-    _check(_lib.spmm_route_dispatch(_ptr(route.offsets), _ptr(route.position), route.T, route.k, route.E, _ptr(x),
+    _check(_lib.spmm_route_dispatch(_ptr(route.offsets), _ptr(route.order), route.T, route.k, route.E, _ptr(x),
                                     _ptr(weight), wkind, _ptr(xs), x.shape[1], kind, _stream(x, stream)))
 
 
@@ -133,7 +133,7 @@ def spmm_route_combine_backward(route: "RowRoute", rows, weight, dout, drows, dw
         types = (torch.float32, dout.dtype) if weight is None else (weight.dtype,)
         _check_tensor("dweight", dweight, types, (route.T, route.k), route.device)
         wkind = _TYPES[dweight.dtype]
-    _check(_lib.spmm_route_combine_backward(_ptr(route.offsets), _ptr(route.position), route.T, route.k, route.E,
+    _check(_lib.spmm_route_combine_backward(_ptr(route.offsets), _ptr(route.order), route.T, route.k, route.E,
                                             _ptr(rows), _ptr(weight), wkind, _ptr(dout), _ptr(drows), _ptr(dweight),
                                             dout.shape[1], kind, _stream(dout, stream)))
 

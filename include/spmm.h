@@ -491,26 +491,26 @@ int spmm_route_build(const int64_t *expert, int64_t pairs, int64_t E, int64_t *o
                      int32_t *position, void *workspace, int64_t workspace_bytes, void *stream);
 
 /*
- * Dispatch: xs [T * k, N], xs[position[t, j]] = x[t] (times weight[t, j] when
- * weight != NULL); rows from offsets[E] on are zero.
+ * Dispatch: xs [T * k, N], xs[p] = x[q / k] for the pair q = order[p] (times
+ * weight[q] when weight != NULL); rows from offsets[E] on are zero.
  * Combine: out [T, N], out[t] = sum over j, ascending, of weight[t, j] *
  * rows[position[t, j]] (weight 1 when NULL), one fused multiply-add per term;
  * pairs of no expert are skipped (their rows and weights are not read into
  * the sum), a row without experts is zero.
  * Each is the other's gradient: d x = combine(d xs, no weight), and with
- * d out = gradient of out: drows[position[t, j]] = weight[t, j] * dout[t]
- * (zero from offsets[E] on) and dweight[t, j] = <rows[position[t, j]],
- * dout[t]> (zero for pairs of no expert), both from
+ * dout the gradient of out, for the pair q = order[p]: drows[p] = weight[q] *
+ * dout[q / k] (zero from offsets[E] on) and dweight[q] = <rows[p],
+ * dout[q / k]> (zero for pairs of no expert), both from
  * spmm_route_combine_backward; either output may be NULL, `rows` too when
  * dweight is.  dweight has weight_type.
  */
-int spmm_route_dispatch(const int64_t *offsets, const int32_t *position, int64_t T, int64_t k, int64_t E,
+int spmm_route_dispatch(const int64_t *offsets, const int32_t *order, int64_t T, int64_t k, int64_t E,
                         const void *x, const void *weight, int weight_type, void *xs, int64_t N, int type,
                         void *stream);
 int spmm_route_combine(const int64_t *offsets, const int32_t *position, int64_t T, int64_t k, int64_t E,
                        const void *rows, const void *weight, int weight_type, void *out, int64_t N, int type,
                        void *stream);
-int spmm_route_combine_backward(const int64_t *offsets, const int32_t *position, int64_t T, int64_t k, int64_t E,
+int spmm_route_combine_backward(const int64_t *offsets, const int32_t *order, int64_t T, int64_t k, int64_t E,
                                 const void *rows, const void *weight, int weight_type, const void *dout, void *drows,
                                 void *dweight, int64_t N, int type, void *stream);
 
