@@ -161,16 +161,27 @@ struct Copy {
     }
 };
 
-// The same through registers, at any width and alignment.
-template <typename T, bool KC, int B, int WAVES>
+// The same through registers, at any width and alignment.  Steps ahead of the
+// last one load whole packs: a tile row (KC) that does not exist repeats the
+// last one, and a pack of columns (KS) that crosses the end of its row reads
+// on into the next, which exists; both only reach outputs that are not
+// stored.  The last step, and every step of rows below a pack, loads exactly
+// the elements that exist.
+template <typename T, bool KC, int B, int WAVES, bool WHOLE>
 __device__ inline void fetch(const Operand<T> &o, int64_t k0, Pack<T> (&r)[B * kChunks / (WAVES * kWave)]) {
     constexpr int kPerRow = KC ? kStepBytes / 16 : B * (int)sizeof(T) / 16;
 #pragma unroll
     for (int i = 0; i < B * kChunks / (WAVES * kWave); ++i) {
         const int idx = threadIdx.x + i * WAVES * kWave, row = idx / kPerRow, c = idx % kPerRow * kPack<T>;
-        const int64_t out = KC ? row : k0 + row, in = KC ? k0 + c : c;
-        const int64_t n = out < o.outer ? o.inner - in : 0;
-        r[i] = load_pack(o.ptr + out * o.ld + in, n);
+        if constexpr (WHOLE) {
+            const int64_t out = KC ? min(int64_t(row), o.outer - 1) : k0 + row;
+            const int64_t in = KC ? k0 + c : min(int64_t(c), o.inner - 1);
+            r[i] = load_pack(o.ptr + out * o.ld + in);
+        } else {
+            const int64_t out = KC ? row : k0 + row, in = KC ? k0 + c : c;
+            const int64_t n = out < o.outer ? o.inner - in : 0;
+            r[i] = load_pack(o.ptr + out * o.ld + in, n);
+        }
     }
 }
 
@@ -355,9 +366,16 @@ __device__ inline void tile_product(const Stages &lds, const Operand<T> &a, cons
         constexpr int kRegA = S::BM * kChunks / S::kThreads, kRegB = S::BN * kChunks / S::kThreads;
         Pack<T> ra[kRegA], rb[kRegB];
         Operands set;
+        const int whole = a.ld >= kPack<T> && b.ld >= kPack<T> ? steps - 1 : 0;
         auto fetch_step = [&](int t) {
-            fetch<T, AKC, S::BM, S::kWaves>(a, (int64_t)t * kStep<T>, ra);
-            fetch<T, BKC, S::BN, S::kWaves>(b, (int64_t)t * kStep<T>, rb);
+            const int64_t k0 = (int64_t)t * kStep<T>;
+            if (t < whole) {
+                fetch<T, AKC, S::BM, S::kWaves, true>(a, k0, ra);
+                fetch<T, BKC, S::BN, S::kWaves, true>(b, k0, rb);
+            } else {
+                fetch<T, AKC, S::BM, S::kWaves, false>(a, k0, ra);
+                fetch<T, BKC, S::BN, S::kWaves, false>(b, k0, rb);
+            }
         };
         auto put_step = [&](LdsByte *to) {
             put<T, AKC, S::BM, S::kWaves>(to, ra);
@@ -441,59 +459,72 @@ __device__ inline int64_t run_bound(const SegmentArgs &a, int64_t i) {
     return b < 0 ? 0 : b > a.R ? a.R : b;
 }
 
-// Tile number `tile` of the runs [v0, v1), each cut into tiles of `len` rows:
-// its run, first row, and end of the run; run < 0: there is no such tile.
-// Every wave finds it by itself: 64 runs at a time, a scan of their tiles.
-struct RowTile {
-    int64_t run, row, end;
-};
-
-__device__ inline RowTile find_tile(const SegmentArgs &a, int64_t v0, int64_t v1, int64_t len, int64_t tile) {
-    const int lane = threadIdx.x & (kWave - 1);
-    RowTile t = {-1, 0, 0};
-    for (; v0 < v1; v0 += kWave) {
-        const int64_t v = v0 + lane;
-        const int64_t lo = v < v1 ? run_bound(a, v) : 0, hi = v < v1 ? run_bound(a, v + 1) : 0;
-        const int mine = hi > lo ? (int)((uint32_t)(hi - lo + len - 1) / (uint32_t)len) : 0;
-        int64_t incl = mine;
-#pragma unroll
-        for (int o = 1; o < kWave; o <<= 1) {
-            const int64_t up = __shfl_up(incl, o, kWave);
-            if (lane >= o) incl += up;
-        }
-        const uint64_t past = __ballot(incl > tile);
-        if (past) {
-            const int at = __ffsll((unsigned long long)past) - 1;
-            t.run = v0 + at;
-            t.row = __shfl(lo, at, kWave) + (tile - __shfl(incl - mine, at, kWave)) * len;
-            t.end = __shfl(hi, at, kWave);
-            break;
-        }
-        tile -= __shfl(incl, kWave - 1, kWave);
-    }
-    t.run = uniform(t.run);
-    t.row = uniform(t.row);
-    t.end = uniform(t.end);
-    return t;
-}
-
-// Tiles of the runs [v0, v1) together.
-__device__ inline int64_t count_tiles(const SegmentArgs &a, int64_t v0, int64_t v1, int64_t len) {
-    int64_t sum = 0;
-    for (int64_t v = v0 + (threadIdx.x & (kWave - 1)); v < v1; v += kWave) {
-        const int64_t lo = run_bound(a, v), hi = run_bound(a, v + 1);
-        if (hi > lo) sum += (hi - lo + len - 1) / len;
-    }
-#pragma unroll
-    for (int o = kWave / 2; o > 0; o >>= 1) sum += __shfl_xor(sum, o, kWave);
-    return uniform(sum);
-}
-
 // Blocks are dealt to the 8 XCDs in turn: give each XCD a run of consecutive
 // tiles, whose operands then meet in one L2.
 __device__ inline int64_t xcd_order(int64_t id, int64_t total) {
     const int64_t per = total / 8, extra = total % 8, x = id % 8, at = id / 8;
     return x * per + (x < extra ? x : extra) + at;
+}
+
+// Tiles of the runs [v0, v1), each cut into pieces of `len` rows and `cols`
+// tiles to a piece: the piece and column tile of tile number `id`, numbered
+// so that each XCD gets a run of them; run < 0: there are fewer tiles.  Every
+// wave finds its tile by itself: 64 runs at a time, a scan of their pieces.
+struct RowTile {
+    int64_t run, row, end, piece, col;
+};
+
+__device__ inline int64_t pieces_of(const SegmentArgs &a, int64_t v, int64_t v1, int64_t len, int64_t *lo, int64_t *hi) {
+    *lo = v < v1 ? run_bound(a, v) : 0;
+    *hi = v < v1 ? run_bound(a, v + 1) : 0;
+    return *hi > *lo ? (uint32_t)(*hi - *lo + len - 1) / (uint32_t)len : 0;
+}
+
+__device__ inline int64_t wave_inclusive(int64_t v) {
+    const int lane = threadIdx.x & (kWave - 1);
+#pragma unroll
+    for (int o = 1; o < kWave; o <<= 1) {
+        const int64_t up = __shfl_up(v, o, kWave);
+        if (lane >= o) v += up;
+    }
+    return v;
+}
+
+// Pieces of the runs [v0, v1) together.
+__device__ inline int64_t count_pieces(const SegmentArgs &a, int64_t v0, int64_t v1, int64_t len) {
+    int64_t sum = 0, lo, hi;
+    for (; v0 < v1; v0 += kWave) sum += pieces_of(a, v0 + (threadIdx.x & (kWave - 1)), v1, len, &lo, &hi);
+#pragma unroll
+    for (int o = kWave / 2; o > 0; o >>= 1) sum += __shfl_xor(sum, o, kWave);
+    return uniform(sum);
+}
+
+__device__ inline RowTile find_tile(const SegmentArgs &a, int64_t v0, int64_t v1, int64_t len, int64_t cols, int64_t id) {
+    const int lane = threadIdx.x & (kWave - 1);
+    RowTile t = {-1, 0, 0, 0, 0};
+    int64_t lo, hi, mine = pieces_of(a, v0 + lane, v1, len, &lo, &hi), incl = wave_inclusive(mine);
+    const int64_t first = __shfl(incl, kWave - 1, kWave);
+    const int64_t total = uniform(v1 - v0 <= kWave ? first : first + count_pieces(a, v0 + kWave, v1, len)) * cols;
+    if (id >= total) return t;
+    const int64_t at = xcd_order(id, total);
+    t.piece = at / cols;
+    t.col = at % cols;
+    int64_t piece = t.piece;
+    for (;;) {
+        const uint64_t past = __ballot(incl > piece);
+        if (past) {
+            const int l = __ffsll((unsigned long long)past) - 1;
+            t.run = uniform(v0 + l);
+            t.row = uniform(__shfl(lo, l, kWave) + (piece - __shfl(incl - mine, l, kWave)) * len);
+            t.end = uniform(__shfl(hi, l, kWave));
+            return t;
+        }
+        piece -= __shfl(incl, kWave - 1, kWave);
+        v0 += kWave;
+        if (v0 >= v1) return t;
+        mine = pieces_of(a, v0 + lane, v1, len, &lo, &hi);
+        incl = wave_inclusive(mine);
+    }
 }
 
 template <typename T, typename S, bool TRANSPOSED, bool DIRECT>
@@ -502,12 +533,11 @@ __global__ __launch_bounds__(S::kThreads) void segment_kernel(SegmentArgs a, int
     const int64_t K = TRANSPOSED ? a.O : a.I, N = TRANSPOSED ? a.I : a.O;
     const T *in = (const T *)(TRANSPOSED ? a.dy : a.x), *w = (const T *)a.w;
     for (int64_t id = blockIdx.x; id < total; id += gridDim.x) {
-        const int64_t t = xcd_order(id, total), n0 = t % col_tiles * S::BN;
-        const RowTile rt = find_tile(a, 0, a.E + 2, S::BM, t / col_tiles);
-        if (rt.run < 0) continue;
-        const int64_t run = rt.run, row = rt.row;
+        const RowTile rt = find_tile(a, 0, a.E + 2, S::BM, col_tiles, id);
+        if (rt.run < 0) return;
+        const int64_t run = uniform(rt.run), row = uniform(rt.row), n0 = rt.col * S::BN;
         T *out = (T *)a.y + row * N + n0;
-        const int64_t rows = rt.end - row;
+        const int64_t rows = uniform(rt.end) - row;
         if (run == 0 || run > a.E) {
             tile_zero<T, S>(out, N, rows, N - n0);
             continue;
@@ -557,22 +587,23 @@ __global__ __launch_bounds__(S::kThreads) void segment_dw_kernel(SegmentArgs a, 
                                                                  int64_t col_tiles, int64_t chunk, int64_t total) {
     SEGMENT_STAGES(lds, S::kStageBytes);
     for (int64_t id = blockIdx.x; id < total; id += gridDim.x) {
-        int64_t t = chunk ? xcd_order(id, total) : id;
-        const int64_t n0 = t % col_tiles * S::BN;
-        t /= col_tiles;
-        const int64_t m0 = t % row_tiles * S::BM;
-        t /= row_tiles;
-        int64_t row, end;
+        const int64_t tiles = row_tiles * col_tiles;
+        int64_t t, at, row, end;
         if (chunk) {
-            const RowTile rt = find_tile(a, 1, a.E + 1, chunk, t);
-            if (rt.run < 0) continue;
-            row = rt.row;
-            end = min(rt.end, row + chunk);
+            const RowTile rt = find_tile(a, 1, a.E + 1, chunk, tiles, id);
+            if (rt.run < 0) return;
+            t = rt.piece;
+            at = rt.col;
+            row = uniform(rt.row);
+            end = min(uniform(rt.end), row + chunk);
         } else {
+            t = id / tiles;
+            at = id % tiles;
             if (a.E <= kWave) t = max(int64_t(0), segment_by_length(a, (int)t));
             row = run_bound(a, t + 1);
             end = max(row, run_bound(a, t + 2));
         }
+        const int64_t m0 = at / col_tiles * S::BM, n0 = at % col_tiles * S::BN;
         Operand<T> A, B;
         A.ptr = (const T *)a.x + row * a.I + m0;
         A.ld = a.I;
@@ -597,7 +628,7 @@ template <typename T>
 __global__ __launch_bounds__(kFoldThreads) void segment_fold_kernel(SegmentArgs a, int64_t chunk) {
     const int64_t n = a.I * a.O;
     for (int64_t e = blockIdx.y; e < a.E; e += gridDim.y) {
-        const int64_t first = count_tiles(a, 1, e + 1, chunk), parts = count_tiles(a, e + 1, e + 2, chunk);
+        const int64_t first = count_pieces(a, 1, e + 1, chunk), parts = count_pieces(a, e + 1, e + 2, chunk);
         const float *from = a.partial + first * n;
         for (int64_t i = (int64_t)blockIdx.x * kFoldThreads + threadIdx.x; i < n;
              i += (int64_t)gridDim.x * kFoldThreads) {
@@ -623,7 +654,8 @@ bool direct_rows(const void *p, int64_t width, int size) {
 // 256 x 256 tiles when there are enough of them to fill the chip.
 bool large_tiles(int64_t tiles, int size, bool direct) { return direct && size == 2 && tiles >= 2 * kUnits; }
 
-// dw: whole segments when their tiles fill the chip twice; else chunks of
+// dw: whole segments when their tiles fill the chip twice or there are few
+// rows (then one long segment costs less than the partial sums); else chunks of
 // rows, about four tiles of work for each compute unit and at least 256
 // elements of the summed index, so that unequal segments cost no balance.
 struct DwShape {
@@ -640,7 +672,7 @@ DwShape dw_shape(int64_t R, int64_t E, int64_t I, int64_t O, int size, bool dire
     d.col_tiles = tiles_of(O, tile);
     const int64_t tiles = d.row_tiles * d.col_tiles, want = std::max<int64_t>(1, 4 * kUnits / tiles);
     d.chunk = d.chunks = 0;
-    if (E * tiles >= 2 * kUnits || R <= 256) return d;
+    if (E * tiles >= 2 * kUnits || R <= 4096) return d;
     d.chunk = std::max<int64_t>(256, (R + want - 1) / want);
     d.chunk = (d.chunk + 31) / 32 * 32;
     d.chunks = R / d.chunk + E;
