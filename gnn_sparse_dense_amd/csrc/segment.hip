@@ -528,7 +528,7 @@ __device__ inline RowTile find_tile(const SegmentArgs &a, int64_t v0, int64_t v1
 }
 
 template <typename T, typename S, bool TRANSPOSED, bool DIRECT>
-__global__ __launch_bounds__(S::kThreads) void segment_kernel(SegmentArgs a, int64_t col_tiles, int64_t total) {
+__global__ __launch_bounds__(S::kThreads, 2) void segment_kernel(SegmentArgs a, int64_t col_tiles, int64_t total) {
     SEGMENT_STAGES(lds, S::kStageBytes);
     const int64_t K = TRANSPOSED ? a.O : a.I, N = TRANSPOSED ? a.I : a.O;
     const T *in = (const T *)(TRANSPOSED ? a.dy : a.x), *w = (const T *)a.w;
@@ -583,7 +583,7 @@ __device__ inline int64_t segment_by_length(const SegmentArgs &a, int rank) {
 // segment's rows, tile of [I, O]) into fp32 partial sums, one [I, O] for each
 // chunk in the order of the segments.
 template <typename T, typename OUT, typename S, bool DIRECT>
-__global__ __launch_bounds__(S::kThreads) void segment_dw_kernel(SegmentArgs a, OUT *dst, int64_t row_tiles,
+__global__ __launch_bounds__(S::kThreads, 2) void segment_dw_kernel(SegmentArgs a, OUT *dst, int64_t row_tiles,
                                                                  int64_t col_tiles, int64_t chunk, int64_t total) {
     SEGMENT_STAGES(lds, S::kStageBytes);
     for (int64_t id = blockIdx.x; id < total; id += gridDim.x) {

@@ -89,7 +89,7 @@ def plain_route(e, E):
 @pytest.mark.parametrize("T,k,E,kind", [
     (0, 2, 4, "all"), (0, 1, 2048, "all"), (1, 1, 1, "all"), (1, 3, 2, "some"), (63, 1, 8, "all"), (64, 2, 8, "all"),
     (65, 2, 511, "some"), (512, 2, 511, "all"), (513, 2, 7, "some"), (1024, 4, 64, "one"), (1365, 3, 64, "some"),
-    (4097, 1, 100, "all"), (2048, 8, 16, "none"), (16384, 1, 511, "some"), (16385, 1, 511, "some"),
+    (4096, 1, 511, "some"), (4097, 1, 100, "all"), (2048, 8, 16, "none"), (16384, 1, 511, "some"), (16385, 1, 511, "some"),
     (300, 2, 512, "all"), (5000, 2, 2048, "some"), (40000, 3, 33, "some"), (70001, 8, 255, "all"),
     (300007, 2, 3, "one"), (1100000, 4, 129, "some")])
 def test_route(T, k, E, kind):

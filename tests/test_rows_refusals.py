@@ -23,8 +23,8 @@ def bytes_of(call, *sizes):
 
 def test_workspaces():
     assert bytes_of("spmm_route_workspace", 0, 8) == 0
-    assert bytes_of("spmm_route_workspace", 16384, 511) == 0          # one block holds it
-    assert bytes_of("spmm_route_workspace", 16385, 511) > 0
+    assert bytes_of("spmm_route_workspace", 4096, 511) == 0          # one block holds it
+    assert bytes_of("spmm_route_workspace", 4097, 511) > 0
     assert bytes_of("spmm_route_workspace", 0, 2048) > 0
     assert bytes_of("spmm_segment_workspace", 0, 4, 8, 8, G.SPMM_BF16) == 0
     assert bytes_of("spmm_segment_workspace", 10 ** 6, 4, 64, 64, G.SPMM_F32) % (4 * 4 * 64 * 64) == 0
