@@ -107,16 +107,24 @@ def spmm_route_dispatch(route: "RowRoute", x, xs, weight=None, stream=None) -> N
     """xs [T * k, N] = rows of x [T, N] in expert order (times weight [T, k])."""
     kind, wkind = _check_exchange(route, "x", x, route.T, weight)
     _check_tensor("xs", xs, (x.dtype,), (route.T * route.k, x.shape[1]), route.device)
-    _check(_lib.spmm_route_dispatch(_ptr(route.offsets), _ptr(route.order), route.T, route.k, route.E, _ptr(x),
-                                    _ptr(weight), wkind, _ptr(xs), x.shape[1], kind, _stream(x, stream)))
+    _dispatch(route, x, xs, weight, wkind, kind, _stream(x, stream))
+
+
+def _dispatch(route, x, xs, weight, wkind, kind, stream):
+    _check(_lib.spmm_route_dispatch(route.offsets.data_ptr(), route.order.data_ptr(), route.T, route.k, route.E,
+                                    x.data_ptr(), _ptr(weight), wkind, xs.data_ptr(), x.shape[1], kind, stream))
 
 
 def spmm_route_combine(route: "RowRoute", rows, weight, out, stream=None) -> None:
     """out [T, N] = the rows [T * k, N] summed back (weight [T, k] or None: 1)."""
     kind, wkind = _check_exchange(route, "rows", rows, route.T * route.k, weight)
     _check_tensor("out", out, (rows.dtype,), (route.T, rows.shape[1]), route.device)
-    _check(_lib.spmm_route_combine(_ptr(route.offsets), _ptr(route.position), route.T, route.k, route.E, _ptr(rows),
-                                   _ptr(weight), wkind, _ptr(out), rows.shape[1], kind, _stream(rows, stream)))
+    _combine(route, rows, weight, wkind, out, kind, _stream(rows, stream))
+
+
+def _combine(route, rows, weight, wkind, out, kind, stream):
+    _check(_lib.spmm_route_combine(route.offsets.data_ptr(), route.position.data_ptr(), route.T, route.k, route.E,
+                                   rows.data_ptr(), _ptr(weight), wkind, out.data_ptr(), rows.shape[1], kind, stream))
 
 
 def spmm_route_combine_backward(route: "RowRoute", rows, weight, dout, drows, dweight, stream=None) -> None:
@@ -133,9 +141,13 @@ def spmm_route_combine_backward(route: "RowRoute", rows, weight, dout, drows, dw
         types = (torch.float32, dout.dtype) if weight is None else (weight.dtype,)
         _check_tensor("dweight", dweight, types, (route.T, route.k), route.device)
         wkind = _TYPES[dweight.dtype]
-    _check(_lib.spmm_route_combine_backward(_ptr(route.offsets), _ptr(route.order), route.T, route.k, route.E,
-                                            _ptr(rows), _ptr(weight), wkind, _ptr(dout), _ptr(drows), _ptr(dweight),
-                                            dout.shape[1], kind, _stream(dout, stream)))
+    _combine_backward(route, rows, weight, wkind, dout, drows, dweight, kind, _stream(dout, stream))
+
+
+def _combine_backward(route, rows, weight, wkind, dout, drows, dweight, kind, stream):
+    _check(_lib.spmm_route_combine_backward(route.offsets.data_ptr(), route.order.data_ptr(), route.T, route.k,
+                                            route.E, _ptr(rows), _ptr(weight), wkind, dout.data_ptr(), _ptr(drows),
+                                            _ptr(dweight), dout.shape[1], kind, stream))
 
 
 def _check_segment(rows_name, rows, width, dtype, offsets, R, E, device):
@@ -151,8 +163,8 @@ def spmm_segment_product(x, w, offsets, y, stream=None) -> None:
     _check_tensor("w", w, (x.dtype,), w.shape, x.device)
     _check_segment("x", x, I, x.dtype, offsets, x.shape[0], E, x.device)
     _check_tensor("y", y, (x.dtype,), (x.shape[0], O), x.device)
-    _check(_lib.spmm_segment_product(_ptr(x), _ptr(w), _ptr(offsets), _ptr(y), x.shape[0], E, I, O, kind,
-                                     _stream(x, stream)))
+    _check(_lib.spmm_segment_product(x.data_ptr(), w.data_ptr(), offsets.data_ptr(), y.data_ptr(), x.shape[0], E, I,
+                                     O, kind, _stream(x, stream)))
 
 
 def spmm_segment_product_dx(dy, w, offsets, dx, stream=None) -> None:
@@ -163,8 +175,12 @@ def spmm_segment_product_dx(dy, w, offsets, dx, stream=None) -> None:
     _check_tensor("w", w, (dy.dtype,), w.shape, dy.device)
     _check_segment("dy", dy, O, dy.dtype, offsets, dy.shape[0], E, dy.device)
     _check_tensor("dx", dx, (dy.dtype,), (dy.shape[0], I), dy.device)
-    _check(_lib.spmm_segment_product_dx(_ptr(dy), _ptr(w), _ptr(offsets), _ptr(dx), dy.shape[0], E, I, O, kind,
-                                        _stream(dy, stream)))
+    _product_dx(dy, w.data_ptr(), offsets, dx, (E, I, O), kind, _stream(dy, stream))
+
+
+def _product_dx(dy, w, offsets, dx, shape, kind, stream):
+    _check(_lib.spmm_segment_product_dx(dy.data_ptr(), w, offsets.data_ptr(), dx.data_ptr(), dy.shape[0], *shape,
+                                        kind, stream))
 
 
 def spmm_segment_product_dw(x, dy, offsets, dw, stream=None) -> None:
@@ -175,9 +191,13 @@ def spmm_segment_product_dw(x, dy, offsets, dw, stream=None) -> None:
     _check_tensor("dw", dw, (x.dtype,), dw.shape, x.device)
     _check_segment("x", x, I, x.dtype, offsets, x.shape[0], E, x.device)
     _check_tensor("dy", dy, (x.dtype,), (x.shape[0], O), x.device)
-    ws, at, n = _workspace(x.device, "spmm_segment_workspace", x.shape[0], E, I, O, kind)
-    _check(_lib.spmm_segment_product_dw(_ptr(x), _ptr(dy), _ptr(offsets), _ptr(dw), x.shape[0], E, I, O, kind, at, n,
-                                        _stream(x, stream)))
+    _product_dw(x, dy, offsets, dw, kind, _stream(x, stream))
+
+
+def _product_dw(x, dy, offsets, dw, kind, stream):
+    ws, at, n = _workspace(x.device, "spmm_segment_workspace", x.shape[0], *dw.shape, kind)
+    _check(_lib.spmm_segment_product_dw(x.data_ptr(), dy.data_ptr(), offsets.data_ptr(), dw.data_ptr(), x.shape[0],
+                                        *dw.shape, kind, at, n, stream))
 
 
 def _check_norm(x, weight, bias):
@@ -222,11 +242,17 @@ def spmm_layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, stre
             _check_tensor(name, t, types, (N,), x.device)
             wkind = _TYPES[t.dtype]
             types = (t.dtype,)
+    _norm_backward(dy, x, weight, wkind, mean.data_ptr(), rstd.data_ptr(), dx, dweight, dbias, kind,
+                   _stream(x, stream))
+
+
+def _norm_backward(dy, x, weight, wkind, mean, rstd, dx, dweight, dbias, kind, stream):
+    R, N = x.shape
     ws, at, n = None, None, 0
     if dweight is not None or dbias is not None:
         ws, at, n = _workspace(x.device, "spmm_layer_norm_workspace", R, N, kind)
-    _check(_lib.spmm_layer_norm_backward(_ptr(dy), _ptr(x), _ptr(weight), wkind, _ptr(mean), _ptr(rstd), _ptr(dx),
-                                         _ptr(dweight), _ptr(dbias), R, N, kind, at, n, _stream(x, stream)))
+    _check(_lib.spmm_layer_norm_backward(dy.data_ptr(), x.data_ptr(), _ptr(weight), wkind, mean, rstd, _ptr(dx),
+                                         _ptr(dweight), _ptr(dbias), R, N, kind, at, n, stream))
 
 
 # ------------------------------------------------------- differentiable calls
@@ -269,6 +295,10 @@ class RowRoute:
                _current_stream(self.offsets))
 
 
+# The backward functions call the library on tensors that the forward pass
+# checked or that they allocate: dy has the forward output's shape, type and
+# device by autograd's own rules.
+
 class _Dispatch(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, route):
@@ -281,8 +311,10 @@ class _Dispatch(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dxs):
         route = ctx.route
+        dxs = dxs.contiguous()
         dx = dxs.new_empty((route.T, dxs.shape[1]))
-        spmm_route_combine(route, dxs.contiguous(), None, dx)
+        kind = _TYPES[dxs.dtype]
+        _combine(route, dxs, None, kind, dx, kind, _current_stream(dxs))
         return dx, None
 
 
@@ -319,11 +351,13 @@ class _Combine(torch.autograd.Function):
         drows = dweight = None
         if ctx.needs_input_grad[0]:
             drows = dout.new_empty((route.T * route.k, dout.shape[1]))
+        kind, stream = _TYPES[dout.dtype], _current_stream(dout)
+        wkind = kind if weight is None else _TYPES[weight.dtype]
         if ctx.needs_input_grad[1]:
             dweight = torch.empty_like(weight)
-            spmm_route_combine_backward(route, rows, weight, dout, drows, dweight)
+            _combine_backward(route, rows, weight, wkind, dout, drows, dweight, kind, stream)
         elif drows is not None:
-            spmm_route_dispatch(route, dout, drows, weight)
+            _dispatch(route, dout, drows, weight, wkind, kind, stream)
         return drows, dweight, None
 
 
@@ -356,13 +390,14 @@ class _SegmentMatmul(torch.autograd.Function):
     def backward(ctx, dy):
         x, w, offsets = ctx.saved_tensors
         dy = dy.contiguous()
+        kind, stream = _TYPES[dy.dtype], _current_stream(dy)
         dx = dw = None
         if ctx.needs_input_grad[0]:
             dx = dy.new_empty((dy.shape[0], ctx.shape[1]))
-            spmm_segment_product_dx(dy, w, offsets, dx)
+            _product_dx(dy, w.data_ptr(), offsets, dx, ctx.shape, kind, stream)
         if ctx.needs_input_grad[1]:
             dw = dy.new_empty(ctx.shape)
-            spmm_segment_product_dw(x, dy, offsets, dw)
+            _product_dw(x, dy, offsets, dw, kind, stream)
         return dx, dw, None
 
 
@@ -386,23 +421,29 @@ class _LayerNorm(torch.autograd.Function):
         x = x.contiguous()
         weight = None if weight is None else weight.contiguous()
         bias = None if bias is None else bias.contiguous()
+        kind, wkind = _check_norm(x, weight, bias)
+        R, N = x.shape
         y = torch.empty_like(x)
-        mean = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
-        rstd = torch.empty_like(mean)
-        spmm_layer_norm(x, weight, bias, y, mean, rstd, eps)
-        ctx.save_for_backward(x, weight, mean, rstd)
-        ctx.bias_dtype = None if bias is None else bias.dtype
+        stats = torch.empty((2, R), dtype=torch.float32, device=x.device)       # mean, rstd
+        at = stats.data_ptr()
+        _check(_lib.spmm_layer_norm(x.data_ptr(), _ptr(weight), _ptr(bias), wkind, y.data_ptr(), at,
+                                    at + 4 * R if at else None, R, N, float(eps), kind, _current_stream(x)))
+        ctx.save_for_backward(x, weight, stats)
+        ctx.types = kind, wkind, None if bias is None else bias.dtype
         return y
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy):
-        x, weight, mean, rstd = ctx.saved_tensors
+        x, weight, stats = ctx.saved_tensors
+        kind, wkind, bias_dtype = ctx.types
         need_x, need_w, need_b = ctx.needs_input_grad[:3]
         dx = torch.empty_like(x) if need_x else None
         dweight = torch.empty_like(weight) if need_w else None
-        dbias = torch.empty(x.shape[1], dtype=ctx.bias_dtype, device=x.device) if need_b else None
-        spmm_layer_norm_backward(dy.contiguous(), x, weight, mean, rstd, dx, dweight, dbias)
+        dbias = torch.empty(x.shape[1], dtype=bias_dtype, device=x.device) if need_b else None
+        mean = stats.data_ptr()
+        _norm_backward(dy.contiguous(), x, weight, wkind, mean, mean + 4 * x.shape[0], dx, dweight, dbias, kind,
+                       _current_stream(x))
         return dx, dweight, dbias, None
 
 
