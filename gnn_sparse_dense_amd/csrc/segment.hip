@@ -222,7 +222,7 @@ struct Reader {
                 at[i] = k * B * 2 + ((piece ^ ((k & 3) << 1)) << 5) + ((l & 3) << 3);
             }
         } else {
-            at[0] = half * 4 * B * 4 + m * 4;
+at[0] = half * 4 * B * 4 + m * 4;
         }
 #pragma unroll
         for (int &o : at) asm volatile("" : "+v"(o));
@@ -296,7 +296,7 @@ struct Stages {
 // out[0..rows) x [0..cols) of a tile = A . B over K summed elements.
 template <typename T, typename OUT, typename S, bool AKC, bool BKC, bool DIRECT>
 __device__ inline void tile_product(const Stages &lds, const Operand<T> &a, const Operand<T> &b, int64_t K, OUT *out,
-                                    int64_t ldo, int64_t rows, int64_t cols) {
+                                    int64_t ldo, int64_t rows, int64_t cols, bool stream) {
     constexpr int MI = S::MI, NI = S::NI, kA = S::BM * kStepBytes;
     const int wave = uniform((int)threadIdx.x / kWave);
     const int m0 = wave / S::WC * (MI * 32), n0 = wave % S::WC * (NI * 32);
@@ -404,8 +404,9 @@ __device__ inline void tile_product(const Stages &lds, const Operand<T> &a, cons
     // covers whole rows of the tile: a lane holds 4 columns of one row, and 32
     // rows to a store would reach the L2 as 16-byte pieces.  Chunk c of row r
     // stands at c ^ r.
-    constexpr int kRow = S::BN * (int)sizeof(OUT), kRowChunks = kRow / 16, kStageRows = S::kStageBytes / kRow;
-    static_assert(kStages * kStageRows >= S::BM && kStageRows % 32 == 0, "the stages hold the tile");
+    constexpr int kRow = S::BN * (int)sizeof(OUT), kRowChunks = kRow / 16;
+    constexpr int kStageRows = S::kStageBytes / kRow / 32 * 32;
+    static_assert(kStages * kStageRows >= S::BM, "the stages hold the tile");
     int thread = threadIdx.x;
     asm volatile("" : "+v"(thread));                 // addresses of the stores are not kept through the loop
     const int lane = thread & (kWave - 1);
@@ -440,7 +441,9 @@ __device__ inline void tile_product(const Stages &lds, const Operand<T> &a, cons
         const int r = r0 + thread / kRowChunks;
         const auto o = lds_load<Pack<OUT>>(lds.at[r0 / kStageRows] + r % kStageRows * kRow +
                                            ((chunk ^ (r & (kRowChunks - 1))) << 4));
-        if (r < rows) store_pack(out + r * ldo + c, o, cols - c);
+        if (r >= rows) continue;
+        if (stream) store_pack_stream(out + r * ldo + c, o, cols - c);
+        else store_pack(out + r * ldo + c, o, cols - c);
     }
 }
 
@@ -528,7 +531,8 @@ __device__ inline RowTile find_tile(const SegmentArgs &a, int64_t v0, int64_t v1
 }
 
 template <typename T, typename S, bool TRANSPOSED, bool DIRECT>
-__global__ __launch_bounds__(S::kThreads, 2) void segment_kernel(SegmentArgs a, int64_t col_tiles, int64_t total) {
+__global__ __launch_bounds__(S::kThreads, 2) void segment_kernel(SegmentArgs a, int64_t col_tiles, int64_t total,
+                                                                bool stream) {
     SEGMENT_STAGES(lds, S::kStageBytes);
     const int64_t K = TRANSPOSED ? a.O : a.I, N = TRANSPOSED ? a.I : a.O;
     const T *in = (const T *)(TRANSPOSED ? a.dy : a.x), *w = (const T *)a.w;
@@ -562,7 +566,7 @@ __global__ __launch_bounds__(S::kThreads, 2) void segment_kernel(SegmentArgs a, 
             B.inner = N - n0;
         }
         __syncthreads();
-        tile_product<T, T, S, true, TRANSPOSED, DIRECT>(lds, A, B, K, out, N, rows, N - n0);
+        tile_product<T, T, S, true, TRANSPOSED, DIRECT>(lds, A, B, K, out, N, rows, N - n0, stream);
     }
 }
 
@@ -584,7 +588,8 @@ __device__ inline int64_t segment_by_length(const SegmentArgs &a, int rank) {
 // chunk in the order of the segments.
 template <typename T, typename OUT, typename S, bool DIRECT>
 __global__ __launch_bounds__(S::kThreads, 2) void segment_dw_kernel(SegmentArgs a, OUT *dst, int64_t row_tiles,
-                                                                 int64_t col_tiles, int64_t chunk, int64_t total) {
+                                                                 int64_t col_tiles, int64_t chunk, int64_t total,
+                                                                 bool stream) {
     SEGMENT_STAGES(lds, S::kStageBytes);
     for (int64_t id = blockIdx.x; id < total; id += gridDim.x) {
         const int64_t tiles = row_tiles * col_tiles;
@@ -617,7 +622,7 @@ __global__ __launch_bounds__(S::kThreads, 2) void segment_dw_kernel(SegmentArgs 
         B.end = (const T *)a.dy + a.R * a.O;
         __syncthreads();
         tile_product<T, OUT, S, false, false, DIRECT>(lds, A, B, end - row, dst + (t * a.I + m0) * a.O + n0, a.O,
-                                                      a.I - m0, a.O - n0);
+                                                      a.I - m0, a.O - n0, stream);
     }
 }
 
@@ -645,6 +650,16 @@ int64_t tiles_of(int64_t n, int tile) { return (n + tile - 1) / tile; }
 constexpr int64_t kMaxBlocks = 1 << 20;
 constexpr int64_t kUnits = 256;                      // compute units
 
+// Non-temporal stores where a call moves more than half of the 256 MB Infinity
+// Cache (65,536 x 1024 x 2048 bf16: 334 -> 289 us; 256 summed elements: 178 ->
+// 115 us): the operands that other tiles read again stay there.
+constexpr int64_t kStreamBytes = int64_t(128) << 20;
+
+template <typename T>
+bool streams(const SegmentArgs &a) {
+    return (a.R * (a.I + a.O) + a.E * a.I * a.O) * (int64_t)sizeof(T) > kStreamBytes;
+}
+
 // The copy into LDS needs rows of whole 16-byte groups, from a 16-byte
 // address, and 32-bit offsets within a tile's rows.
 bool direct_rows(const void *p, int64_t width, int size) {
@@ -656,8 +671,10 @@ bool large_tiles(int64_t tiles, int size, bool direct) { return direct && size =
 
 // dw: whole segments when their tiles fill the chip twice or there are few
 // rows (then one long segment costs less than the partial sums); else chunks of
-// rows, about four tiles of work for each compute unit and at least 256
-// elements of the summed index, so that unequal segments cost no balance.
+// rows, about two tiles of work for each compute unit (150,001 fp32 rows of 7
+// segments, 128 x 256: 110 us with the sums' 11; with four 131 and 19 us) and at
+// least 256 elements of the summed index, so that unequal segments cost no
+// balance.
 struct DwShape {
     bool large;
     int64_t row_tiles, col_tiles;
@@ -670,7 +687,7 @@ DwShape dw_shape(int64_t R, int64_t E, int64_t I, int64_t O, int size, bool dire
     const int tile = d.large ? 256 : 128;
     d.row_tiles = tiles_of(I, tile);
     d.col_tiles = tiles_of(O, tile);
-    const int64_t tiles = d.row_tiles * d.col_tiles, want = std::max<int64_t>(1, 4 * kUnits / tiles);
+    const int64_t tiles = d.row_tiles * d.col_tiles, want = std::max<int64_t>(1, 2 * kUnits / tiles);
     d.chunk = d.chunks = 0;
     if (E * tiles >= 2 * kUnits || R <= 4096) return d;
     d.chunk = std::max<int64_t>(256, (R + want - 1) / want);
@@ -685,8 +702,9 @@ hipError_t segment_launch(const SegmentArgs &a, bool transposed, hipStream_t s) 
     const int64_t row_tiles = a.R / S::BM + a.E + 2, col_tiles = tiles_of(transposed ? a.I : a.O, S::BN);
     const int64_t total = row_tiles * col_tiles;
     const unsigned blocks = (unsigned)std::min(total, kMaxBlocks);
-    if (transposed) segment_kernel<T, S, true, DIRECT><<<blocks, S::kThreads, 0, s>>>(a, col_tiles, total);
-    else segment_kernel<T, S, false, DIRECT><<<blocks, S::kThreads, 0, s>>>(a, col_tiles, total);
+    const bool stream = streams<T>(a);
+    if (transposed) segment_kernel<T, S, true, DIRECT><<<blocks, S::kThreads, 0, s>>>(a, col_tiles, total, stream);
+    else segment_kernel<T, S, false, DIRECT><<<blocks, S::kThreads, 0, s>>>(a, col_tiles, total, stream);
     return hipGetLastError();
 }
 
@@ -706,19 +724,20 @@ template <typename T, typename OUT>
 hipError_t segment_dw_launch(const SegmentArgs &a, OUT *dst, const DwShape &d, bool direct, hipStream_t s) {
     const int64_t total = (d.chunk ? d.chunks : a.E) * d.row_tiles * d.col_tiles;
     const unsigned blocks = (unsigned)std::min(total, kMaxBlocks);
+    const bool stream = d.chunk == 0 && streams<T>(a);       // partial sums are read again at once
     if constexpr (sizeof(T) == 2 && __is_same(T, OUT)) {       // large tiles take whole segments
         if (d.large) {
             segment_dw_kernel<T, OUT, Large, true><<<blocks, Large::kThreads, 0, s>>>(a, dst, d.row_tiles, d.col_tiles,
-                                                                                     d.chunk, total);
+                                                                                     d.chunk, total, stream);
             return hipGetLastError();
         }
     }
     if (direct)
         segment_dw_kernel<T, OUT, Medium, true><<<blocks, Medium::kThreads, 0, s>>>(a, dst, d.row_tiles, d.col_tiles,
-                                                                                   d.chunk, total);
+                                                                                   d.chunk, total, stream);
     else
         segment_dw_kernel<T, OUT, Medium, false><<<blocks, Medium::kThreads, 0, s>>>(a, dst, d.row_tiles, d.col_tiles,
-                                                                                    d.chunk, total);
+                                                                                    d.chunk, total, stream);
     return hipGetLastError();
 }
 
