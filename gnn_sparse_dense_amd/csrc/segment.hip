@@ -471,8 +471,10 @@ __device__ inline int64_t xcd_order(int64_t id, int64_t total) {
 
 // Tiles of the runs [v0, v1), each cut into pieces of `len` rows and `cols`
 // tiles to a piece: the piece and column tile of tile number `id`, numbered
-// so that each XCD gets a run of them; run < 0: there are fewer tiles.  Every
-// wave finds its tile by itself: 64 runs at a time, a scan of their pieces.
+// so that each XCD gets a run of them; run < 0: there are fewer tiles.  `most`
+// tiles are the most that offsets in order can have; tiles beyond them, of
+// offsets that decrease, are left out.  Every wave finds its tile by itself:
+// 64 runs at a time, a scan of their pieces.
 struct RowTile {
     int64_t run, row, end, piece, col;
 };
@@ -502,12 +504,14 @@ __device__ inline int64_t count_pieces(const SegmentArgs &a, int64_t v0, int64_t
     return uniform(sum);
 }
 
-__device__ inline RowTile find_tile(const SegmentArgs &a, int64_t v0, int64_t v1, int64_t len, int64_t cols, int64_t id) {
+__device__ inline RowTile find_tile(const SegmentArgs &a, int64_t v0, int64_t v1, int64_t len, int64_t cols, int64_t id,
+                                   int64_t most) {
     const int lane = threadIdx.x & (kWave - 1);
     RowTile t = {-1, 0, 0, 0, 0};
     int64_t lo, hi, mine = pieces_of(a, v0 + lane, v1, len, &lo, &hi), incl = wave_inclusive(mine);
     const int64_t first = __shfl(incl, kWave - 1, kWave);
-    const int64_t total = uniform(v1 - v0 <= kWave ? first : first + count_pieces(a, v0 + kWave, v1, len)) * cols;
+    const int64_t count = uniform(v1 - v0 <= kWave ? first : first + count_pieces(a, v0 + kWave, v1, len));
+    const int64_t total = min(count * cols, most);
     if (id >= total) return t;
     const int64_t at = xcd_order(id, total);
     t.piece = at / cols;
@@ -537,7 +541,7 @@ __global__ __launch_bounds__(S::kThreads, 2) void segment_kernel(SegmentArgs a, 
     const int64_t K = TRANSPOSED ? a.O : a.I, N = TRANSPOSED ? a.I : a.O;
     const T *in = (const T *)(TRANSPOSED ? a.dy : a.x), *w = (const T *)a.w;
     for (int64_t id = blockIdx.x; id < total; id += gridDim.x) {
-        const RowTile rt = find_tile(a, 0, a.E + 2, S::BM, col_tiles, id);
+        const RowTile rt = find_tile(a, 0, a.E + 2, S::BM, col_tiles, id, total);
         if (rt.run < 0) return;
         const int64_t run = uniform(rt.run), row = uniform(rt.row), n0 = rt.col * S::BN;
         T *out = (T *)a.y + row * N + n0;
@@ -595,7 +599,7 @@ __global__ __launch_bounds__(S::kThreads, 2) void segment_dw_kernel(SegmentArgs 
         const int64_t tiles = row_tiles * col_tiles;
         int64_t t, at, row, end;
         if (chunk) {
-            const RowTile rt = find_tile(a, 1, a.E + 1, chunk, tiles, id);
+            const RowTile rt = find_tile(a, 1, a.E + 1, chunk, tiles, id, total);
             if (rt.run < 0) return;
             t = rt.piece;
             at = rt.col;
@@ -630,10 +634,12 @@ constexpr int kFoldThreads = 256;
 
 // Adds a segment's partial sums in the order of its chunks.
 template <typename T>
-__global__ __launch_bounds__(kFoldThreads) void segment_fold_kernel(SegmentArgs a, int64_t chunk) {
+__global__ __launch_bounds__(kFoldThreads) void segment_fold_kernel(SegmentArgs a, int64_t chunk,
+                                                                    int64_t chunks) {
     const int64_t n = a.I * a.O;
     for (int64_t e = blockIdx.y; e < a.E; e += gridDim.y) {
-        const int64_t first = count_pieces(a, 1, e + 1, chunk), parts = count_pieces(a, e + 1, e + 2, chunk);
+        const int64_t first = min(chunks, count_pieces(a, 1, e + 1, chunk));
+        const int64_t parts = min(chunks - first, count_pieces(a, e + 1, e + 2, chunk));
         const float *from = a.partial + first * n;
         for (int64_t i = (int64_t)blockIdx.x * kFoldThreads + threadIdx.x; i < n;
              i += (int64_t)gridDim.x * kFoldThreads) {
@@ -750,7 +756,7 @@ hipError_t segment_dw(const SegmentArgs &a, hipStream_t s) {
     const int64_t n = a.I * a.O;
     const dim3 grid((unsigned)std::min<int64_t>((n + kFoldThreads - 1) / kFoldThreads, 1 << 16),
                     (unsigned)std::min<int64_t>(a.E, 1 << 14));
-    segment_fold_kernel<T><<<grid, kFoldThreads, 0, s>>>(a, d.chunk);
+    segment_fold_kernel<T><<<grid, kFoldThreads, 0, s>>>(a, d.chunk, d.chunks);
     return hipGetLastError();
 }
 

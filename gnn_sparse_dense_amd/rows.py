@@ -10,9 +10,10 @@ each row belongs to one or more experts (or node types), and the layer norm.
 Rows are fp32, bf16 or fp16 matrices; sums are fp32 and outputs are rounded
 once.  All five run on torch's current stream of the tensors' device,
 allocate through torch and never wait for the GPU, so they can be captured
-into a graph.  dispatch, combine, segment_matmul and layer_norm are
-differentiable (once); the spmm_* functions are the C calls on caller's
-tensors.
+into a graph (a backward pass only while no eager graph of the same leaves
+lives: torch ties a leaf's gradient to the stream it was first used on).
+dispatch, combine, segment_matmul and layer_norm are differentiable (once);
+the spmm_* functions are the C calls on the caller's tensors.
 """
 from __future__ import annotations
 
@@ -53,12 +54,6 @@ def _check_rows_type(name, t, dim=2):
     return _TYPES[t.dtype]
 
 
-def _stream(t, stream):
-    if stream is None:
-        return _current_stream(t)
-    return stream if isinstance(stream, int) else stream.cuda_stream
-
-
 @functools.lru_cache(maxsize=256)
 def _workspace_bytes(call: str, *sizes: int) -> int:
     n = ctypes.c_int64()
@@ -77,7 +72,7 @@ def _workspace(device, call: str, *sizes: int):
 
 # ---------------------------------------------------------------- the C calls
 
-def spmm_route_build(expert, E: int, offsets, order, position, stream=None) -> None:
+def spmm_route_build(expert, E: int, offsets, order, position) -> None:
     """Sort the pairs of expert (int64, any shape) by expert into offsets
     int64 [E + 1], order and position int32 (expert's number of elements)."""
     pairs, E = expert.numel(), int(E)
@@ -85,7 +80,7 @@ def spmm_route_build(expert, E: int, offsets, order, position, stream=None) -> N
     _check_tensor("offsets", offsets, (torch.int64,), (E + 1,), offsets.device)
     _check_tensor("order", order, (torch.int32,), (pairs,), offsets.device)
     _check_tensor("position", position, (torch.int32,), expert.shape, offsets.device)
-    _build(expert, pairs, E, offsets, order, position, _stream(offsets, stream))
+    _build(expert, pairs, E, offsets, order, position, _current_stream(offsets))
 
 
 def _build(expert, pairs, E, offsets, order, position, stream):
@@ -103,11 +98,11 @@ def _check_exchange(route, name, rows, count, weight):
     return kind, _TYPES[weight.dtype]
 
 
-def spmm_route_dispatch(route: "RowRoute", x, xs, weight=None, stream=None) -> None:
+def spmm_route_dispatch(route: "RowRoute", x, xs, weight=None) -> None:
     """xs [T * k, N] = rows of x [T, N] in expert order (times weight [T, k])."""
     kind, wkind = _check_exchange(route, "x", x, route.T, weight)
     _check_tensor("xs", xs, (x.dtype,), (route.T * route.k, x.shape[1]), route.device)
-    _dispatch(route, x, xs, weight, wkind, kind, _stream(x, stream))
+    _dispatch(route, x, xs, weight, wkind, kind, _current_stream(x))
 
 
 def _dispatch(route, x, xs, weight, wkind, kind, stream):
@@ -115,11 +110,11 @@ def _dispatch(route, x, xs, weight, wkind, kind, stream):
                                     x.data_ptr(), _ptr(weight), wkind, xs.data_ptr(), x.shape[1], kind, stream))
 
 
-def spmm_route_combine(route: "RowRoute", rows, weight, out, stream=None) -> None:
+def spmm_route_combine(route: "RowRoute", rows, weight, out) -> None:
     """out [T, N] = the rows [T * k, N] summed back (weight [T, k] or None: 1)."""
     kind, wkind = _check_exchange(route, "rows", rows, route.T * route.k, weight)
     _check_tensor("out", out, (rows.dtype,), (route.T, rows.shape[1]), route.device)
-    _combine(route, rows, weight, wkind, out, kind, _stream(rows, stream))
+    _combine(route, rows, weight, wkind, out, kind, _current_stream(rows))
 
 
 def _combine(route, rows, weight, wkind, out, kind, stream):
@@ -127,7 +122,7 @@ def _combine(route, rows, weight, wkind, out, kind, stream):
                                    rows.data_ptr(), _ptr(weight), wkind, out.data_ptr(), rows.shape[1], kind, stream))
 
 
-def spmm_route_combine_backward(route: "RowRoute", rows, weight, dout, drows, dweight, stream=None) -> None:
+def spmm_route_combine_backward(route: "RowRoute", rows, weight, dout, drows, dweight) -> None:
     """Gradients of combine: drows [T * k, N] and dweight [T, k], either may
     be None (rows too, without dweight)."""
     kind, wkind = _check_exchange(route, "dout", dout, route.T, weight)
@@ -141,7 +136,7 @@ def spmm_route_combine_backward(route: "RowRoute", rows, weight, dout, drows, dw
         types = (torch.float32, dout.dtype) if weight is None else (weight.dtype,)
         _check_tensor("dweight", dweight, types, (route.T, route.k), route.device)
         wkind = _TYPES[dweight.dtype]
-    _combine_backward(route, rows, weight, wkind, dout, drows, dweight, kind, _stream(dout, stream))
+    _combine_backward(route, rows, weight, wkind, dout, drows, dweight, kind, _current_stream(dout))
 
 
 def _combine_backward(route, rows, weight, wkind, dout, drows, dweight, kind, stream):
@@ -155,7 +150,7 @@ def _check_segment(rows_name, rows, width, dtype, offsets, R, E, device):
     _check_tensor("offsets", offsets, (torch.int64,), (E + 1,), device)
 
 
-def spmm_segment_product(x, w, offsets, y, stream=None) -> None:
+def spmm_segment_product(x, w, offsets, y) -> None:
     """y [R, O] = x [R, I] times w[e] [I, O] for the rows of each segment e."""
     kind = _check_rows_type("x", x)
     _check_rows_type("w", w, 3)
@@ -164,10 +159,10 @@ def spmm_segment_product(x, w, offsets, y, stream=None) -> None:
     _check_segment("x", x, I, x.dtype, offsets, x.shape[0], E, x.device)
     _check_tensor("y", y, (x.dtype,), (x.shape[0], O), x.device)
     _check(_lib.spmm_segment_product(x.data_ptr(), w.data_ptr(), offsets.data_ptr(), y.data_ptr(), x.shape[0], E, I,
-                                     O, kind, _stream(x, stream)))
+                                     O, kind, _current_stream(x)))
 
 
-def spmm_segment_product_dx(dy, w, offsets, dx, stream=None) -> None:
+def spmm_segment_product_dx(dy, w, offsets, dx) -> None:
     """dx [R, I] = dy [R, O] times the transpose of w[e] for each segment e."""
     kind = _check_rows_type("dy", dy)
     _check_rows_type("w", w, 3)
@@ -175,7 +170,7 @@ def spmm_segment_product_dx(dy, w, offsets, dx, stream=None) -> None:
     _check_tensor("w", w, (dy.dtype,), w.shape, dy.device)
     _check_segment("dy", dy, O, dy.dtype, offsets, dy.shape[0], E, dy.device)
     _check_tensor("dx", dx, (dy.dtype,), (dy.shape[0], I), dy.device)
-    _product_dx(dy, w.data_ptr(), offsets, dx, (E, I, O), kind, _stream(dy, stream))
+    _product_dx(dy, w.data_ptr(), offsets, dx, (E, I, O), kind, _current_stream(dy))
 
 
 def _product_dx(dy, w, offsets, dx, shape, kind, stream):
@@ -183,7 +178,7 @@ def _product_dx(dy, w, offsets, dx, shape, kind, stream):
                                         kind, stream))
 
 
-def spmm_segment_product_dw(x, dy, offsets, dw, stream=None) -> None:
+def spmm_segment_product_dw(x, dy, offsets, dw) -> None:
     """dw [E, I, O]: dw[e] = sum over the rows of segment e of x[r]^T dy[r]."""
     kind = _check_rows_type("x", x)
     _check_rows_type("dw", dw, 3)
@@ -191,7 +186,7 @@ def spmm_segment_product_dw(x, dy, offsets, dw, stream=None) -> None:
     _check_tensor("dw", dw, (x.dtype,), dw.shape, x.device)
     _check_segment("x", x, I, x.dtype, offsets, x.shape[0], E, x.device)
     _check_tensor("dy", dy, (x.dtype,), (x.shape[0], O), x.device)
-    _product_dw(x, dy, offsets, dw, kind, _stream(x, stream))
+    _product_dw(x, dy, offsets, dw, kind, _current_stream(x))
 
 
 def _product_dw(x, dy, offsets, dw, kind, stream):
@@ -213,7 +208,7 @@ def _check_norm(x, weight, bias):
     return kind, wkind
 
 
-def spmm_layer_norm(x, weight, bias, y, mean=None, rstd=None, eps: float = 1e-5, stream=None) -> None:
+def spmm_layer_norm(x, weight, bias, y, mean=None, rstd=None, eps: float = 1e-5) -> None:
     """y = layer norm of each row of x [R, N]; mean and rstd (fp32 [R]) are
     what the backward pass reads."""
     kind, wkind = _check_norm(x, weight, bias)
@@ -223,10 +218,10 @@ def spmm_layer_norm(x, weight, bias, y, mean=None, rstd=None, eps: float = 1e-5,
         if t is not None:
             _check_tensor(name, t, (torch.float32,), (R,), x.device)
     _check(_lib.spmm_layer_norm(_ptr(x), _ptr(weight), _ptr(bias), wkind, _ptr(y), _ptr(mean), _ptr(rstd), R, N,
-                                float(eps), kind, _stream(x, stream)))
+                                float(eps), kind, _current_stream(x)))
 
 
-def spmm_layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, stream=None) -> None:
+def spmm_layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias) -> None:
     """Gradients of the layer norm; any of dx [R, N], dweight and dbias [N]
     may be None."""
     kind, wkind = _check_norm(x, weight, None)
@@ -243,7 +238,7 @@ def spmm_layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, stre
             wkind = _TYPES[t.dtype]
             types = (t.dtype,)
     _norm_backward(dy, x, weight, wkind, mean.data_ptr(), rstd.data_ptr(), dx, dweight, dbias, kind,
-                   _stream(x, stream))
+                   _current_stream(x))
 
 
 def _norm_backward(dy, x, weight, wkind, mean, rstd, dx, dweight, dbias, kind, stream):

@@ -200,6 +200,40 @@ def test_exchange_writes_inside_its_arrays(kind):
     assert torch.equal(only_rows, drows) and torch.equal(only_w, dw) and torch.equal(again, drows)
 
 
+@pytest.mark.parametrize("T,k,N,kind", [(720000, 3, 2048, "bf16"), (50021, 3, 1433, "fp16"), (300007, 2, 64, "fp32"),
+                                        (700001, 2, 100, "fp16")])
+def test_exchange_of_large_calls(T, k, N, kind):
+    """Calls that stream past the cache, and (2048 wide) offsets past 2^32
+    elements; rows at the ends and around the borders, and random ones."""
+    dtype, g, E = TYPES[kind], rng(T, N), 9
+    e = pairs_of(g, T, k, E, "some")
+    r = G.RowRoute(e.to(DEV), E)
+    order, kept = r.order.cpu().long(), int(r.offsets[-1])
+    position = r.position.cpu().long()
+    x = torch.randn(T, N, device=DEV, dtype=dtype)
+    xs = G.dispatch(r, x)
+    at = torch.cat([torch.randint(0, T * k, (3000,), generator=g),
+                    torch.tensor([0, 1, kept - 1, kept, T * k - 1, T * k // 2])]
+                   + [torch.arange(min(T * k, c) - 2, min(T * k, c + 3)) for c in (2 ** 31 // N, 2 ** 32 // N)])
+    want = torch.where((at < kept)[:, None], x[(order[at] // k).to(DEV)].cpu(), torch.zeros((), dtype=dtype))
+    assert torch.equal(xs[at.to(DEV)].cpu(), want)
+    w = torch.rand(T, k, generator=g)
+    wd = w.to(DEV)
+    out, drows, dw = torch.empty_like(x), torch.empty_like(xs), torch.empty_like(wd)
+    G.spmm_route_combine(r, xs, wd, out)
+    t = torch.cat([torch.randint(0, T, (1500,), generator=g), torch.tensor([0, T - 1])])
+    there = position[t] < kept
+    rows = torch.where(there[:, :, None], xs[position[t].to(DEV)].double().cpu(), torch.zeros((), dtype=torch.float64))
+    terms = w[t].double()[:, :, None] * rows
+    close(out[t.to(DEV)], terms.sum(1), k * U * terms.abs().sum(1), dtype, "out")
+    G.spmm_route_combine_backward(r, xs, wd, x, drows, dw)
+    d = x[(order[at] // k).to(DEV)].double().cpu()
+    grad = torch.where((at < kept)[:, None], w.reshape(-1)[order[at]].double()[:, None] * d, torch.zeros((), dtype=torch.float64))
+    close(drows[at.to(DEV)], grad, U * grad.abs(), dtype, "drows")
+    dots = rows * x[t.to(DEV)].double().cpu()[:, None, :]
+    close(dw[t.to(DEV)], dots.sum(2), N * U * dots.abs().sum(2), torch.float32, "dweight")
+
+
 def test_infinite_weights_and_rows_follow_the_formula():
     e = torch.tensor([[0, 1], [1, -1], [-1, -1]], device=DEV)
     r = G.RowRoute(e, 2)
@@ -298,6 +332,53 @@ def test_segment_rows_of_another_segment_do_not_leak(kind):
     assert torch.equal(got[2][[0, 1, 3]], want[2][[0, 1, 3]]) and bool(torch.isnan(got[0][70:135]).all())
 
 
+@pytest.mark.parametrize("offsets", [[0, 6000, 0, 6000, 0, 6000], [6000, 0, 0, 0, 0, 0], [-5, 2 ** 40, 3, -2 ** 40, 6000, 1]])
+@pytest.mark.parametrize("I,O", [(64, 64), (65, 33)])
+def test_segment_offsets_out_of_order_touch_nothing_outside(I, O, offsets):
+    """What comes out is not specified; what stands around the outputs stays."""
+    R, E = 6000, 5
+    x, w, dy = (torch.ones(*s, device=DEV) for s in ((R, I), (E, I, O), (R, O)))
+    b = torch.tensor(offsets, device=DEV)
+    y, c1 = guarded((R, O), torch.float32)
+    dx, c2 = guarded((R, I), torch.float32)
+    dw, c3 = guarded((E, I, O), torch.float32)
+    G.spmm_segment_product(x, w, b, y)
+    G.spmm_segment_product_dx(dy, w, b, dx)
+    G.spmm_segment_product_dw(x, dy, b, dw)
+    torch.cuda.synchronize()
+    c1(), c2(), c3()
+
+
+def test_segment_products_of_many_rows():
+    """Long segments: dw in chunks of rows, more chunks than one scan covers,
+    and products whose element offsets pass 2^31."""
+    g = rng(41)
+    b = torch.tensor([0, 17, 17, 50000, 299000, 300000], device=DEV)
+    x, dy = normal(g, 300011, 24).to(DEV), normal(g, 300011, 40).to(DEV)
+    dw = torch.empty(5, 24, 40, device=DEV)
+    G.spmm_segment_product_dw(x, dy, b, dw)
+    for e in range(5):
+        X, D = (t[int(b[e]):int(b[e + 1])].double().cpu() for t in (x, dy))
+        close(dw[e], X.t() @ D, 2 * U * max(1, len(X)) * (X.abs().t() @ D.abs()), torch.float32, f"dw of segment {e}")
+    R, I, O = 1100000, 2048, 16
+    x = torch.randn(R, I, device=DEV, dtype=torch.bfloat16)
+    w = normal(g, 2, I, O, dtype=torch.bfloat16).to(DEV)
+    b = torch.tensor([0, 3, R], device=DEV)
+    y = torch.empty(R, O, device=DEV, dtype=torch.bfloat16)
+    G.spmm_segment_product(x, w, b, y)
+    rows = torch.tensor([0, 3, 524288, 1048575, 1048576, R - 1])
+    X, W = x[rows.to(DEV)].double().cpu(), w.double().cpu()
+    want = torch.stack([X[i] @ W[0 if r < 3 else 1] for i, r in enumerate(rows.tolist())])
+    size = torch.stack([X[i].abs() @ W[0 if r < 3 else 1].abs() for i, r in enumerate(rows.tolist())])
+    close(y[rows.to(DEV)], want, 2 * U * I * size, torch.bfloat16, "y far into x")
+    dx = torch.empty_like(x)
+    G.spmm_segment_product_dx(y, w, b, dx)
+    Y = y[rows.to(DEV)].double().cpu()
+    want = torch.stack([W[0 if r < 3 else 1] @ Y[i] for i, r in enumerate(rows.tolist())])
+    size = torch.stack([W[0 if r < 3 else 1].abs() @ Y[i].abs() for i, r in enumerate(rows.tolist())])
+    close(dx[rows.to(DEV)], want, 2 * U * O * size, torch.bfloat16, "dx far into x")
+
+
 # ---------------------------------------------------------------- layer norm
 
 NORM = [(0, 8), (1, 1), (3, 5), (7, 32), (33, 100), (700, 64), (5000, 16), (5, 1433), (9, 4096), (3, 2056), (2, 8200),
@@ -379,6 +460,35 @@ def test_layer_norm_parts_and_bounds(N):
     assert all(torch.equal(p, q) for p, q in zip(only, (dx, dw, db)))
     assert torch.equal(G.layer_norm(x, w), G.layer_norm(x, w, torch.zeros_like(b)))
     assert torch.equal(G.layer_norm(x, None, b), G.layer_norm(x, torch.ones_like(w), b))
+
+
+@pytest.mark.parametrize("R,N,kind", [(1100001, 2048, "bf16"), (1100001, 61, "fp32"), (100003, 1433, "fp16")])
+def test_layer_norm_of_large_calls(R, N, kind):
+    """Calls that stream past the cache and element offsets past 2^31: rows
+    against the same rows alone, column sums against 64 bits."""
+    dtype = TYPES[kind]
+    x, dy = (torch.randn(R, N, device=DEV, dtype=dtype) for _ in range(2))
+    w, b = (torch.randn(N, device=DEV) for _ in range(2))
+    y, dx = torch.empty_like(x), torch.empty_like(x)
+    mean, rstd = torch.empty(R, device=DEV), torch.empty(R, device=DEV)
+    dw, db = torch.empty_like(w), torch.empty_like(b)
+    G.spmm_layer_norm(x, w, b, y, mean, rstd)
+    G.spmm_layer_norm_backward(dy, x, w, mean, rstd, dx, dw, db)
+    at = torch.cat([torch.randint(0, R, (500,), generator=rng(R)), torch.tensor([0, R - 1, 2 ** 31 // N % R])]).to(DEV)
+    few = [t[at].contiguous() for t in (x, dy, mean, rstd)]
+    assert torch.equal(y[at], G.layer_norm(few[0], w, b))
+    some = torch.empty_like(few[0])
+    G.spmm_layer_norm_backward(few[1], few[0], w, few[2], few[3], some, None, None)
+    assert torch.equal(dx[at], some)
+    sums = torch.zeros(4, N, dtype=torch.float64, device=DEV)
+    for i in range(0, R, 50000):
+        d = dy[i:i + 50000].double()
+        u = (x[i:i + 50000].double() - mean[i:i + 50000].double()[:, None]) * rstd[i:i + 50000].double()[:, None]
+        sums += torch.stack([(d * u).sum(0), (d * u).abs().sum(0), d.sum(0), d.abs().sum(0)])
+    sums = sums.cpu()
+    chain = R / 256 + 200                             # rows of one group, its block's groups, the blocks' parts
+    close(dw, sums[0], (chain + 4) * U * sums[1], torch.float32, "dweight")
+    close(db, sums[2], chain * U * sums[3], torch.float32, "dbias")
 
 
 def test_layer_norm_of_more_dimensions_and_views():
