@@ -19,11 +19,16 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import os
 
 import torch
-from torch.autograd.function import once_differentiable
 
-from . import SPMM_BF16, SPMM_F16, SPMM_F32, _check, _current_stream, _lib
+from . import HERE, SPMM_BF16, SPMM_F16, SPMM_F32, _check, _current_stream, _lib
+
+if not os.path.exists(os.path.join(HERE, "_rows.so")):
+    raise ImportError(f"{HERE}/_rows.so is missing: build it first (python -c 'import __graft_entry__ as g; g.build()')")
+
+from . import _rows  # noqa: E402  (the autograd nodes, csrc/torch_rows.cpp)
 
 _TYPES = {torch.float32: SPMM_F32, torch.bfloat16: SPMM_BF16, torch.float16: SPMM_F16}
 
@@ -80,13 +85,9 @@ def spmm_route_build(expert, E: int, offsets, order, position) -> None:
     _check_tensor("offsets", offsets, (torch.int64,), (E + 1,), offsets.device)
     _check_tensor("order", order, (torch.int32,), (pairs,), offsets.device)
     _check_tensor("position", position, (torch.int32,), expert.shape, offsets.device)
-    _build(expert, pairs, E, offsets, order, position, _current_stream(offsets))
-
-
-def _build(expert, pairs, E, offsets, order, position, stream):
     ws, at, n = _workspace(offsets.device, "spmm_route_workspace", pairs, E)
-    _check(_lib.spmm_route_build(expert.data_ptr(), pairs, E, offsets.data_ptr(), order.data_ptr(),
-                                 position.data_ptr(), at, n, stream))
+    _check(_lib.spmm_route_build(_ptr(expert), pairs, E, _ptr(offsets), _ptr(order), _ptr(position), at, n,
+                                 _current_stream(offsets)))
 
 
 def _check_exchange(route, name, rows, count, weight):
@@ -102,24 +103,16 @@ def spmm_route_dispatch(route: "RowRoute", x, xs, weight=None) -> None:
     """xs [T * k, N] = rows of x [T, N] in expert order (times weight [T, k])."""
     kind, wkind = _check_exchange(route, "x", x, route.T, weight)
     _check_tensor("xs", xs, (x.dtype,), (route.T * route.k, x.shape[1]), route.device)
-    _dispatch(route, x, xs, weight, wkind, kind, _current_stream(x))
-
-
-def _dispatch(route, x, xs, weight, wkind, kind, stream):
-    _check(_lib.spmm_route_dispatch(route.offsets.data_ptr(), route.order.data_ptr(), route.T, route.k, route.E,
-                                    x.data_ptr(), _ptr(weight), wkind, xs.data_ptr(), x.shape[1], kind, stream))
+    _check(_lib.spmm_route_dispatch(_ptr(route.offsets), _ptr(route.order), route.T, route.k, route.E, _ptr(x),
+                                    _ptr(weight), wkind, _ptr(xs), x.shape[1], kind, _current_stream(x)))
 
 
 def spmm_route_combine(route: "RowRoute", rows, weight, out) -> None:
     """out [T, N] = the rows [T * k, N] summed back (weight [T, k] or None: 1)."""
     kind, wkind = _check_exchange(route, "rows", rows, route.T * route.k, weight)
     _check_tensor("out", out, (rows.dtype,), (route.T, rows.shape[1]), route.device)
-    _combine(route, rows, weight, wkind, out, kind, _current_stream(rows))
-
-
-def _combine(route, rows, weight, wkind, out, kind, stream):
-    _check(_lib.spmm_route_combine(route.offsets.data_ptr(), route.position.data_ptr(), route.T, route.k, route.E,
-                                   rows.data_ptr(), _ptr(weight), wkind, out.data_ptr(), rows.shape[1], kind, stream))
+    _check(_lib.spmm_route_combine(_ptr(route.offsets), _ptr(route.position), route.T, route.k, route.E, _ptr(rows),
+                                   _ptr(weight), wkind, _ptr(out), rows.shape[1], kind, _current_stream(rows)))
 
 
 def spmm_route_combine_backward(route: "RowRoute", rows, weight, dout, drows, dweight) -> None:
@@ -136,13 +129,9 @@ def spmm_route_combine_backward(route: "RowRoute", rows, weight, dout, drows, dw
         types = (torch.float32, dout.dtype) if weight is None else (weight.dtype,)
         _check_tensor("dweight", dweight, types, (route.T, route.k), route.device)
         wkind = _TYPES[dweight.dtype]
-    _combine_backward(route, rows, weight, wkind, dout, drows, dweight, kind, _current_stream(dout))
-
-
-def _combine_backward(route, rows, weight, wkind, dout, drows, dweight, kind, stream):
-    _check(_lib.spmm_route_combine_backward(route.offsets.data_ptr(), route.order.data_ptr(), route.T, route.k,
-                                            route.E, _ptr(rows), _ptr(weight), wkind, dout.data_ptr(), _ptr(drows),
-                                            _ptr(dweight), dout.shape[1], kind, stream))
+    _check(_lib.spmm_route_combine_backward(_ptr(route.offsets), _ptr(route.order), route.T, route.k, route.E,
+                                            _ptr(rows), _ptr(weight), wkind, _ptr(dout), _ptr(drows), _ptr(dweight),
+                                            dout.shape[1], kind, _current_stream(dout)))
 
 
 def _check_segment(rows_name, rows, width, dtype, offsets, R, E, device):
@@ -158,8 +147,8 @@ def spmm_segment_product(x, w, offsets, y) -> None:
     _check_tensor("w", w, (x.dtype,), w.shape, x.device)
     _check_segment("x", x, I, x.dtype, offsets, x.shape[0], E, x.device)
     _check_tensor("y", y, (x.dtype,), (x.shape[0], O), x.device)
-    _check(_lib.spmm_segment_product(x.data_ptr(), w.data_ptr(), offsets.data_ptr(), y.data_ptr(), x.shape[0], E, I,
-                                     O, kind, _current_stream(x)))
+    _check(_lib.spmm_segment_product(_ptr(x), _ptr(w), _ptr(offsets), _ptr(y), x.shape[0], E, I, O, kind,
+                                     _current_stream(x)))
 
 
 def spmm_segment_product_dx(dy, w, offsets, dx) -> None:
@@ -170,12 +159,8 @@ def spmm_segment_product_dx(dy, w, offsets, dx) -> None:
     _check_tensor("w", w, (dy.dtype,), w.shape, dy.device)
     _check_segment("dy", dy, O, dy.dtype, offsets, dy.shape[0], E, dy.device)
     _check_tensor("dx", dx, (dy.dtype,), (dy.shape[0], I), dy.device)
-    _product_dx(dy, w.data_ptr(), offsets, dx, (E, I, O), kind, _current_stream(dy))
-
-
-def _product_dx(dy, w, offsets, dx, shape, kind, stream):
-    _check(_lib.spmm_segment_product_dx(dy.data_ptr(), w, offsets.data_ptr(), dx.data_ptr(), dy.shape[0], *shape,
-                                        kind, stream))
+    _check(_lib.spmm_segment_product_dx(_ptr(dy), _ptr(w), _ptr(offsets), _ptr(dx), dy.shape[0], E, I, O, kind,
+                                        _current_stream(dy)))
 
 
 def spmm_segment_product_dw(x, dy, offsets, dw) -> None:
@@ -186,13 +171,9 @@ def spmm_segment_product_dw(x, dy, offsets, dw) -> None:
     _check_tensor("dw", dw, (x.dtype,), dw.shape, x.device)
     _check_segment("x", x, I, x.dtype, offsets, x.shape[0], E, x.device)
     _check_tensor("dy", dy, (x.dtype,), (x.shape[0], O), x.device)
-    _product_dw(x, dy, offsets, dw, kind, _current_stream(x))
-
-
-def _product_dw(x, dy, offsets, dw, kind, stream):
-    ws, at, n = _workspace(x.device, "spmm_segment_workspace", x.shape[0], *dw.shape, kind)
-    _check(_lib.spmm_segment_product_dw(x.data_ptr(), dy.data_ptr(), offsets.data_ptr(), dw.data_ptr(), x.shape[0],
-                                        *dw.shape, kind, at, n, stream))
+    ws, at, n = _workspace(x.device, "spmm_segment_workspace", x.shape[0], E, I, O, kind)
+    _check(_lib.spmm_segment_product_dw(_ptr(x), _ptr(dy), _ptr(offsets), _ptr(dw), x.shape[0], E, I, O, kind, at, n,
+                                        _current_stream(x)))
 
 
 def _check_norm(x, weight, bias):
@@ -237,24 +218,14 @@ def spmm_layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias) -> N
             _check_tensor(name, t, types, (N,), x.device)
             wkind = _TYPES[t.dtype]
             types = (t.dtype,)
-    _norm_backward(dy, x, weight, wkind, mean.data_ptr(), rstd.data_ptr(), dx, dweight, dbias, kind,
-                   _current_stream(x))
-
-
-def _norm_backward(dy, x, weight, wkind, mean, rstd, dx, dweight, dbias, kind, stream):
-    R, N = x.shape
     ws, at, n = None, None, 0
     if dweight is not None or dbias is not None:
         ws, at, n = _workspace(x.device, "spmm_layer_norm_workspace", R, N, kind)
-    _check(_lib.spmm_layer_norm_backward(dy.data_ptr(), x.data_ptr(), _ptr(weight), wkind, mean, rstd, _ptr(dx),
-                                         _ptr(dweight), _ptr(dbias), R, N, kind, at, n, stream))
+    _check(_lib.spmm_layer_norm_backward(_ptr(dy), _ptr(x), _ptr(weight), wkind, _ptr(mean), _ptr(rstd), _ptr(dx),
+                                         _ptr(dweight), _ptr(dbias), R, N, kind, at, n, _current_stream(x)))
 
 
 # ------------------------------------------------------- differentiable calls
-
-def _wants_grad(*tensors) -> bool:
-    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
-
 
 class RowRoute:
     """Rows sorted by expert, built once per routing and applied many times.
@@ -268,92 +239,22 @@ class RowRoute:
     position: int32 [T, k], the place of each pair
     """
 
+    __slots__ = ("offsets", "order", "position", "T", "k", "E")
+
     def __init__(self, expert, num_experts: int):
-        if expert.dtype != torch.int64:
-            raise TypeError(f"expert must be int64, got {expert.dtype}")
-        if expert.dim() not in (1, 2):
-            raise ValueError(f"expert has {expert.dim()} dimensions, expected 1 or 2")
-        if not expert.is_cuda:
-            raise ValueError("expert must be a GPU tensor")
-        self.T = int(expert.shape[0])
-        self.k = int(expert.shape[1]) if expert.dim() == 2 else 1
-        if self.k < 1:
-            raise ValueError("expert must have at least one choice per row")
         self.E = int(num_experts)
-        self.device = expert.device
-        pairs = self.T * self.k
-        _workspace_bytes("spmm_route_workspace", pairs, self.E)      # refuses sizes before any allocation
-        self.offsets = torch.empty(self.E + 1, dtype=torch.int64, device=self.device)
-        self.order = torch.empty(pairs, dtype=torch.int32, device=self.device)
-        self.position = torch.empty((self.T, self.k), dtype=torch.int32, device=self.device)
-        _build(expert.contiguous(), pairs, self.E, self.offsets, self.order, self.position,
-               _current_stream(self.offsets))
+        self.offsets, self.order, self.position, self.T, self.k = _rows.route_build(expert, self.E)
 
-
-# The backward functions call the library on tensors that the forward pass
-# checked or that they allocate: dy has the forward output's shape, type and
-# device by autograd's own rules.
-
-class _Dispatch(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, x, route):
-        ctx.route = route
-        xs = x.new_empty((route.T * route.k, x.shape[1]))
-        spmm_route_dispatch(route, x.contiguous(), xs)
-        return xs
-
-    @staticmethod
-    @once_differentiable
-    def backward(ctx, dxs):
-        route = ctx.route
-        dxs = dxs.contiguous()
-        dx = dxs.new_empty((route.T, dxs.shape[1]))
-        kind = _TYPES[dxs.dtype]
-        _combine(route, dxs, None, kind, dx, kind, _current_stream(dxs))
-        return dx, None
+    @property
+    def device(self):
+        return self.offsets.device
 
 
 def dispatch(route: RowRoute, x):
     """Rows of x [T, N] in expert order: [T * k, N], row route.position[t, j]
     = x[t]; rows from route.offsets[E] on (pairs without an expert) are zero.
     Differentiable in x."""
-    _check_rows_type("x", x)
-    if _wants_grad(x):
-        return _Dispatch.apply(x, route)
-    xs = x.new_empty((route.T * route.k, x.shape[1]))
-    spmm_route_dispatch(route, x.contiguous(), xs)
-    return xs
-
-
-class _Combine(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, rows, weight, route):
-        rows = rows.contiguous()
-        weight = None if weight is None else weight.contiguous()
-        ctx.route = route
-        # rows are read again only for the weights' gradient
-        ctx.save_for_backward(rows if ctx.needs_input_grad[1] else None, weight)
-        out = rows.new_empty((route.T, rows.shape[1]))
-        spmm_route_combine(route, rows, weight, out)
-        return out
-
-    @staticmethod
-    @once_differentiable
-    def backward(ctx, dout):
-        route = ctx.route
-        rows, weight = ctx.saved_tensors
-        dout = dout.contiguous()
-        drows = dweight = None
-        if ctx.needs_input_grad[0]:
-            drows = dout.new_empty((route.T * route.k, dout.shape[1]))
-        kind, stream = _TYPES[dout.dtype], _current_stream(dout)
-        wkind = kind if weight is None else _TYPES[weight.dtype]
-        if ctx.needs_input_grad[1]:
-            dweight = torch.empty_like(weight)
-            _combine_backward(route, rows, weight, wkind, dout, drows, dweight, kind, stream)
-        elif drows is not None:
-            _dispatch(route, dout, drows, weight, wkind, kind, stream)
-        return drows, dweight, None
+    return _rows.dispatch(route.offsets, route.order, route.position, route.T, route.k, route.E, x)
 
 
 def combine(route: RowRoute, rows, weight=None):
@@ -361,39 +262,7 @@ def combine(route: RowRoute, rows, weight=None):
     with rows [T * k, N] in expert order and weight [T, k] in fp32 or the
     rows' type (None: 1); pairs without an expert do not enter.
     Differentiable in rows and weight."""
-    _check_rows_type("rows", rows)
-    if _wants_grad(rows, weight):
-        return _Combine.apply(rows, weight, route)
-    out = rows.new_empty((route.T, rows.shape[1]))
-    spmm_route_combine(route, rows.contiguous(), None if weight is None else weight.contiguous(), out)
-    return out
-
-
-class _SegmentMatmul(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, x, w, offsets):
-        x, w, offsets = x.contiguous(), w.contiguous(), offsets.contiguous()
-        need_x, need_w = ctx.needs_input_grad[:2]
-        ctx.save_for_backward(x if need_w else None, w if need_x else None, offsets)
-        ctx.shape = w.shape
-        y = x.new_empty((x.shape[0], w.shape[2]))
-        spmm_segment_product(x, w, offsets, y)
-        return y
-
-    @staticmethod
-    @once_differentiable
-    def backward(ctx, dy):
-        x, w, offsets = ctx.saved_tensors
-        dy = dy.contiguous()
-        kind, stream = _TYPES[dy.dtype], _current_stream(dy)
-        dx = dw = None
-        if ctx.needs_input_grad[0]:
-            dx = dy.new_empty((dy.shape[0], ctx.shape[1]))
-            _product_dx(dy, w.data_ptr(), offsets, dx, ctx.shape, kind, stream)
-        if ctx.needs_input_grad[1]:
-            dw = dy.new_empty(ctx.shape)
-            _product_dw(x, dy, offsets, dw, kind, stream)
-        return dx, dw, None
+    return _rows.combine(route.offsets, route.order, route.position, route.T, route.k, route.E, rows, weight)
 
 
 def segment_matmul(x, w, offsets):
@@ -401,61 +270,11 @@ def segment_matmul(x, w, offsets):
     offsets[e + 1] of x [R, I], with w [E, I, O] of x's type and offsets int64
     [E + 1] on the GPU (a RowRoute's, or the bounds of rows sorted by type);
     rows outside the segments are zero.  Differentiable in x and w."""
-    _check_rows_type("x", x)
-    _check_rows_type("w", w, 3)
-    if _wants_grad(x, w):
-        return _SegmentMatmul.apply(x, w, offsets)
-    y = x.new_empty((x.shape[0], w.shape[2]))
-    spmm_segment_product(x.contiguous(), w.contiguous(), offsets.contiguous(), y)
-    return y
-
-
-class _LayerNorm(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, x, weight, bias, eps):
-        x = x.contiguous()
-        weight = None if weight is None else weight.contiguous()
-        bias = None if bias is None else bias.contiguous()
-        kind, wkind = _check_norm(x, weight, bias)
-        R, N = x.shape
-        y = torch.empty_like(x)
-        stats = torch.empty((2, R), dtype=torch.float32, device=x.device)       # mean, rstd
-        at = stats.data_ptr()
-        _check(_lib.spmm_layer_norm(x.data_ptr(), _ptr(weight), _ptr(bias), wkind, y.data_ptr(), at,
-                                    at + 4 * R if at else None, R, N, float(eps), kind, _current_stream(x)))
-        ctx.save_for_backward(x, weight, stats)
-        ctx.types = kind, wkind, None if bias is None else bias.dtype
-        return y
-
-    @staticmethod
-    @once_differentiable
-    def backward(ctx, dy):
-        x, weight, stats = ctx.saved_tensors
-        kind, wkind, bias_dtype = ctx.types
-        need_x, need_w, need_b = ctx.needs_input_grad[:3]
-        dx = torch.empty_like(x) if need_x else None
-        dweight = torch.empty_like(weight) if need_w else None
-        dbias = torch.empty(x.shape[1], dtype=bias_dtype, device=x.device) if need_b else None
-        mean = stats.data_ptr()
-        _norm_backward(dy.contiguous(), x, weight, wkind, mean, mean + 4 * x.shape[0], dx, dweight, dbias, kind,
-                       _current_stream(x))
-        return dx, dweight, dbias, None
+    return _rows.segment_matmul(x, w, offsets)
 
 
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-5):
     """Layer norm over the last dimension of x [..., N]: (x - mean) /
     sqrt(var + eps) * weight + bias with the biased variance; weight and bias
     [N] in fp32 or x's type (None: 1 and 0).  Differentiable in all three."""
-    if x.dim() < 1:
-        raise ValueError("x must have at least one dimension")
-    shape = x.shape
-    if x.dim() != 2:
-        x = x.reshape(-1, shape[-1]) if shape[-1] else x.reshape(0, 0)
-    if _wants_grad(x, weight, bias):
-        y = _LayerNorm.apply(x, weight, bias, eps)
-    else:
-        x = x.contiguous()
-        y = torch.empty_like(x)
-        spmm_layer_norm(x, None if weight is None else weight.contiguous(),
-                        None if bias is None else bias.contiguous(), y, None, None, eps)
-    return y if y.shape == shape else y.reshape(shape)
+    return _rows.layer_norm(x, weight, bias, eps)

@@ -512,6 +512,50 @@ def test_layer_norm_passes_nan_and_inf_on_within_their_rows():
     assert bool(torch.isfinite(y[[0, 2, 4]]).all())
 
 
+def test_gradients_that_are_not_asked_for_and_inputs_that_are_not_given():
+    """Each subset of the inputs on its own gives the bits of all together."""
+    g = rng(61)
+    x, w, b, dy = (normal(g, *s).to(DEV).requires_grad_() for s in ((30, 70), (70,), (70,), (30, 70)))
+    both = torch.autograd.grad(G.layer_norm(x, w, b), [x, w, b], dy)
+    for i, leaf in enumerate((x, w, b)):
+        assert torch.equal(torch.autograd.grad(G.layer_norm(x, w, b), leaf, dy)[0], both[i])
+    alone, = torch.autograd.grad(G.layer_norm(x.detach(), None, b), b, dy)
+    assert torch.equal(alone, both[2])
+    dx, db = torch.autograd.grad(G.layer_norm(x, None, b), [x, b], dy)
+    assert torch.equal(db, both[2]) and torch.equal(dx, torch.autograd.grad(G.layer_norm(x), x, dy)[0])
+    assert torch.equal(torch.autograd.grad(G.layer_norm(x.detach(), w.detach(), b), b, dy)[0], both[2])
+
+    r = G.RowRoute(torch.randint(0, 3, (30, 2), generator=g).to(DEV), 3)
+    rows, wt = normal(g, 60, 70).to(DEV).requires_grad_(), torch.rand(30, 2, generator=g).to(DEV).requires_grad_()
+    drows, dwt = torch.autograd.grad(G.combine(r, rows, wt), [rows, wt], dy)
+    assert torch.equal(torch.autograd.grad(G.combine(r, rows, wt.detach()), rows, dy)[0], drows)
+    assert torch.equal(torch.autograd.grad(G.combine(r, rows.detach(), wt), wt, dy)[0], dwt)
+    assert torch.equal(torch.autograd.grad(G.combine(r, rows, wt), wt, dy)[0], dwt)
+    m, o = normal(g, 3, 70, 20).to(DEV).requires_grad_(), torch.tensor([0, 5, 5, 28], device=DEV)
+    d = dy[:, :20].detach()                           # a strided gradient
+    dx, dm = torch.autograd.grad(G.segment_matmul(x, m, o), [x, m], d)
+    assert torch.equal(torch.autograd.grad(G.segment_matmul(x, m.detach(), o), x, d)[0], dx)
+    assert torch.equal(torch.autograd.grad(G.segment_matmul(x.detach(), m, o), m, d)[0], dm)
+
+
+def test_broadcast_inputs_and_second_derivatives():
+    g = rng(62)
+    r = G.RowRoute(torch.randint(0, 3, (30, 2), generator=g).to(DEV), 3)
+    rows, one = normal(g, 60, 8).to(DEV), torch.rand(30, 1, generator=g).to(DEV).requires_grad_()
+    full = one.detach().expand(30, 2).contiguous().requires_grad_()
+    out, want = G.combine(r, rows, one.expand(30, 2)), G.combine(r, rows, full)
+    assert torch.equal(out, want)
+    d1, = torch.autograd.grad(out.sum(), one)
+    d2, = torch.autograd.grad(want.sum(), full)
+    assert torch.equal(d1, d2.sum(1, keepdim=True))
+    x = normal(g, 4, 8).to(DEV).requires_grad_()
+    dx, = torch.autograd.grad(G.layer_norm(x).square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="differentiable once"):
+        dx.sum().backward()
+    with torch.no_grad():
+        assert not G.layer_norm(x).requires_grad
+
+
 # ------------------------------------------------------------------ together
 
 def block(mod, p, expert, E):

@@ -104,7 +104,7 @@ def test_host_tensors_shapes_and_types_are_refused_by_the_binding():
 
 class FakeRoute:
     T, k, E, device = 4, 2, 3, torch.device("cpu")
-    offsets = order = position = None
+    offsets = order = position = torch.zeros(4, dtype=torch.int64)
 
 
 def test_shapes_of_the_exchange_are_refused_by_the_binding():
