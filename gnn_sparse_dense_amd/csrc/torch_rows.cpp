@@ -108,9 +108,13 @@ int code(const Tensor &t) {
     return t.scalar_type() == at::kFloat ? SPMM_F32 : t.scalar_type() == at::kBFloat16 ? SPMM_BF16 : SPMM_F16;
 }
 
+// A tangent of forward mode takes the node too, which refuses it: the plain
+// calls would drop it.
 bool wants_grad(const Tensor &a, const Tensor &b = {}, const Tensor &c = {}) {
-    if (!at::GradMode::is_enabled()) return false;
-    return a.requires_grad() || (b.defined() && b.requires_grad()) || (c.defined() && c.requires_grad());
+    const bool backward = at::GradMode::is_enabled();
+    for (const Tensor *t : {&a, &b, &c})
+        if (t->defined() && ((backward && t->requires_grad()) || t->_fw_grad(/*level=*/0).defined())) return true;
+    return false;
 }
 
 // Gradients that would themselves be differentiated raise when that happens.

@@ -739,3 +739,21 @@ def test_aggregation_and_typed_product_together():
     dB, dw = torch.autograd.grad(out.square().sum(), [B, wt])
     assert dB.shape == B.shape and bool(torch.isfinite(dB).all()) and bool(dB.any()) and bool(dw.any())
     adj.close()
+
+
+def test_forward_mode_is_refused():
+    """A tangent is refused whether or not gradients are recorded, never dropped."""
+    g = rng(71)
+    x, t = normal(g, 6, 8).to(DEV), normal(g, 6, 8).to(DEV)
+    w, weight = normal(g, 2, 8, 4).to(DEV), normal(g, 6, 1).to(DEV)
+    route = G.RowRoute(torch.tensor([0, 1, 1, 0, 1, 0], device=DEV).reshape(6, 1), 2)
+    with torch.autograd.forward_ad.dual_level():
+        dual = torch.autograd.forward_ad.make_dual(x, t)
+        for call in (lambda: G.layer_norm(dual), lambda: G.dispatch(route, dual),
+                     lambda: G.combine(route, dual, weight),
+                     lambda: G.segment_matmul(dual, w, route.offsets)):
+            with pytest.raises(RuntimeError, match="jvp"):
+                call()
+            with torch.no_grad(), pytest.raises(RuntimeError, match="jvp"):
+                call()
+    torch.testing.assert_close(G.layer_norm(x), torch.nn.functional.layer_norm(x, (8,)))
