@@ -6,7 +6,11 @@
 // The nodes are C++ because a small training call is host time: a layer norm
 // of 9 x 368 with its gradients takes 71 us, and took 127 us with the backward
 // functions in Python (the engine by itself, around an identity: 43 us).
+#include <ATen/hip/impl/HIPStreamMasqueradingAsCUDA.h>
+#include <c10/hip/HIPGraphsC10Utils.h>
+#include <c10/hip/HIPGuard.h>
 #include <c10/hip/HIPStream.h>
+#include <torch/csrc/autograd/functions/accumulate_grad.h>
 #include <torch/csrc/autograd/functions/basic_ops.h>
 #include <torch/extension.h>
 
@@ -117,6 +121,31 @@ bool wants_grad(const Tensor &a, const Tensor &b = {}, const Tensor &c = {}) {
     return false;
 }
 
+bool capturing(const c10::hip::HIPStream &stream) {
+    if (!stream.stream()) return false;                  // the default stream cannot be captured
+    const c10::hip::HIPStreamGuard guard(stream);
+    return c10::hip::currentStreamCaptureStatusMayInitCtx() != c10::hip::CaptureStatus::None;
+}
+
+// torch hands a leaf's gradient over on the stream of the leaf's first use, as
+// long as a graph of the leaf lives.  Where this backward pass is captured and
+// that stream is not, the hand-over would tie the capture to a stream outside
+// of it, which ends the process: refused before the gradient exists.
+void refuse_leaves_outside_capture(const Tensor &grad) {
+    if (!capturing(c10::hip::getCurrentHIPStream(grad.get_device()))) return;
+    const auto node = torch::autograd::get_current_node();
+    for (size_t i = 0; node && i < node->num_outputs(); ++i) {
+        const auto &leaf = node->next_edge(i).function;
+        if (!node->task_should_compute_output(i) || !dynamic_cast<torch::autograd::AccumulateGrad *>(leaf.get()))
+            continue;
+        const auto stream = leaf->stream();
+        if (stream && !capturing(c10::hip::HIPStreamMasqueradingAsCUDA(*stream).hip_stream()))
+            throw std::runtime_error(
+                "backward of a row operator is captured while a graph of the same leaf lives that was built on a "
+                "stream outside the capture: drop that graph first");
+    }
+}
+
 // Gradients that would themselves be differentiated raise when that happens.
 variable_list once(const variable_list &grads, variable_list outputs) {
     if (!at::GradMode::is_enabled()) return outputs;
@@ -202,6 +231,7 @@ struct Dispatch : torch::autograd::Function<Dispatch> {
     }
 
     static variable_list backward(AutogradContext *ctx, variable_list grads) {
+        refuse_leaves_outside_capture(grads[0]);
         const Route r = kept(ctx, ctx->get_saved_variables());
         const Tensor dxs = grads[0].contiguous();
         const Tensor dx = at::empty({r.T, dxs.size(1)}, dxs.options());
@@ -236,6 +266,7 @@ struct Combine : torch::autograd::Function<Combine> {
     }
 
     static variable_list backward(AutogradContext *ctx, variable_list grads) {
+        refuse_leaves_outside_capture(grads[0]);
         const variable_list saved = ctx->get_saved_variables();
         const Route r = kept(ctx, saved);
         const Tensor &rows = saved[0], &weight = saved[1], dout = grads[0].contiguous();
@@ -285,6 +316,7 @@ struct SegmentMatmul : torch::autograd::Function<SegmentMatmul> {
     }
 
     static variable_list backward(AutogradContext *ctx, variable_list grads) {
+        refuse_leaves_outside_capture(grads[0]);
         const variable_list saved = ctx->get_saved_variables();
         const Tensor &x = saved[0], &w = saved[1], &offsets = saved[2], dy = grads[0].contiguous();
         const auto shape = ctx->saved_data["shape"].toIntVector();
@@ -347,6 +379,7 @@ struct LayerNorm : torch::autograd::Function<LayerNorm> {
     }
 
     static variable_list backward(AutogradContext *ctx, variable_list grads) {
+        refuse_leaves_outside_capture(grads[0]);
         const variable_list saved = ctx->get_saved_variables();
         const Tensor &x = saved[0], &weight = saved[1], &stats = saved[2], dy = grads[0].contiguous();
         const int wtype = (int)ctx->saved_data["wtype"].toInt();

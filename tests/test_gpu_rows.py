@@ -705,6 +705,39 @@ def test_block_captured_and_replayed_with_new_inputs():
             assert all(torch.equal(a, b) for a, b in zip(grads, wgrads)), f"replay {rep} of graph {n}"
 
 
+def test_captured_backward_beside_an_eager_graph_of_its_leaves_is_refused():
+    """The gradient of a leaf whose eager graph lives would leave the capture;
+    once that graph is gone, the same backward pass is captured and replayed."""
+    g = rng(73)
+    x, w = normal(g, 40, 24).to(DEV).requires_grad_(), normal(g, 3, 24, 16).to(DEV).requires_grad_()
+    e = torch.randint(0, 3, (20, 2), generator=g).to(DEV)
+    d40, d16 = normal(g, 40, 24).to(DEV), normal(g, 40, 16).to(DEV)
+    weight = normal(g, 20, 2).to(DEV).requires_grad_()
+    route = G.RowRoute(e, 3)
+    x20 = normal(g, 20, 24).to(DEV).requires_grad_()
+    d20, d80 = normal(g, 20, 24).to(DEV), normal(g, 40, 24).to(DEV)
+    cases = [(lambda: G.layer_norm(x), x, d40), (lambda: G.segment_matmul(x.detach(), w, route.offsets), w, d16),
+             (lambda: G.combine(route, x.detach(), weight), weight, d20), (lambda: G.dispatch(route, x20), x20, d80)]
+    for call, leaf, d in cases:
+        alive = call()
+        want, = torch.autograd.grad(call(), leaf, d)
+        torch.cuda.synchronize()
+        refused = torch.cuda.CUDAGraph()
+        with pytest.raises(RuntimeError, match="stream outside the capture"):
+            with torch.cuda.graph(refused, capture_error_mode="thread_local"):
+                torch.autograd.grad(call(), leaf, d)
+        del alive
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, capture_error_mode="thread_local"):
+            got, = torch.autograd.grad(call(), leaf, d)
+        for _ in range(3):
+            got.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(got, want)
+
+
 def test_another_stream():
     expert, p, dout, E = block_inputs(T=400)
     leaves = [t.to(DEV).requires_grad_() for t in p]
