@@ -230,7 +230,7 @@ struct Reader {
                 at[i] = k * B * 2 + ((piece ^ ((k & 3) << 1)) << 5) + ((l & 3) << 3);
             }
         } else {
-at[0] = half * 4 * B * 4 + m * 4;
+            at[0] = half * 4 * B * 4 + m * 4;
         }
 #pragma unroll
         for (int &o : at) asm volatile("" : "+v"(o));
@@ -341,6 +341,14 @@ __device__ inline void tile_product(const Stages &lds, const Operand<T> &a, cons
         Copy<T, AKC, S::BM, S::kWaves> ca(a, wave);
         Copy<T, BKC, S::BN, S::kWaves> cb(b, wave);
         constexpr int kCopies = decltype(ca)::kCopies + decltype(cb)::kCopies;
+        // dw's large tiles have twice the LDS reads of y's: one copy (0x20) and
+        // an even share of the reads (0x100) are put before each product (0x8)
+        // (65,536 rows in 32 segments, 1024 x 2048 bf16: 282 -> 271 us, in 8,
+        // 2048 x 4096: 882 -> 853 us).  y and dx gain 3% or lose it by the
+        // sizes, and keep the compiler's order.
+        constexpr bool kSpread = S::BM == 256 && !AKC && !BKC;
+        constexpr int kProducts = kParts * MI * NI, kReads = kParts * (MI + NI) * 2;
+        constexpr int kPerProduct = (kReads + kProducts - 1) / kProducts;
         Operands set[2];
         auto copy_step = [&](LdsByte *to) {
             ca.step(to, wave);
@@ -351,6 +359,14 @@ __device__ inline void tile_product(const Stages &lds, const Operand<T> &a, cons
             copy_step(lds.at[u]);
             read_step(lds.at[(u + 1) % kStages], set[(u + 1) & 1]);
             multiply_step(set[u & 1]);
+            if constexpr (kSpread) {
+#pragma unroll
+                for (int i = 0; i < kProducts; ++i) {
+                    if (i * kPerProduct < kReads) __builtin_amdgcn_sched_group_barrier(0x100, kPerProduct, 0);
+                    if (i < kCopies) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                }
+            }
             __builtin_amdgcn_sched_barrier(0);
         };
 #pragma unroll
