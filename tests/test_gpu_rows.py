@@ -91,7 +91,8 @@ def plain_route(e, E):
     (65, 2, 511, "some"), (512, 2, 511, "all"), (513, 2, 7, "some"), (1024, 4, 64, "one"), (1365, 3, 64, "some"),
     (4096, 1, 511, "some"), (4097, 1, 100, "all"), (2048, 8, 16, "none"), (16384, 1, 511, "some"), (16385, 1, 511, "some"),
     (300, 2, 512, "all"), (5000, 2, 2048, "some"), (40000, 3, 33, "some"), (70001, 8, 255, "all"),
-    (300007, 2, 3, "one"), (1100000, 4, 129, "some")])
+    (300007, 2, 3, "one"), (1100000, 4, 129, "some"),
+    (262144, 2, 64, "one"), (131073, 4, 1024, "some"), (131073, 4, 1025, "some"), (600001, 1, 200, "none")])
 def test_route(T, k, E, kind):
     log(f"route T={T} k={k} E={E} {kind}")
     e = pairs_of(rng(T, k, E), T, k, E, kind)
