@@ -22,8 +22,8 @@
 // size crosses to the host and a captured call follows new offsets.
 //
 // Measured, medians of the kernels alone: 65,536 rows in 32 segments, 1024 x
-// 2048 bf16, y 344 us, dx 345 us (0.8 PFLOP/s), dw 290 us (0.95), matrix cores
-// 47%, 47% and 53% busy: a block to a unit, so the first copies and the last
+// 2048 bf16, y 343 us, dx 336 us (0.8 PFLOP/s), dw 281 us (0.98), matrix cores
+// 47%, 47% and 52% busy: a block to a unit, so the first copies and the last
 // stores of a tile are not covered.  150,001 rows in 7, 128 x 256 fp32: y 125,
 // dx 112, dw 99 + 11 us (79 to 99 TFLOP/s of the 154 that a large fp32 product
 // reaches).  96 rows in 16, 1024 x 2048 bf16: 14 us, the weights' 67 MB at 4.8
