@@ -147,22 +147,30 @@ void refuse_leaves_outside_capture(const Tensor &grad) {
 }
 
 // Gradients that would themselves be differentiated raise when that happens.
-variable_list once(const variable_list &grads, variable_list outputs) {
+// reads[i]: the inputs of the node, by their place among its edges, that output
+// i depends on next to the incoming gradients.  What raises stands between the
+// output and the graphs of all of these, so that the way to any one of them
+// leads through it: a graph of the output alone is not walked where only an
+// input's gradient is asked for.
+using Reads = std::initializer_list<size_t>;
+
+variable_list once(const variable_list &grads, variable_list outputs, std::initializer_list<Reads> reads) {
     if (!at::GradMode::is_enabled()) return outputs;
-    bool again = false;
-    for (const Tensor &g : grads) again |= g.defined() && g.requires_grad();
-    if (!again) return outputs;
-    std::vector<size_t> at;
-    variable_list given;
-    for (size_t i = 0; i < outputs.size(); ++i)
-        if (outputs[i].defined()) {
-            at.push_back(i);
-            given.push_back(outputs[i].detach().requires_grad_());
-        }
-    auto error = std::make_shared<torch::autograd::DelayedError>(
-        "trying to differentiate twice a row operator, which is differentiable once", (int64_t)given.size());
-    given = (*error)(std::move(given));
-    for (size_t i = 0; i < at.size(); ++i) outputs[at[i]] = given[i];
+    const auto node = torch::autograd::get_current_node();
+    size_t i = 0;
+    for (const Reads &inputs : reads) {
+        Tensor &out = outputs[i++];
+        if (!out.defined()) continue;
+        torch::autograd::edge_list from;
+        for (const Tensor &g : grads)
+            if (g.defined() && g.requires_grad()) from.push_back(torch::autograd::impl::gradient_edge(g));
+        for (const size_t at : inputs)                           // an input without a gradient has no function
+            if (node->next_edge(at).is_valid()) from.push_back(node->next_edge(at));
+        if (!from.empty())
+            torch::autograd::create_gradient_edge(
+                out, std::make_shared<torch::autograd::Error>(
+                         "trying to differentiate twice a row operator, which is differentiable once", std::move(from)));
+    }
     return outputs;
 }
 
@@ -236,7 +244,7 @@ struct Dispatch : torch::autograd::Function<Dispatch> {
         const Tensor dxs = grads[0].contiguous();
         const Tensor dx = at::empty({r.T, dxs.size(1)}, dxs.options());
         run_combine(r, dxs, {}, SPMM_F32, dx);
-        return once(grads, {dx, Tensor()});
+        return once(grads, {dx, Tensor()}, {{}});
     }
 };
 
@@ -281,7 +289,8 @@ struct Combine : torch::autograd::Function<Combine> {
         } else if (drows.defined()) {
             run_dispatch(r, dout, weight, wtype, drows);
         }
-        return once(grads, {drows, dweight, Tensor()});
+        const Reads weights = {1}, none = {};
+        return once(grads, {drows, dweight, Tensor()}, {weight.defined() ? weights : none, {0}});
     }
 };
 
@@ -335,7 +344,7 @@ struct SegmentMatmul : torch::autograd::Function<SegmentMatmul> {
             check(spmm_segment_product_dw(ptr(x), ptr(dy), ptr<int64_t>(offsets), ptr(dw), R, E, I, O, code(dy),
                                           ptr(work), bytes, stream_of(dy)));
         }
-        return once(grads, {dx, dw, Tensor()});
+        return once(grads, {dx, dw, Tensor()}, {{1}, {0}});
     }
 };
 
@@ -399,7 +408,8 @@ struct LayerNorm : torch::autograd::Function<LayerNorm> {
         float *mean = ptr<float>(stats);
         check(spmm_layer_norm_backward(ptr(dy), ptr(x), ptr(weight), wtype, mean, mean ? mean + R : nullptr, ptr(dx),
                                        ptr(dweight), ptr(dbias), R, N, code(x), ptr(work), bytes, stream_of(x)));
-        return once(grads, {dx, dweight, dbias, Tensor()});
+        const Reads both = {0, 1}, first = {0};
+        return once(grads, {dx, dweight, dbias, Tensor()}, {weight.defined() ? both : first, {0}, {}});
     }
 };
 
