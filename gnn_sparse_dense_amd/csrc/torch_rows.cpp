@@ -366,21 +366,27 @@ int norm_weight_type(const Tensor &x, const Tensor &weight, const Tensor &bias) 
     return weight.defined() ? code(weight) : bias.defined() ? code(bias) : code(x);
 }
 
+// Rows of x [..., N].
+int64_t norm_rows(const Tensor &x) { return x.size(-1) ? x.numel() / x.size(-1) : 0; }
+
 // stats: fp32 [2, R], mean and 1 / deviation of each row, or undefined.
 Tensor normed(const Tensor &x, const Tensor &weight, const Tensor &bias, double eps, const Tensor &stats) {
-    const Tensor y = at::empty_like(x);
+    const Tensor y = at::empty(x.sizes(), x.options());
+    const int64_t R = norm_rows(x);
     float *mean = ptr<float>(stats);
     check(spmm_layer_norm(ptr(x), ptr(weight), ptr(bias), norm_weight_type(x, weight, bias), ptr(y), mean,
-                          mean ? mean + x.size(0) : nullptr, x.size(0), x.size(1), eps, code(x), stream_of(x)));
+                          mean ? mean + R : nullptr, R, x.size(-1), eps, code(x), stream_of(x)));
     return y;
 }
 
+// The node takes x as it was given, so that a leaf of any number of dimensions
+// is next to it (refuse_leaves_outside_capture).
 struct LayerNorm : torch::autograd::Function<LayerNorm> {
     static Tensor forward(AutogradContext *ctx, const Tensor &x_, const std::optional<Tensor> &weight_,
                           const std::optional<Tensor> &bias_, double eps) {
         const Tensor x = x_.contiguous();
         const Tensor weight = packed(weight_.value_or(Tensor())), bias = packed(bias_.value_or(Tensor()));
-        const Tensor stats = at::empty({2, x.size(0)}, x.options().dtype(at::kFloat));
+        const Tensor stats = at::empty({2, norm_rows(x)}, x.options().dtype(at::kFloat));
         ctx->save_for_backward({x, weight, stats});
         ctx->saved_data["wtype"] = (int64_t)norm_weight_type(x, weight, bias);
         ctx->saved_data["bias"] = bias.defined();
@@ -393,9 +399,9 @@ struct LayerNorm : torch::autograd::Function<LayerNorm> {
         const Tensor &x = saved[0], &weight = saved[1], &stats = saved[2], dy = grads[0].contiguous();
         const int wtype = (int)ctx->saved_data["wtype"].toInt();
         const auto wopts = x.options().dtype(wtype == SPMM_F32 ? at::kFloat : x.scalar_type());
-        const int64_t R = x.size(0), N = x.size(1);
+        const int64_t R = norm_rows(x), N = x.size(-1);
         Tensor dx, dweight, dbias, work;
-        if (ctx->needs_input_grad(0)) dx = at::empty_like(x);
+        if (ctx->needs_input_grad(0)) dx = at::empty(x.sizes(), x.options());
         // an input that is not given has no place among the edges
         const size_t after = weight.defined() ? 2 : 1;
         if (weight.defined() && ctx->needs_input_grad(1)) dweight = at::empty({N}, wopts);
@@ -431,11 +437,8 @@ Tensor layer_norm(const Tensor &x, const std::optional<Tensor> &weight_, const s
         throw py::type_error("weight (" + name_of(weight.scalar_type()) + ") and bias (" +
                              name_of(bias.scalar_type()) + ") must have one type");
     check_like("x", x, x.sizes(), x.device());
-    const Tensor rows = x.dim() == 2 ? x : x.reshape({N ? x.numel() / N : 0, N});
-    const Tensor y = wants_grad(rows, weight, bias)
-                         ? LayerNorm::apply(rows, weight_, bias_, eps)
-                         : normed(rows.contiguous(), packed(weight), packed(bias), eps, {});
-    return x.dim() == 2 ? y : y.reshape(x.sizes());
+    return wants_grad(x, weight, bias) ? LayerNorm::apply(x, weight_, bias_, eps)
+                                       : normed(x.contiguous(), packed(weight), packed(bias), eps, {});
 }
 
 }  // namespace
