@@ -18,8 +18,9 @@
 // (fp32).
 //
 // The row operands' tiles come from the segment bounds on the device: tile
-// number -> segment by a wave-wide scan over the segments' tile counts, so no
-// size crosses to the host and a captured call follows new offsets.
+// number -> segment by a wave-wide scan over the segments' tile counts, or by a
+// search where there are many, so no size crosses to the host and a captured
+// call follows new offsets.
 //
 // Measured, medians of the kernels alone: 65,536 rows in 32 segments, 1024 x
 // 2048 bf16, y 343 us, dx 336 us (0.8 PFLOP/s), dw 281 us (0.98), matrix cores
@@ -571,6 +572,40 @@ __device__ inline RowTile find_tile(const SegmentArgs &a, int64_t v0, int64_t v1
     }
 }
 
+// The same for many runs, where counting the pieces of all of them in every
+// wave would cost the square of their number.  Run v, from row lo, owns the
+// slots from lo / LEN + v on to the next run's: at least as many as it has
+// pieces, since ceil(n / LEN) <= floor((lo + n) / LEN) - floor(lo / LEN) + 1.
+// The slots' run is found by a search that looks at 64 runs at a time; the
+// slots that a run does not need hold no rows.  From 127 segments on, more than
+// two scans (segments of uneven lengths, 64 x 64 bf16): 40 rows to a segment, 126
+// segments 8.5 us both ways, 190 9.3 -> 9.0, 512 23 -> 12, 2000 147 -> 29, 65,536
+// segments 224 -> 2.2 ms; 400 rows to a segment, 126 11.9 -> 12.6 us, 190 17.7 ->
+// 15.0, 512 79 -> 50, 2000 591 -> 168.
+constexpr int kScannedSegments = 126;
+
+template <int LEN>
+__device__ inline RowTile find_slot(const SegmentArgs &a, int64_t cols, int64_t id, int64_t total) {
+    const int lane = threadIdx.x & (kWave - 1);
+    const int64_t at = xcd_order(id, total);
+    RowTile t;
+    t.piece = at / cols;
+    t.col = at % cols;
+    int64_t v = 0, n = a.E + 2;                      // the run is one of n from v on
+    while (n > 1) {
+        const int64_t step = (n + kWave - 1) / kWave, to = lane * step;
+        const bool from = lane == 0 || (to < n && run_bound(a, v + to) / LEN + v + to <= t.piece);
+        const int64_t past = (kWave - 1 - __builtin_clzll(__ballot(from))) * step;
+        v += past;
+        n = min(step, n - past);
+    }
+    const int64_t lo = run_bound(a, v);
+    t.run = uniform(v);
+    t.row = uniform(lo + (t.piece - lo / LEN - v) * LEN);
+    t.end = uniform(run_bound(a, v + 1));
+    return t;
+}
+
 template <typename T, typename S, bool TRANSPOSED, bool DIRECT>
 __global__ __launch_bounds__(S::kThreads, 2) void segment_kernel(SegmentArgs a, int64_t col_tiles, int64_t total,
                                                                 bool stream) {
@@ -578,8 +613,14 @@ __global__ __launch_bounds__(S::kThreads, 2) void segment_kernel(SegmentArgs a, 
     const int64_t K = TRANSPOSED ? a.O : a.I, N = TRANSPOSED ? a.I : a.O;
     const T *in = (const T *)(TRANSPOSED ? a.dy : a.x), *w = (const T *)a.w;
     for (int64_t id = blockIdx.x; id < total; id += gridDim.x) {
-        const RowTile rt = find_tile(a, 0, a.E + 2, S::BM, col_tiles, id, total);
-        if (rt.run < 0) return;
+        RowTile rt;
+        if (a.E > kScannedSegments) {
+            rt = find_slot<S::BM>(a, col_tiles, id, total);
+            if (rt.row < 0 || rt.row >= rt.end) continue;
+        } else {
+            rt = find_tile(a, 0, a.E + 2, S::BM, col_tiles, id, total);
+            if (rt.run < 0) return;
+        }
         const int64_t run = uniform(rt.run), row = uniform(rt.row), n0 = rt.col * S::BN;
         T *out = (T *)a.y + row * N + n0;
         const int64_t rows = uniform(rt.end) - row;

@@ -30,3 +30,17 @@ def dw_shape(R, E, I, O, size, aligned=True):
         return tile, tiles, 0, 0
     chunk = ceil(max(256, ceil(R, max(1, 2 * UNITS // tiles))), 32) * 32
     return tile, tiles, chunk, R // chunk + E
+
+
+def slot_of(bounds, R, length, piece):
+    """Run, first row and end of the rows of slot `piece` (first >= end: none).
+    Runs are the rows before the segments, the segments, the rows behind them;
+    the search keeps the last of 64 probes that does not lie behind the slot."""
+    at = [0, *(min(max(b, 0), R) for b in bounds), R]
+    v, n = 0, len(at) - 1
+    while n > 1:
+        step = ceil(n, 64)
+        lane = next(i for i in range(63, -1, -1) if i == 0 or (i * step < n and at[v + i * step] // length + v + i * step <= piece))
+        v += lane * step
+        n = min(step, n - lane * step)
+    return v, at[v] + (piece - at[v] // length - v) * length, at[v + 1]

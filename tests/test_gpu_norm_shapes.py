@@ -74,17 +74,14 @@ def check(R, N, kind, wtype):
     close(grads[2], D.sum(0), rows * U * D.abs().sum(0), wtype, "dbias")
 
 
-@pytest.mark.parametrize("weights", ["fp32", "own"])
-@pytest.mark.parametrize("kind", sorted(TYPES))
+@pytest.mark.parametrize("kind,weights", [("fp32", "fp32"), ("bf16", "fp32"), ("bf16", "bf16"), ("fp16", "fp32"),
+                                          ("fp16", "fp16")])
 @pytest.mark.parametrize("packs", BORDERS)
 def test_layer_norm_around_each_border(packs, kind, weights):
     """Whole packs, one element more and one less; 37 rows end inside a block."""
-    if kind == "fp32" and weights == "own":
-        pytest.skip("fp32 is the rows' own type")
-    wtype = torch.float32 if weights == "fp32" else TYPES[kind]
     for more in (-1, 0, 1):
         log(f"norm N={packs * PACK[kind] + more} {kind} weights={weights}")
-        check(37, packs * PACK[kind] + more, kind, wtype)
+        check(37, packs * PACK[kind] + more, kind, TYPES[weights])
 
 
 def rows_for_turns(packs):

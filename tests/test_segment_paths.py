@@ -1,11 +1,12 @@
 """The model of the segment product's paths against the library's workspace,
 and the paths that the GPU tests' shapes take."""
 import ctypes
+import random
 
 import pytest
 
 import gnn_sparse_dense_amd as G
-from tests.segment_paths import direct, dw_shape, product_tile
+from tests.segment_paths import direct, dw_shape, product_tile, slot_of
 from tests.test_gpu_segment_paths import DW_CHUNKS, DW_LARGE, PRODUCT
 
 
@@ -37,3 +38,28 @@ def test_shapes_of_the_gpu_tests_reach_their_paths():
     for t in (0, 1):
         assert any(p[t][0] == 256 and p[t][1] > 8 for p in large)
         assert {p[t][1] % 4 for p in large if p[t][0] == 256} >= {1, 2, 3}
+
+
+@pytest.mark.parametrize("E,most", [(1, 900), (63, 700), (64, 20), (300, 90), (4200, 2)])
+@pytest.mark.parametrize("length", [128, 256])
+def test_every_piece_of_a_run_has_a_slot(E, most, length):
+    """Slots of the search against the runs cut one after another."""
+    g = random.Random(E + most)
+    for empty in ((0.0, 0.5, 1.0) if E < 1000 else (0.5,)):
+        bounds = [g.randint(0, 300)]
+        for _ in range(E):
+            bounds.append(bounds[-1] + (0 if g.random() < empty else g.randint(0, most)))
+        R = bounds[-1] + g.choice([0, 1, 500])
+        want = [(v, row, hi) for v, (lo, hi) in enumerate(zip([0, *bounds], [*bounds, R])) for row in range(lo, hi, length)]
+        slots = [slot_of(bounds, R, length, s) for s in range(R // length + E + 2)]
+        assert [s for s in slots if s[1] < s[2]] == want
+
+
+def test_slots_of_bounds_out_of_order_stay_inside():
+    g = random.Random(5)
+    for _ in range(30):
+        R, E = g.randint(0, 5000), g.randint(1, 200)
+        bounds = [g.choice([-7, 0, R, 2 ** 40, g.randint(0, R)]) for _ in range(E + 1)]
+        for s in range(R // 128 + E + 2):
+            v, row, end = slot_of(bounds, R, 128, s)
+            assert 0 <= v <= E + 1 and row >= 0 and end <= R
