@@ -10,12 +10,13 @@
 #include <c10/hip/HIPGraphsC10Utils.h>
 #include <c10/hip/HIPGuard.h>
 #include <c10/hip/HIPStream.h>
-#include <torch/csrc/autograd/functions/accumulate_grad.h>
 #include <torch/csrc/autograd/functions/basic_ops.h>
 #include <torch/extension.h>
 
 #include <stdexcept>
 #include <string>
+#include <unordered_set>
+#include <vector>
 
 #include "spmm.h"
 
@@ -127,22 +128,32 @@ bool capturing(const c10::hip::HIPStream &stream) {
     return c10::hip::currentStreamCaptureStatusMayInitCtx() != c10::hip::CaptureStatus::None;
 }
 
-// torch hands a leaf's gradient over on the stream of the leaf's first use, as
-// long as a graph of the leaf lives.  Where this backward pass is captured and
-// that stream is not, the hand-over would tie the capture to a stream outside
-// of it, which ends the process: refused before the gradient exists.
-void refuse_leaves_outside_capture(const Tensor &grad) {
+// torch hands a gradient over on the stream of the node that takes it, and a
+// leaf's on the stream of its first use, as long as a graph of the leaf lives.
+// Where this backward pass is captured and such a stream is not, the hand-over
+// would tie the capture to a stream outside of it, which ends the process:
+// refused before the gradient exists, for every node that this pass still
+// leads to from here, torch's among them.
+void refuse_nodes_outside_capture(const Tensor &grad) {
     if (!capturing(c10::hip::getCurrentHIPStream(grad.get_device()))) return;
     const auto node = torch::autograd::get_current_node();
-    for (size_t i = 0; node && i < node->num_outputs(); ++i) {
-        const auto &leaf = node->next_edge(i).function;
-        if (!node->task_should_compute_output(i) || !dynamic_cast<torch::autograd::AccumulateGrad *>(leaf.get()))
-            continue;
-        const auto stream = leaf->stream();
-        if (stream && !capturing(c10::hip::HIPStreamMasqueradingAsCUDA(*stream).hip_stream()))
-            throw std::runtime_error(
-                "backward of a row operator is captured while a graph of the same leaf lives that was built on a "
-                "stream outside the capture: drop that graph first");
+    std::vector<torch::autograd::Node *> todo;
+    std::unordered_set<torch::autograd::Node *> seen;
+    if (node) todo.push_back(node.get());
+    while (!todo.empty()) {
+        torch::autograd::Node *from = todo.back();
+        todo.pop_back();
+        for (size_t i = 0; i < from->num_outputs(); ++i) {
+            if (!from->task_should_compute_output(i)) continue;
+            torch::autograd::Node *to = from->next_edge(i).function.get();
+            if (!seen.insert(to).second) continue;
+            const auto stream = to->stream();
+            if (stream && !capturing(c10::hip::HIPStreamMasqueradingAsCUDA(*stream).hip_stream()))
+                throw std::runtime_error(
+                    "backward of a row operator is captured while a graph of the same leaf lives that was built on a "
+                    "stream outside the capture: drop that graph first");
+            todo.push_back(to);
+        }
     }
 }
 
@@ -239,7 +250,7 @@ struct Dispatch : torch::autograd::Function<Dispatch> {
     }
 
     static variable_list backward(AutogradContext *ctx, variable_list grads) {
-        refuse_leaves_outside_capture(grads[0]);
+        refuse_nodes_outside_capture(grads[0]);
         const Route r = kept(ctx, ctx->get_saved_variables());
         const Tensor dxs = grads[0].contiguous();
         const Tensor dx = at::empty({r.T, dxs.size(1)}, dxs.options());
@@ -274,7 +285,7 @@ struct Combine : torch::autograd::Function<Combine> {
     }
 
     static variable_list backward(AutogradContext *ctx, variable_list grads) {
-        refuse_leaves_outside_capture(grads[0]);
+        refuse_nodes_outside_capture(grads[0]);
         const variable_list saved = ctx->get_saved_variables();
         const Route r = kept(ctx, saved);
         const Tensor &rows = saved[0], &weight = saved[1], dout = grads[0].contiguous();
@@ -325,7 +336,7 @@ struct SegmentMatmul : torch::autograd::Function<SegmentMatmul> {
     }
 
     static variable_list backward(AutogradContext *ctx, variable_list grads) {
-        refuse_leaves_outside_capture(grads[0]);
+        refuse_nodes_outside_capture(grads[0]);
         const variable_list saved = ctx->get_saved_variables();
         const Tensor &x = saved[0], &w = saved[1], &offsets = saved[2], dy = grads[0].contiguous();
         const auto shape = ctx->saved_data["shape"].toIntVector();
@@ -379,8 +390,7 @@ Tensor normed(const Tensor &x, const Tensor &weight, const Tensor &bias, double 
     return y;
 }
 
-// The node takes x as it was given, so that a leaf of any number of dimensions
-// is next to it (refuse_leaves_outside_capture).
+// The node takes x as it was given: no view stands between it and a leaf.
 struct LayerNorm : torch::autograd::Function<LayerNorm> {
     static Tensor forward(AutogradContext *ctx, const Tensor &x_, const std::optional<Tensor> &weight_,
                           const std::optional<Tensor> &bias_, double eps) {
@@ -394,7 +404,7 @@ struct LayerNorm : torch::autograd::Function<LayerNorm> {
     }
 
     static variable_list backward(AutogradContext *ctx, variable_list grads) {
-        refuse_leaves_outside_capture(grads[0]);
+        refuse_nodes_outside_capture(grads[0]);
         const variable_list saved = ctx->get_saved_variables();
         const Tensor &x = saved[0], &weight = saved[1], &stats = saved[2], dy = grads[0].contiguous();
         const int wtype = (int)ctx->saved_data["wtype"].toInt();

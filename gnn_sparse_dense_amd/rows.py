@@ -12,7 +12,7 @@ once.  All five run on torch's current stream of the tensors' device,
 allocate through torch and never wait for the GPU, so they can be captured
 into a graph (a backward pass only while no eager graph of the same leaves
 lives, since torch ties a leaf's gradient to the stream it was first used on:
-refused for leaves that these operators read directly).
+refused for every leaf that the pass leads to from one of these operators).
 dispatch, combine, segment_matmul and layer_norm are differentiable (once);
 the spmm_* functions are the C calls on the caller's tensors.
 """

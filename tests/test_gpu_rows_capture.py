@@ -1,5 +1,6 @@
-"""Backward passes of the layer norm that are captured into a graph: inputs of
-any number of dimensions, and torch's own mode of capture."""
+"""Backward passes of the row operators that are captured into a graph, in
+torch's own mode of capture: inputs of any number of dimensions, and leaves
+behind torch's operations."""
 import pytest
 import torch
 
@@ -41,6 +42,60 @@ def test_captured_backward_beside_an_eager_graph_is_refused_in_any_dimensions(sh
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         got, = torch.autograd.grad(G.layer_norm(x), x, dy)
+    for _ in range(3):
+        got.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+
+
+def test_captured_backward_to_leaves_behind_torch_operations_is_refused():
+    """The eager graph's leaf stands behind a cast, a product or a reshape."""
+    g = rng(77)
+    x, w = normal(g, 20, 24).to(DEV).requires_grad_(), normal(g, 3, 24, 16).to(DEV).requires_grad_()
+    weight = normal(g, 20, 2).to(DEV).requires_grad_()
+    r = G.RowRoute(torch.randint(0, 3, (20, 2), generator=g).to(DEV), 3)
+    rows = normal(g, 40, 24).to(DEV)
+    half, d24, d40 = torch.bfloat16, normal(g, 20, 24).to(DEV), normal(g, 40, 24).to(DEV)
+    d16 = normal(g, 40, 16).to(DEV).to(half)
+    cases = [(lambda: G.layer_norm(x * 2), x, d24), (lambda: G.layer_norm((x * 2).view(2, 10, 24)), x, d24.view(2, 10, 24)),
+             (lambda: G.segment_matmul(rows.to(half), w.to(half), r.offsets), w, d16),
+             (lambda: G.combine(r, rows, torch.softmax(weight, 1)), weight, d24), (lambda: G.dispatch(r, x + 1), x, d40)]
+    for call, leaf, d in cases:
+        alive = leaf * 1
+        want, = torch.autograd.grad(call(), leaf, d)
+        torch.cuda.synchronize()
+        with pytest.raises(RuntimeError, match="stream outside the capture"):
+            with torch.cuda.graph(torch.cuda.CUDAGraph()):
+                torch.autograd.grad(call(), leaf, d)
+        del alive
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got, = torch.autograd.grad(call(), leaf, d)
+        for _ in range(3):
+            got.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(got, want)
+
+
+def test_captured_backward_to_an_eager_result_is_refused():
+    """The gradient of what was computed outside the capture goes to a node of
+    that stream; the same values as a leaf of their own are captured."""
+    x, d = normal(rng(78), 20, 24).to(DEV).requires_grad_(), normal(rng(79), 20, 24).to(DEV)
+    eager = x * 2
+    want, = torch.autograd.grad(G.layer_norm(eager), eager, d, retain_graph=True)
+    torch.cuda.synchronize()
+    for wanted in (eager, x):
+        with pytest.raises(RuntimeError, match="stream outside the capture"):
+            with torch.cuda.graph(torch.cuda.CUDAGraph()):
+                torch.autograd.grad(G.layer_norm(eager), wanted, d, retain_graph=True)
+        torch.cuda.synchronize()
+    leaf = eager.detach().requires_grad_()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got, = torch.autograd.grad(G.layer_norm(leaf), leaf, d)
     for _ in range(3):
         got.zero_()
         graph.replay()
