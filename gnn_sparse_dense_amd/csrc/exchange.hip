@@ -25,8 +25,11 @@
 // us with plain, 72 us with non-temporal stores, 69 us with loads as well (4.9
 // TB/s); gradients by source row 134 us, by output row 118 us (5.1 TB/s).
 // 50,021 x 1433 fp16 rows, k = 3: dispatch by source row 239 us, by output
-// row in packs of one row 218 us, in aligned packs 190 us (3.0 TB/s; at width
-// 1432, with aligned loads, 143 us); combine 143, 136 and 147 us.
+// row in packs of one row 218 us, in aligned packs 190 us (at width 1432, with
+// aligned loads, 143 us); combine 143, 136 and 147 us.  Those are figures of one
+// occasion each.  Loops of one call as the kernels stand: dispatch 140, combine
+// 132, gradients 205 us, at width 1432 125, 110 and 196 us; dispatch between
+// other kernels 167 us.
 #include "rows.h"
 
 #include <algorithm>

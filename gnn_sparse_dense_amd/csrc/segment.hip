@@ -22,13 +22,13 @@
 // search where there are many, so no size crosses to the host and a captured
 // call follows new offsets.
 //
-// Measured, medians of the kernels alone: 65,536 rows in 32 segments, 1024 x
-// 2048 bf16, y 343 us, dx 336 us (0.8 PFLOP/s), dw 281 us (0.98), matrix cores
-// 47%, 47% and 52% busy: a block to a unit, so the first copies and the last
-// stores of a tile are not covered.  150,001 rows in 7, 128 x 256 fp32: y 125,
-// dx 112, dw 99 + 11 us (79 to 99 TFLOP/s of the 154 that a large fp32 product
-// reaches).  96 rows in 16, 1024 x 2048 bf16: 14 us, the weights' 67 MB at 4.8
-// TB/s.
+// Measured, medians of the kernels alone under the profiler: 65,536 rows in 32
+// segments, 1024 x 2048 bf16, y 310 us, dx 312 us (0.88 PFLOP/s), dw 259 us
+// (1.06), matrix cores 45%, 45% and 52% busy: a block to a unit, so the first
+// copies and the last stores of a tile are not covered.  150,001 rows in 7, 128 x
+// 256 fp32: y 124, dx 110, dw 98 + 11 us (79 to 101 TFLOP/s of the 154 that a
+// large fp32 product reaches).  96 rows in 16, 1024 x 2048 bf16: 14 us, the
+// weights' 67 MB at 4.9 TB/s.
 #include "rows.h"
 
 #include <algorithm>
@@ -344,8 +344,8 @@ __device__ inline void tile_product(const Stages &lds, const Operand<T> &a, cons
         constexpr int kCopies = decltype(ca)::kCopies + decltype(cb)::kCopies;
         // dw's large tiles have twice the LDS reads of y's: one copy (0x20) and
         // an even share of the reads (0x100) are put before each product (0x8)
-        // (65,536 rows in 32 segments, 1024 x 2048 bf16: 282 -> 271 us, in 8,
-        // 2048 x 4096: 882 -> 853 us).  y and dx gain 3% or lose it by the
+        // (loops of one call, 65,536 rows in 32 segments, 1024 x 2048 bf16: 282 ->
+        // 271 us, in 8, 2048 x 4096: 882 -> 853 us).  y and dx gain 3% or lose it by the
         // sizes, and keep the compiler's order.
         constexpr bool kSpread = S::BM == 256 && !AKC && !BKC;
         constexpr int kProducts = kParts * MI * NI, kReads = kParts * (MI + NI) * 2;
@@ -665,7 +665,7 @@ __device__ inline int64_t segment_by_length(const SegmentArgs &a, int rank) {
 }
 
 // dw.  chunk == 0: tile (segment, tile of [I, O]) over all rows of the
-// segment; the longest segments start first.  chunk > 0: tile (chunk of a
+// segment; of up to 64 segments the longest start first.  chunk > 0: tile (chunk of a
 // segment's rows, tile of [I, O]) into fp32 partial sums, one [I, O] for each
 // chunk in the order of the segments.
 template <typename T, typename OUT, typename S, bool DIRECT>
@@ -736,8 +736,12 @@ constexpr int64_t kMaxBlocks = 1 << 20;
 constexpr int64_t kUnits = 256;                      // compute units
 
 // Non-temporal stores where a call moves more than half of the 256 MB Infinity
-// Cache (65,536 x 1024 x 2048 bf16: 334 -> 289 us; 256 summed elements: 178 ->
-// 115 us): the operands that other tiles read again stay there.
+// Cache, so that the operands that other tiles read again stay there.  65,536
+// rows, 1024 x 2048 bf16, calls of both kinds and directions in turn: 32 segments
+// y 308 -> 302, dx 292 -> 278 us; one segment 296 -> 289 and 274 -> 267, with 256
+// summed elements 130 -> 122 and 118 -> 110.  In a loop of one call, whose
+// outputs would push out its own operands, one segment's y 319 -> 269 to 293 and
+// 143 -> 110 to 136 us.
 constexpr int64_t kStreamBytes = int64_t(128) << 20;
 
 template <typename T>
