@@ -10,6 +10,7 @@
 #include <c10/hip/HIPGraphsC10Utils.h>
 #include <c10/hip/HIPGuard.h>
 #include <c10/hip/HIPStream.h>
+#include <torch/csrc/autograd/functions/accumulate_grad.h>
 #include <torch/csrc/autograd/functions/basic_ops.h>
 #include <torch/extension.h>
 
@@ -130,10 +131,13 @@ bool capturing(const c10::hip::HIPStream &stream) {
 
 // torch hands a gradient over on the stream of the node that takes it, and a
 // leaf's on the stream of its first use, as long as a graph of the leaf lives.
-// Where this backward pass is captured and such a stream is not, the hand-over
-// would tie the capture to a stream outside of it, which ends the process:
-// refused before the gradient exists, for every node that this pass still
-// leads to from here, torch's among them.
+// Where this backward pass is captured and that is the default stream, the
+// hand-over would tie the capture to a stream that cannot be captured, which
+// ends the process: refused before the gradient exists, for every node that this
+// pass still leads to from here, torch's among them.  A leaf's stream of another
+// kind joins the capture, and torch joins it back at the end of the pass (its
+// own graphed callables keep such graphs of their warm-up); other nodes' streams
+// it does not join back, so those are refused too.
 void refuse_nodes_outside_capture(const Tensor &grad) {
     if (!capturing(c10::hip::getCurrentHIPStream(grad.get_device()))) return;
     const auto node = torch::autograd::get_current_node();
@@ -147,11 +151,14 @@ void refuse_nodes_outside_capture(const Tensor &grad) {
             if (!from->task_should_compute_output(i)) continue;
             torch::autograd::Node *to = from->next_edge(i).function.get();
             if (!seen.insert(to).second) continue;
-            const auto stream = to->stream();
-            if (stream && !capturing(c10::hip::HIPStreamMasqueradingAsCUDA(*stream).hip_stream()))
-                throw std::runtime_error(
-                    "backward of a row operator is captured while a graph of the same leaf lives that was built on a "
-                    "stream outside the capture: drop that graph first");
+            if (const auto stream = to->stream()) {
+                const auto on = c10::hip::HIPStreamMasqueradingAsCUDA(*stream).hip_stream();
+                const bool leaf = dynamic_cast<torch::autograd::AccumulateGrad *>(to);
+                if (!(leaf && on.stream()) && !capturing(on))
+                    throw std::runtime_error(
+                        "backward of a row operator is captured while a graph of the same leaf lives that was built on "
+                        "a stream outside the capture: drop that graph first");
+            }
             todo.push_back(to);
         }
     }

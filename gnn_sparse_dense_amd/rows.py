@@ -11,8 +11,9 @@ Rows are fp32, bf16 or fp16 matrices; sums are fp32 and outputs are rounded
 once.  All five run on torch's current stream of the tensors' device,
 allocate through torch and never wait for the GPU, so they can be captured
 into a graph (a backward pass only while no eager graph of the same leaves
-lives, since torch ties a leaf's gradient to the stream it was first used on:
-refused for every leaf that the pass leads to from one of these operators).
+lives that was built on the default stream, since torch ties a leaf's gradient
+to the stream it was first used on: refused for every leaf that the pass leads
+to from one of these operators).
 dispatch, combine, segment_matmul and layer_norm are differentiable (once);
 the spmm_* functions are the C calls on the caller's tensors.
 """

@@ -101,3 +101,59 @@ def test_captured_backward_to_an_eager_result_is_refused():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(got, want)
+
+
+def test_a_layer_through_torchs_graphed_callables():
+    """Forward and backward captured apart by torch, parameters as leaves."""
+    class Layer(torch.nn.Module):
+        def __init__(self, g):
+            super().__init__()
+            self.gamma, self.beta = (torch.nn.Parameter(normal(g, 24).to(DEV)) for _ in range(2))
+            self.w = torch.nn.Parameter(normal(g, 3, 24, 16).to(DEV))
+
+        def forward(self, x, expert, weight):
+            r = G.RowRoute(expert, 3)
+            h = G.layer_norm(x, self.gamma, self.beta)
+            return G.combine(r, G.segment_matmul(G.dispatch(r, h), self.w, r.offsets), torch.softmax(weight, 1))
+
+    def inputs(g):
+        return (normal(g, 50, 24).to(DEV).requires_grad_(), torch.randint(-1, 3, (50, 2), generator=g).to(DEV),
+                normal(g, 50, 2).to(DEV).requires_grad_())
+    eager, layer = Layer(rng(91)), Layer(rng(91))
+    graphed = torch.cuda.make_graphed_callables(layer, inputs(rng(92)))
+    for seed in range(93, 97):
+        got, want = inputs(rng(seed)), inputs(rng(seed))
+        d = normal(rng(seed + 50), 50, 16).to(DEV)
+        out, ref = graphed(*got), eager(*want)
+        for m in (layer, eager):
+            m.zero_grad()
+        out.backward(d)
+        ref.backward(d)
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref)
+        pairs = [(got[0], want[0]), (got[2], want[2]), *zip(layer.parameters(), eager.parameters())]
+        assert all(torch.equal(a.grad, b.grad) for a, b in pairs)
+
+
+def test_captured_backward_beside_an_eager_graph_of_another_stream():
+    """A leaf whose graph of a warm-up lives: its stream joins the capture."""
+    x, d = normal(rng(95), 20, 24).to(DEV).requires_grad_(), normal(rng(96), 20, 24).to(DEV)
+    w = normal(rng(97), 24).to(DEV).requires_grad_()
+    warm = torch.cuda.Stream()
+    warm.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(warm):
+        alive = G.layer_norm(x, w)
+        want = torch.autograd.grad(alive, [x, w], d, retain_graph=True)
+    torch.cuda.current_stream().wait_stream(warm)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = torch.autograd.grad(G.layer_norm(x, w), [x, w], d)
+    for _ in range(3):
+        for t in got:
+            t.zero_()
+        float(torch.randn(1 << 16, device=DEV).sum())
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    del alive
