@@ -52,6 +52,8 @@ EXPORTED = (
     "spmm_route_workspace", "spmm_route_build", "spmm_route_dispatch", "spmm_route_combine",
     "spmm_route_combine_backward", "spmm_segment_product", "spmm_segment_product_dx", "spmm_segment_workspace",
     "spmm_segment_product_dw", "spmm_layer_norm", "spmm_layer_norm_workspace", "spmm_layer_norm_backward",
+    "spmm_segment_attention_workspace", "spmm_segment_attention", "spmm_segment_attention_backward_workspace",
+    "spmm_segment_attention_backward", "spmm_dropout",
 )
 
 SPMM_F32, SPMM_BF16, SPMM_F16 = 0, 1, 2
@@ -63,6 +65,7 @@ _ROW_OPERATORS = (
     "spmm_route_build", "spmm_route_dispatch", "spmm_route_combine", "spmm_route_combine_backward",
     "spmm_segment_product", "spmm_segment_product_dx", "spmm_segment_product_dw",
     "spmm_layer_norm", "spmm_layer_norm_backward",
+    "segment_attention", "dropout", "spmm_segment_attention", "spmm_segment_attention_backward", "spmm_dropout",
 )
 
 
@@ -167,6 +170,7 @@ def _load() -> ctypes.CDLL:
     pi64, f64 = ctypes.POINTER(ctypes.c_int64), ctypes.c_double
     exchange = [p, p, i64, i64, i64, p, p, i32]
     product = [p, p, p, p, i64, i64, i64, i64, i32]
+    heads = [p, i64, p, i64, p, i64, p, p]
     for name, args in {
         "spmm_route_workspace": [i64, i64, pi64],
         "spmm_route_build": [p, i64, i64, p, p, p, p, i64, p],
@@ -180,6 +184,11 @@ def _load() -> ctypes.CDLL:
         "spmm_layer_norm": [p, p, p, i32, p, p, p, i64, i64, f64, i32, p],
         "spmm_layer_norm_workspace": [i64, i64, i32, pi64],
         "spmm_layer_norm_backward": [p, p, p, i32, p, p, p, p, p, i64, i64, i32, p, i64, p],
+        "spmm_segment_attention_workspace": [i64] * 6 + [i32, pi64],
+        "spmm_segment_attention": heads + [p, p] + [i64] * 6 + [f64, i32, i32, p, i64, p],
+        "spmm_segment_attention_backward_workspace": [i64] * 6 + [i32, pi64],
+        "spmm_segment_attention_backward": heads + [p] * 6 + [i64] * 6 + [f64, i32, i32, p, i64, p],
+        "spmm_dropout": [p, p, p, i64, f64, p, i64, i32, p],
     }.items():
         fn = getattr(lib, name)
         fn.argtypes, fn.restype = args, i32

@@ -39,6 +39,11 @@ SOURCES = [
     "exchange.hip",
     "layer_norm.hip",
     "segment.hip",
+    "dropout.hip",
+    "attention.hip",
+    "attention_f32.hip",
+    "attention_bf16.hip",
+    "attention_f16.hip",
 ]
 
 COMMON = [

@@ -2028,3 +2028,185 @@ SPMM_API int spmm_layer_norm_backward(const void *dy, const void *x, const void 
     return launched(launch_norm_backward(a, type, reinterpret_cast<hipStream_t>(stream)),
                     "layer norm backward launch");
 }
+
+// Sizes of an attention call.
+static int check_attention(int64_t R, int64_t K, int64_t S, int64_t H, int64_t Hk, int64_t D, int type) {
+    if (R < 0 || K < 0) return fail(SPMM_E_INVALID_ARG, "negative size");
+    if (S < 1 || H < 1 || Hk < 1 || D < 1) return fail(SPMM_E_INVALID_ARG, "S, H, Hk and D must be positive");
+    if (H % Hk) return fail(SPMM_E_INVALID_ARG, "H (%lld) must be a multiple of Hk (%lld)", (long long)H, (long long)Hk);
+    if (D > kAttentionMaxWidth)
+        return fail(SPMM_E_UNSUPPORTED, "heads of at most %d elements (got %lld)", kAttentionMaxWidth, (long long)D);
+    const int64_t most = INT_MAX - 4096;
+    if (R >= most || K >= most || S >= (1 << 24) || H >= (1 << 16) || R * H >= most || K * Hk >= most ||
+        S * Hk >= (1 << 24))
+        return fail(SPMM_E_UNSUPPORTED, "R * H and K * Hk must be below 2^31 - 4097, S * Hk below 2^24 and H below 2^16");
+    return check_types(type, false, 0);
+}
+
+// Rows of `heads` heads of D elements, `ld` elements apart.
+static int check_rows_apart(const char *name, int64_t ld, int64_t heads, int64_t D) {
+    if (ld < heads * D || ld >= INT_MAX)
+        return fail(SPMM_E_INVALID_ARG, "%s must be at least a row's %lld elements and below 2^31 - 1 (got %lld)", name,
+                    (long long)(heads * D), (long long)ld);
+    return SPMM_OK;
+}
+
+static int64_t rows_apart_bytes(int64_t rows, int64_t ld, int64_t width, int64_t size) {
+    return rows ? ((rows - 1) * ld + width) * size : 0;
+}
+
+SPMM_API int spmm_segment_attention_workspace(int64_t R, int64_t K, int64_t S, int64_t H, int64_t Hk, int64_t D,
+                                              int type, int64_t *bytes) {
+    if (!bytes) return fail(SPMM_E_INVALID_ARG, "output is NULL");
+    if (const int st = check_attention(R, K, S, H, Hk, D, type)) return st;
+    *bytes = attention_workspace_floats(R, K, S, H, Hk, D) * (int64_t)sizeof(float);
+    return succeed();
+}
+
+SPMM_API int spmm_segment_attention(const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv,
+                                    const int64_t *offsets, const int64_t *key_offsets, void *out, float *lse,
+                                    int64_t R, int64_t K, int64_t S, int64_t H, int64_t Hk, int64_t D, double scale,
+                                    int causal, int type, void *workspace, int64_t workspace_bytes, void *stream) {
+    if (const int st = check_attention(R, K, S, H, Hk, D, type)) return st;
+    if (!((float)scale * 1.44269504f > 0.0f && std::isfinite((float)scale * 1.44269504f)))
+        return fail(SPMM_E_INVALID_ARG, "scale must be positive and finite in fp32 (got %g)", scale);
+    if (const int st = check_rows_apart("ldq", ldq, H, D)) return st;
+    if (const int st = check_rows_apart("ldk", ldk, Hk, D)) return st;
+    if (const int st = check_rows_apart("ldv", ldv, Hk, D)) return st;
+    const int64_t need = attention_workspace_floats(R, K, S, H, Hk, D) * (int64_t)sizeof(float);
+    if (const int st = check_workspace(need, workspace_bytes)) return st;
+    if (R == 0) return succeed();
+    const int64_t size = type_size(type);
+    int device;
+    if (const int st = check_arrays({{"offsets", offsets, (S + 1) * 8, 8, false},
+                                     {"key_offsets", key_offsets, (S + 1) * 8, 8, false},
+                                     {"q", q, rows_apart_bytes(R, ldq, H * D, size), (size_t)size, false},
+                                     {"k", k, rows_apart_bytes(K, ldk, Hk * D, size), (size_t)size, false},
+                                     {"v", v, rows_apart_bytes(K, ldv, Hk * D, size), (size_t)size, false},
+                                     {"out", out, R * H * D * size, (size_t)size, true},
+                                     {"lse", lse, lse ? R * H * 4 : 0, 4, true},
+                                     {"workspace", workspace, need, 4, true}},
+                                    &device))
+        return st;
+    DeviceGuard dg(device);
+    AttentionArgs a = {};
+    a.offsets = offsets;
+    a.key_offsets = key_offsets;
+    a.R = R;
+    a.K = K;
+    a.S = S;
+    a.H = H;
+    a.Hk = Hk;
+    a.D = D;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.ldq = ldq;
+    a.ldk = ldk;
+    a.ldv = ldv;
+    a.scale = (float)scale;
+    a.causal = causal != 0;
+    a.out = out;
+    a.lse = lse;
+    return launched(launch_attention(a, static_cast<float *>(workspace), type, reinterpret_cast<hipStream_t>(stream)),
+                    "attention launch");
+}
+
+SPMM_API int spmm_segment_attention_backward_workspace(int64_t R, int64_t K, int64_t S, int64_t H, int64_t Hk,
+                                                       int64_t D, int type, int64_t *bytes) {
+    if (!bytes) return fail(SPMM_E_INVALID_ARG, "output is NULL");
+    if (const int st = check_attention(R, K, S, H, Hk, D, type)) return st;
+    *bytes = attention_backward_workspace_floats(R, K, S, H, Hk, D) * (int64_t)sizeof(float);
+    return succeed();
+}
+
+SPMM_API int spmm_segment_attention_backward(const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v,
+                                             int64_t ldv, const int64_t *offsets, const int64_t *key_offsets,
+                                             const void *out, const float *lse, const void *dout, void *dq, void *dk,
+                                             void *dv, int64_t R, int64_t K, int64_t S, int64_t H, int64_t Hk,
+                                             int64_t D, double scale, int causal, int type, void *workspace,
+                                             int64_t workspace_bytes, void *stream) {
+    if (const int st = check_attention(R, K, S, H, Hk, D, type)) return st;
+    if (!((float)scale * 1.44269504f > 0.0f && std::isfinite((float)scale * 1.44269504f)))
+        return fail(SPMM_E_INVALID_ARG, "scale must be positive and finite in fp32 (got %g)", scale);
+    if (const int st = check_rows_apart("ldq", ldq, H, D)) return st;
+    if (const int st = check_rows_apart("ldk", ldk, Hk, D)) return st;
+    if (const int st = check_rows_apart("ldv", ldv, Hk, D)) return st;
+    if (!dq && !dk && !dv) return fail(SPMM_E_INVALID_ARG, "dq, dk and dv are all NULL");
+    const int64_t need = attention_backward_workspace_floats(R, K, S, H, Hk, D) * (int64_t)sizeof(float);
+    if (const int st = check_workspace(need, workspace_bytes)) return st;
+    if (R == 0 && K == 0) return succeed();
+    const int64_t size = type_size(type), queries = R * H * D * size, keys = K * Hk * D * size;
+    int device;
+    if (const int st = check_arrays({{"offsets", offsets, (S + 1) * 8, 8, false},
+                                     {"key_offsets", key_offsets, (S + 1) * 8, 8, false},
+                                     {"q", q, rows_apart_bytes(R, ldq, H * D, size), (size_t)size, false},
+                                     {"k", k, rows_apart_bytes(K, ldk, Hk * D, size), (size_t)size, false},
+                                     {"v", v, rows_apart_bytes(K, ldv, Hk * D, size), (size_t)size, false},
+                                     {"out", out, queries, (size_t)size, false},
+                                     {"lse", lse, R * H * 4, 4, false},
+                                     {"dout", dout, queries, (size_t)size, false},
+                                     {"dq", dq, dq ? queries : 0, (size_t)size, true},
+                                     {"dk", dk, dk ? keys : 0, (size_t)size, true},
+                                     {"dv", dv, dv ? keys : 0, (size_t)size, true},
+                                     {"workspace", workspace, need, 4, true}},
+                                    &device))
+        return st;
+    DeviceGuard dg(device);
+    AttentionArgs a = {};
+    a.offsets = offsets;
+    a.key_offsets = key_offsets;
+    a.R = R;
+    a.K = K;
+    a.S = S;
+    a.H = H;
+    a.Hk = Hk;
+    a.D = D;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.ldq = ldq;
+    a.ldk = ldk;
+    a.ldv = ldv;
+    a.scale = (float)scale;
+    a.causal = causal != 0;
+    a.out = const_cast<void *>(out);
+    a.lse = const_cast<float *>(lse);
+    a.dout = dout;
+    a.dq = dq;
+    a.dk = dk;
+    a.dv = dv;
+    return launched(
+        launch_attention_backward(a, static_cast<float *>(workspace), type, reinterpret_cast<hipStream_t>(stream)),
+        "attention backward launch");
+}
+
+SPMM_API int spmm_dropout(const void *x, const void *residual, void *y, int64_t n, double p, const int64_t *seed,
+                          int64_t offset, int type, void *stream) {
+    if (n < 0) return fail(SPMM_E_INVALID_ARG, "negative size");
+    if (!(p >= 0.0 && p <= 1.0)) return fail(SPMM_E_INVALID_ARG, "p must be between 0 and 1 (got %g)", p);
+    if (const int st = check_types(type, false, 0)) return st;
+    if (n >= int64_t(1) << 59) return fail(SPMM_E_UNSUPPORTED, "x has too many elements");
+    if (n == 0) return succeed();
+    const int64_t size = type_size(type);
+    int device;
+    if (const int st = check_arrays({{"x", x, n * size, (size_t)size, false},
+                                     {"residual", residual, residual ? n * size : 0, (size_t)size, false},
+                                     {"seed", seed, 8, 8, false},
+                                     {"y", y, n * size, (size_t)size, true}},
+                                    &device))
+        return st;
+    DeviceGuard dg(device);
+    const double below = std::nearbyint(p * 4294967296.0);
+    DropoutArgs a = {};
+    a.x = x;
+    a.residual = residual;
+    a.y = y;
+    a.n = n;
+    a.seed = seed;
+    a.offset = offset;
+    a.none = below >= 4294967296.0;
+    a.below = a.none ? 0u : (uint32_t)below;
+    a.scale = a.none ? 0.0f : (float)(1.0 / (1.0 - p));
+    return launched(launch_dropout(a, type, reinterpret_cast<hipStream_t>(stream)), "dropout launch");
+}

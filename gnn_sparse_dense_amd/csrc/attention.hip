@@ -1,0 +1,117 @@
+// Attention within segments: what a call's shape decides on the host.  The
+// kernels and their mathematics are in attention_impl.h.
+#include "rows.h"
+
+#include <algorithm>
+
+namespace gspmm {
+
+template <typename T>
+hipError_t launch_attention_pass(const AttentionArgs &a, AttentionPass pass, bool large, bool direct, hipStream_t s);
+template <typename T>
+hipError_t launch_attention_join(const AttentionArgs &a, hipStream_t s);
+template <typename T>
+hipError_t launch_attention_add(const AttentionArgs &a, hipStream_t s);
+
+namespace {
+
+// Exact quotients of n < 2^31: (n * magic) >> shift with magic = floor(2^shift / d) + 1.
+Divisor divisor(int64_t d) {
+    int s = 0;
+    while ((int64_t(1) << s) < d) ++s;
+    return {(uint32_t)((uint64_t(1) << (31 + s)) / (uint64_t)d + 1), 31 + s, (int)d};
+}
+
+// The copy into LDS needs rows of whole 16-byte groups, from a 16-byte address,
+// and 32-bit offsets within a tile's rows.
+bool direct_rows(const void *p, int64_t ld, int64_t D, int size) {
+    return (uintptr_t)p % 16 == 0 && ld * size % 16 == 0 && D * size % 16 == 0 && ld * size < (int64_t(1) << 24);
+}
+
+// Tiles of 128 rows by four waves that share their keys, or of 32 by one: by the
+// mean length of a segment, since the device alone knows each.
+bool large_tiles(int64_t rows, int64_t S) { return rows > 64 * S; }
+
+// Parts of a segment's keys (rows) that are worked on side by side and joined
+// afterwards, where there are too few tiles to fill the chip: about `want` blocks,
+// at least 256 keys (rows) to a part of a segment of mean length.
+int64_t parts_of(int64_t blocks, int64_t want, int64_t length, int64_t S, int64_t most) {
+    return std::max<int64_t>(1, std::min({want / std::max<int64_t>(1, blocks), length / std::max<int64_t>(1, S) / 256, most}));
+}
+
+int64_t tiles(int64_t rows, int64_t S, bool large) { return rows / (large ? 128 : 32) + std::min(rows, S); }
+
+int query_parts(int64_t R, int64_t K, int64_t S, int64_t H, int64_t Hk) {
+    const bool large = large_tiles(R * (H / Hk), S);
+    return (int)parts_of(tiles(R * (H / Hk), S, large) * Hk, large ? 512 : 2048, K, S, 64);
+}
+
+int key_parts(int64_t R, int64_t K, int64_t S, int64_t H, int64_t Hk) {
+    const bool large = large_tiles(K, S);
+    return (int)parts_of(tiles(K, S, large) * Hk, large ? 512 : 2048, R * (H / Hk), S, 16);
+}
+
+}  // namespace
+
+int64_t attention_workspace_floats(int64_t R, int64_t K, int64_t S, int64_t H, int64_t Hk, int64_t D) {
+    const int64_t parts = query_parts(R, K, S, H, Hk);
+    return parts > 1 ? parts * R * H * (D + 2) : 0;
+}
+
+int64_t attention_backward_workspace_floats(int64_t R, int64_t K, int64_t S, int64_t H, int64_t Hk, int64_t D) {
+    const int64_t parts = key_parts(R, K, S, H, Hk);
+    return R * H + (parts > 1 ? 2 * parts * K * Hk * D : 0);
+}
+
+hipError_t launch_attention(const AttentionArgs &args, float *workspace, int type, hipStream_t s) {
+    if (args.R == 0) return hipSuccess;
+    AttentionArgs a = args;
+    const int size = type == SPMM_F32 ? 4 : 2;
+    a.G = divisor(a.H / a.Hk);
+    a.parts = query_parts(a.R, a.K, a.S, a.H, a.Hk);
+    if (a.parts > 1) {
+        a.partial = workspace;
+        a.partial_top = workspace + a.parts * a.R * a.H * a.D;
+        a.partial_sum = a.partial_top + a.parts * a.R * a.H;
+    }
+    const bool large = large_tiles(a.R * a.G.d, a.S);
+    const bool direct = direct_rows(a.k, a.ldk, a.D, size) && direct_rows(a.v, a.ldv, a.D, size);
+    const auto pass = AttentionPass::kForward;
+    if (const hipError_t e = type == SPMM_F32    ? launch_attention_pass<float>(a, pass, large, direct, s)
+                             : type == SPMM_BF16 ? launch_attention_pass<__bf16>(a, pass, large, direct, s)
+                                                 : launch_attention_pass<_Float16>(a, pass, large, direct, s))
+        return e;
+    if (a.parts == 1) return hipSuccess;
+    return type == SPMM_F32    ? launch_attention_join<float>(a, s)
+           : type == SPMM_BF16 ? launch_attention_join<__bf16>(a, s)
+                               : launch_attention_join<_Float16>(a, s);
+}
+
+hipError_t launch_attention_backward(const AttentionArgs &args, float *workspace, int type, hipStream_t s) {
+    AttentionArgs a = args;
+    const int size = type == SPMM_F32 ? 4 : 2;
+    a.G = divisor(a.H / a.Hk);
+    a.parts = 1;
+    a.key_parts = key_parts(a.R, a.K, a.S, a.H, a.Hk);
+    a.delta = workspace;
+    a.partial_dk = workspace + a.R * a.H;
+    a.partial_dv = a.partial_dk + a.key_parts * a.K * a.Hk * a.D;
+    auto pass = [&](AttentionPass p, bool large, bool direct) {
+        return type == SPMM_F32    ? launch_attention_pass<float>(a, p, large, direct, s)
+               : type == SPMM_BF16 ? launch_attention_pass<__bf16>(a, p, large, direct, s)
+                                   : launch_attention_pass<_Float16>(a, p, large, direct, s);
+    };
+    if (a.R > 0) {
+        const bool direct = direct_rows(a.k, a.ldk, a.D, size) && direct_rows(a.v, a.ldv, a.D, size);
+        if (const hipError_t e = pass(AttentionPass::kQueries, large_tiles(a.R * a.G.d, a.S), direct)) return e;
+    }
+    if (a.K == 0 || (!a.dk && !a.dv)) return hipSuccess;
+    const bool direct = direct_rows(a.q, a.ldq, a.D, size) && direct_rows(a.dout, a.H * a.D, a.D, size);
+    if (const hipError_t e = pass(AttentionPass::kKeys, large_tiles(a.K, a.S), direct)) return e;
+    if (a.key_parts == 1) return hipSuccess;
+    return type == SPMM_F32    ? launch_attention_add<float>(a, s)
+           : type == SPMM_BF16 ? launch_attention_add<__bf16>(a, s)
+                               : launch_attention_add<_Float16>(a, s);
+}
+
+}  // namespace gspmm

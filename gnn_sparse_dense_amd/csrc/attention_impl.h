@@ -1,0 +1,853 @@
+// Attention among the rows of each segment, and its gradients.  For a row i of
+// segment s and a head h, over the keys j of s (causal: j <= i + m - n for the
+// n rows and m keys of s, both counted from its start):
+//
+//   out_i = sum_j p_ij v_j,   p_ij = exp(scale q_i.k_j) / sum_j exp(scale q_i.k_j)
+//
+//   dv_j = sum_i p_ij dout_i            ds_ij = p_ij (dout_i.v_j - dout_i.out_i)
+//   dq_i = scale sum_j ds_ij k_j        dk_j  = scale sum_i ds_ij q_i
+//
+// One pass over the keys with the running maximum and sum of the softmax; the
+// scores never leave the registers.  The G = H / Hk query heads of a key head
+// are packed into its rows (packed row i G + g), so a step with one new row per
+// sequence fills tiles with its heads, keys are read once for all of a group,
+// and the sums over a group's heads in dk and dv are sums over rows.
+//
+// A wave owns 32 packed rows (32 keys in dk and dv) and walks tiles of keys
+// (rows) in LDS.  Scores are computed with the tile's rows in the registers and
+// the wave's own in the lanes, so a row's maximum and sum are in-lane plus one
+// exchange of the two half waves, and the products of the second stage take the
+// probabilities from the registers they are in: the summed index may stand in
+// any order, so the turned LDS reads of v (k, q, dout) follow the order that the
+// matrix instruction left.  Tiles are copied into LDS ahead of their use, 16
+// bytes per lane, chunks placed so that both ways of reading meet no bank twice.
+//
+// Sums and statistics are fp32.  Probabilities and ds are rounded to the rows'
+// type where they enter a matrix instruction (16-bit types).
+#pragma once
+
+#include "tile_product.h"
+
+namespace gspmm {
+
+namespace {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// ---- exact division by a number fixed on the host, for n < 2^31 ----
+
+__device__ inline int quotient(const Divisor &d, int n) {
+    return (int)(((uint64_t)(uint32_t)n * d.magic) >> d.shift);
+}
+
+// ---- LDS layout of a tile: rows of kPitch bytes, a power of two ----
+//
+// Chunk c of row r stands at c ^ place(r).  16 lanes that read one chunk of 16
+// rows, and 32 lanes that turn 4 rows of 64 bytes, cover the 64 banks once.
+template <typename T, int DP>
+struct Tile {
+    static constexpr int kPitch = DP * (int)sizeof(T) <= 64 ? 64 : DP * (int)sizeof(T) <= 128 ? 128
+                                  : DP * (int)sizeof(T) <= 256 ? 256 : 512;
+    static constexpr int kChunks = kPitch / 16;
+    static constexpr int kDrop = kChunks >= 16 ? 0 : kChunks == 8 ? 1 : 2;
+    static constexpr int kSteps = DP * (int)sizeof(T) / 32;      // matrix steps along a row
+    static constexpr int kBlocks = DP / 32;                      // 32-element blocks of a row
+    static constexpr int kGroups = 16 / kPack<T>;                // matrix steps along 32 rows
+
+    static __device__ inline int place(int r) { return ((r & 3) >> kDrop) << 2 | (r >> 2 & 3); }
+};
+
+// The lane's operand of matrix step ks: row block * 32 + lane % 32.
+template <typename T, int DP>
+struct RowReader {
+    using L = Tile<T, DP>;
+    int at;
+
+    __device__ inline RowReader() {
+        const int lane = threadIdx.x & (kWave - 1), r = lane & 31;
+        at = r * L::kPitch + (((lane >> 5) ^ L::place(r)) << 4);
+    }
+
+    __device__ inline Pack<T> read(LdsByte *tile, int block, int ks) const {
+        return lds_load<Pack<T>>(tile + ((at ^ (ks << 5)) + block * 32 * L::kPitch));
+    }
+};
+
+// The same of the tile turned: element d * 32 + lane % 32 of the rows that the
+// registers group * kPack .. of multiply() stand for in the lane's half.
+template <typename T, int DP>
+struct TurnedReader {
+    using L = Tile<T, DP>;
+    int at;
+
+    __device__ inline TurnedReader() {
+        const int lane = threadIdx.x & (kWave - 1), half = lane >> 5;
+        if constexpr (sizeof(T) == 2) {
+            // lane l of 16 points at 4 elements of row l / 4 and receives
+            // element l of the rows 0..3
+            const int l = lane & 15, r = 4 * half + (l >> 2);
+            const int chunk = (lane >> 4 & 1) * 2 + (l >> 1 & 1);
+            at = r * L::kPitch + ((chunk ^ L::place(r)) << 4) + (l & 1) * 8;
+        } else {
+            at = 4 * half * L::kPitch + (((lane & 31) >> 2 ^ half) << 4) + (lane & 3) * 4;
+        }
+    }
+
+    __device__ inline Pack<T> read(LdsByte *tile, int block, int group, int d) const {
+        if constexpr (sizeof(T) == 2) {
+            typedef __attribute__((address_space(3))) i16x4 LdsFour;
+            struct {
+                i16x4 lo, hi;
+            } both;
+            const int row = (block * 32 + group * 16) * L::kPitch;
+            both.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsFour *)(tile + ((at ^ (d << 6)) + row)));
+            both.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (LdsFour *)(tile + ((at ^ (d << 6) ^ 32) + (row + 8 * L::kPitch))));
+            return __builtin_bit_cast(Pack<T>, both);
+        } else {
+            Pack<T> r;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int place = (d * 8) ^ ((j >> L::kDrop) << 2) ^ (2 * group & 3);
+                r.v[j] = *(__attribute__((address_space(3))) float *)(tile + ((at ^ (place << 4)) +
+                                                                              (block * 32 + 8 * group + j) * L::kPitch));
+            }
+            return r;
+        }
+    }
+};
+
+// ---- rows of a tile in memory ----
+
+// Consecutive rows of one head.
+template <typename T>
+struct KeyRows {
+    const T *base;
+    int64_t ld;
+    int left;           // rows that exist
+
+    __device__ inline int64_t at(int r) const { return r < left ? r * ld : -1; }
+};
+
+// Consecutive packed rows of one key head, from packed row m0 of a segment;
+// base: row m0 / G, the group's first head.
+template <typename T>
+struct PackedRows {
+    const T *base;
+    int64_t ld;
+    int left, m0, i0, D;
+    Divisor G;
+
+    __device__ inline int64_t at(int r) const {
+        const int m = m0 + r, i = quotient(G, m);
+        return r < left ? (i - i0) * ld + (m - i * G.d) * D : -1;
+    }
+};
+
+// Fills ROWS rows of a tile, zeros where a row or an element does not exist.
+// DIRECT: copied straight into LDS; else through registers, load() ahead of
+// the use of what put() overwrites.
+template <typename T, int DP, int ROWS, int WAVES, bool DIRECT>
+struct Fill {
+    using L = Tile<T, DP>;
+    static constexpr int kCopies = ROWS * L::kPitch / 1024 / WAVES;
+    Pack<T> r[DIRECT ? 1 : kCopies];
+
+    template <typename Rows>
+    __device__ inline void load(LdsByte *lds, const Rows &rows, int D, int wave) {
+        const char *base = (const char *)uniform((int64_t)rows.base);
+        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)base, 0, 0x7fffffff, 0x00020000);
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i) {
+            const int byte = (i * WAVES + wave) * 1024 + (threadIdx.x & (kWave - 1)) * 16;
+            const int row = byte / L::kPitch, e = ((byte % L::kPitch / 16) ^ L::place(row)) * kPack<T>;
+            const int64_t at = rows.at(row);
+            if constexpr (DIRECT) {
+                // behind 2^31 - 1 bytes the copy writes zeros
+                const uint32_t off = at >= 0 && e < D ? (uint32_t)(at + e) * (uint32_t)sizeof(T) : 0x80000000u;
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                    rsrc, (__attribute__((address_space(3))) void *)(lds + (i * WAVES + wave) * 1024), 16, off, 0, 0, 0);
+            } else {
+                r[i] = load_pack(rows.base + (at >= 0 ? at + e : 0), at >= 0 ? D - e : 0);
+            }
+        }
+    }
+
+    __device__ inline void put(LdsByte *lds, int wave) {
+        if constexpr (!DIRECT) {
+#pragma unroll
+            for (int i = 0; i < kCopies; ++i)
+                lds_store(lds + ((i * WAVES + wave) * 1024 + (threadIdx.x & (kWave - 1)) * 16), r[i]);
+        }
+    }
+};
+
+// ---- the tiles of a call ----
+
+// S segments between rows (each `scale` packed rows) as S + 2 runs: the rows
+// before the first segment, the segments, the rows behind the last.
+struct Runs {
+    const int64_t *offsets;
+    int64_t S, rows;
+    int scale;
+
+    __device__ inline int64_t bound(int64_t v) const {
+        if (v <= 0) return 0;
+        if (v > S + 1) return rows;
+        const int64_t b = offsets[v - 1];
+        return b < 0 ? 0 : b > rows ? rows : b;
+    }
+};
+
+// Run v, from packed row lo, owns the slots from lo / LEN + v on to the next
+// run's: at least as many as it has tiles of LEN rows.  The slot's run is found
+// by a search that looks at 64 runs at a time; a slot that its run does not need
+// has tile >= tiles.
+struct Slot {
+    int64_t run, row0;            // the run's first row
+    int rows, packed;             // how many it has
+    int tile, tiles;
+};
+
+template <int LEN>
+__device__ inline Slot find(const Runs &a, int slot) {
+    const int lane = threadIdx.x & (kWave - 1);
+    int64_t v = 0, n = a.S + 2;
+    while (n > 1) {
+        const int64_t step = (n + kWave - 1) / kWave, to = lane * step;
+        const bool from = lane == 0 || (to < n && a.bound(v + to) * a.scale / LEN + v + to <= slot);
+        const int64_t past = (kWave - 1 - __builtin_clzll(__ballot(from))) * step;
+        v += past;
+        n = min(step, n - past);
+    }
+    Slot s;
+    s.run = uniform(v);
+    s.row0 = uniform(a.bound(v));
+    s.rows = uniform((int)max(int64_t(0), a.bound(v + 1) - s.row0));
+    s.packed = s.rows * a.scale;
+    s.tiles = (s.packed + LEN - 1) / LEN;
+    const int64_t tile = slot - s.row0 * a.scale / LEN - s.run;
+    s.tile = tile < 0 || tile >= s.tiles ? s.tiles : (int)tile;
+    return s;
+}
+
+__device__ inline float other_half(float v) { return __shfl_xor(v, 32, kWave); }
+
+__device__ inline float exp2_of(float v) { return __builtin_amdgcn_exp2f(v); }
+
+// Key of register i of a score block, from the block's first.
+__device__ inline int register_row(int i) {
+    return 8 * (i >> 2) + 4 * ((threadIdx.x & (kWave - 1)) >> 5) + (i & 3);
+}
+
+template <typename T>
+__device__ inline Pack<T> group_of(const f32x16 &s, int group) {
+    Pack<T> p;
+#pragma unroll
+    for (int e = 0; e < kPack<T>; ++e) p.v[e] = (T)s[group * kPack<T> + e];
+    return p;
+}
+
+// The floats of a block's 32 rows as the registers of multiply() stand for them.
+__device__ inline f32x16 register_floats(LdsByte *floats, int block) {
+    typedef float f32x4 __attribute__((ext_vector_type(4)));
+    const int half = (threadIdx.x & (kWave - 1)) >> 5;
+    f32x16 r;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const auto v = lds_load<f32x4>(floats + half * 16 + (block * 32 + 8 * q) * 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) r[q * 4 + e] = v[e];
+    }
+    return r;
+}
+
+// A wave's lanes copy from[at] into LDS in their order, zeros where !in.
+__device__ inline void copy_floats(LdsByte *lds, const float *from, int at, bool in) {
+    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)uniform((int64_t)from), 0, 0x7fffffff, 0x00020000);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (__attribute__((address_space(3))) void *)lds, 4,
+                                             in ? (uint32_t)at * 4u : 0x80000000u, 0, 0, 0);
+}
+
+// The lane's row of D elements (times f) from the blocks of multiply().
+template <typename OUT, int BLOCKS>
+__device__ inline void store_row(OUT *row, const f32x16 (&acc)[BLOCKS], float f, int D) {
+    const int half = (threadIdx.x & (kWave - 1)) >> 5;
+#pragma unroll
+    for (int b = 0; b < BLOCKS; ++b)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int d = b * 32 + q * 8 + half * 4;
+            OUT v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = (OUT)(acc[b][q * 4 + e] * f);
+            if (d + 4 <= D) {
+                __builtin_memcpy(row + d, v, sizeof(v));
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (d + e < D) row[d + e] = v[e];
+            }
+        }
+}
+
+// What both query-side kernels know of a tile of packed rows.
+template <typename T>
+struct Queries {
+    int m, packed;      // the lane's packed row, and how many there are
+    int64_t row;        // its row and head
+    int head;
+    int seen;           // keys that it sees
+    int seen_least, seen_most;      // over the wave's rows
+    int64_t key0;       // the segment's first key
+    int keys;
+
+    __device__ inline void locate(const AttentionArgs &a, const Slot &s, int hk, int m0, int rows_ahead) {
+        const Runs keyruns = {a.key_offsets, a.S, a.K, 1};
+        packed = s.packed;
+        key0 = uniform(keyruns.bound(s.run));
+        keys = uniform((int)max(int64_t(0), keyruns.bound(s.run + 1) - key0));
+        m = m0 + rows_ahead + (threadIdx.x & 31);
+        const int mc = min(m, packed - 1), i = quotient(a.G, mc);
+        row = s.row0 + i;
+        head = hk * a.G.d + mc - i * a.G.d;
+        const int ahead = keys - s.rows + 1;
+        seen = sees(a, i, ahead);
+        seen_least = uniform(sees(a, quotient(a.G, min(m0 + rows_ahead, packed - 1)), ahead));
+        seen_most = uniform(sees(a, quotient(a.G, min(m0 + rows_ahead + 31, packed - 1)), ahead));
+    }
+
+    __device__ inline int sees(const AttentionArgs &a, int i, int ahead) const {
+        return a.causal ? max(0, min(keys, i + ahead)) : keys;
+    }
+
+    __device__ inline bool exists() const { return m < packed; }
+};
+
+template <int LEN>
+__device__ inline int seen_by_tile(const AttentionArgs &a, const Slot &s, int keys) {
+    const int last = quotient(a.G, min((s.tile + 1) * LEN, s.packed) - 1);
+    return a.causal ? max(0, min(keys, last + keys - s.rows + 1)) : keys;
+}
+
+// The lane's row of an operand, as the packs that the matrix steps take.
+template <typename T, int DP>
+using RowPacks = Pack<T>[Tile<T, DP>::kSteps];
+
+template <typename T, int DP>
+__device__ inline void load_row(RowPacks<T, DP> &r, const T *row, int D, bool exists) {
+    const int half = (threadIdx.x & (kWave - 1)) >> 5;
+#pragma unroll
+    for (int ks = 0; ks < Tile<T, DP>::kSteps; ++ks) {
+        const int e = (2 * ks + half) * kPack<T>;
+        r[ks] = load_pack(row + (exists && e < D ? e : 0), exists ? D - e : 0);
+    }
+}
+
+template <typename T, int WAVES>
+constexpr int kTileRows = WAVES == 1 || sizeof(T) == 4 ? 32 : 64;
+
+// Two waves to a SIMD where 256 registers hold one's rows, sums and, without
+// direct copies, the tile on its way.
+template <typename T, int DP, bool DIRECT>
+constexpr int kQuerySide = sizeof(T) * DP > (DIRECT ? 256 : 128) ? 1 : 2;
+template <typename T, int DP, bool DIRECT>
+constexpr int kKeySide = sizeof(T) * DP > (DIRECT ? 128 : 64) ? 1 : 2;
+
+// Two stages of two tiles each, arrays of their own (see Stages).
+#define TILE_PAIRS(x, y, bytes)                                  \
+    __shared__ __attribute__((aligned(1024))) char x##0[bytes]; \
+    __shared__ __attribute__((aligned(1024))) char y##0[bytes]; \
+    __shared__ __attribute__((aligned(1024))) char x##1[bytes]; \
+    __shared__ __attribute__((aligned(1024))) char y##1[bytes]; \
+    LdsByte *const x[2] = {(LdsByte *)x##0, (LdsByte *)x##1};   \
+    LdsByte *const y[2] = {(LdsByte *)y##0, (LdsByte *)y##1}
+
+// Walks the tiles [t0, t1) of two arrays: while tile t is used, tile t + 1 is
+// on its way into the other stage.
+template <bool DIRECT, typename LoadAll, typename PutAll, typename Use>
+__device__ inline void walk(int t0, int t1, LoadAll load, PutAll put, Use use) {
+    if (t0 >= t1) return;
+    load(t0, 0);
+    if constexpr (DIRECT) {
+        auto step = [&](int t, int u) {
+            wait_copies<0>();
+            load(t + 1, 1 - u);                          // behind the last tile: zeros, or a tile that is not used
+            use(t, u);
+        };
+        int t = t0;
+        for (; t + 1 < t1; t += 2) {
+            step(t, 0);
+            step(t + 1, 1);
+        }
+        if (t < t1) step(t, 0);
+        wait_copies<0>();
+    } else {
+        put(0);
+        for (int t = t0; t < t1; t += 2) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+                if (t + u < t1) {
+                    __syncthreads();
+                    const bool more = t + u + 1 < t1;
+                    if (more) load(t + u + 1, 1 - u);
+                    use(t + u, u);
+                    if (more) put(1 - u);
+                }
+        }
+        __syncthreads();
+    }
+}
+
+// ---- forward ----
+
+template <typename T, int DP, int WAVES, bool DIRECT>
+__global__ __launch_bounds__(WAVES * kWave, (kQuerySide<T, DP, DIRECT>)) void attention_kernel(AttentionArgs a, unsigned total) {
+    using L = Tile<T, DP>;
+    constexpr int BM = 32 * WAVES, BN = kTileRows<T, WAVES>, NB = BN / 32;
+    TILE_PAIRS(ktile, vtile, BN * L::kPitch);
+    const int wave = uniform((int)threadIdx.x / kWave), half = (threadIdx.x & (kWave - 1)) >> 5;
+    const int D = (int)a.D;
+    const RowReader<T, DP> rows;
+    const TurnedReader<T, DP> turned;
+    const Runs runs = {a.offsets, a.S, a.R, a.G.d};
+    const float c = a.scale * kLog2e;
+    for (unsigned id = blockIdx.x; id < total; id += gridDim.x) {
+        const unsigned heads = (unsigned)a.Hk, rest = id / heads, parts = (unsigned)a.parts;
+        const int hk = (int)(id - rest * heads), part = (int)(rest % parts);
+        Slot s = find<BM>(runs, (int)(rest / parts));
+        if (s.tile >= s.tiles) continue;
+        s.tile = s.tiles - 1 - s.tile;                   // causal: the longest first
+        Queries<T> q;
+        q.locate(a, s, hk, s.tile * BM, wave * 32);
+        f32x16 acc[L::kBlocks] = {};
+        float top = -INFINITY, sum = 0.0f;
+        if (s.run > 0 && s.run <= a.S) {
+            const int tiles = (seen_by_tile<BM>(a, s, q.keys) + BN - 1) / BN;
+            const int per = (tiles + a.parts - 1) / a.parts;
+            const int t0 = part * per, t1 = min(tiles, t0 + per);
+            RowPacks<T, DP> mine;
+            load_row<T, DP>(mine, (const T *)a.q + q.row * a.ldq + q.head * D, D, q.exists());
+            const T *k = (const T *)a.k + q.key0 * a.ldk + hk * D, *v = (const T *)a.v + q.key0 * a.ldv + hk * D;
+            Fill<T, DP, BN, WAVES, DIRECT> fk, fv;
+            __syncthreads();
+            walk<DIRECT>(
+                t0, t1,
+                [&](int t, int u) {
+                    const int j = t * BN, left = q.keys - j;
+                    fk.load(ktile[u], KeyRows<T>{k + j * a.ldk, a.ldk, left}, D, wave);
+                    fv.load(vtile[u], KeyRows<T>{v + j * a.ldv, a.ldv, left}, D, wave);
+                },
+                [&](int u) {
+                    fk.put(ktile[u], wave);
+                    fv.put(vtile[u], wave);
+                },
+                [&](int t, int u) {
+                    const int j0 = t * BN;
+                    if (j0 >= q.seen_most) return;
+                    f32x16 sc[NB] = {};
+#pragma unroll
+                    for (int ks = 0; ks < L::kSteps; ++ks)
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) multiply<T>(mine[ks], rows.read(ktile[u], b, ks), sc[b]);
+                    if (j0 + BN > q.seen_least) {
+#pragma unroll
+                        for (int b = 0; b < NB; ++b)
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                if (j0 + b * 32 + register_row(i) >= q.seen) sc[b][i] = -INFINITY;
+                    }
+                    float most = sc[0][0];
+#pragma unroll
+                    for (int b = 0; b < NB; ++b)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) most = fmaxf(most, sc[b][i]);
+                    most = fmaxf(most, other_half(most)) * c;
+                    // The sums keep the maximum they were taken against until it
+                    // grows by 2^8: weights up to 256 lose nothing in any of the
+                    // types, and most tiles rescale nothing.
+                    if (__any(most > top + 8.0f)) {
+                        const float next = fmaxf(top, most);
+                        const float f = next == -INFINITY ? 1.0f : exp2_of(top - next);
+                        top = next;
+                        sum *= f;
+#pragma unroll
+                        for (int b = 0; b < L::kBlocks; ++b) acc[b] *= f;
+                    }
+                    const float from = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+                    for (int b = 0; b < NB; ++b)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            sc[b][i] = exp2_of(fmaf(sc[b][i], c, -from));
+                            sum += sc[b][i];
+                        }
+#pragma unroll
+                    for (int b = 0; b < NB; ++b)
+#pragma unroll
+                        for (int g = 0; g < L::kGroups; ++g) {
+                            const Pack<T> p = group_of<T>(sc[b], g);
+#pragma unroll
+                            for (int d = 0; d < L::kBlocks; ++d)
+                                multiply<T>(p, turned.read(vtile[u], b, g, d), acc[d]);
+                        }
+                });
+        }
+        sum += other_half(sum);
+        const int64_t at = q.row * a.H + q.head, all = a.R * a.H;
+        if (q.exists() && a.parts > 1) {
+            store_row(a.partial + (part * all + at) * D, acc, 1.0f, D);
+            if (half == 0) {
+                a.partial_top[part * all + at] = top;
+                a.partial_sum[part * all + at] = sum;
+            }
+        } else if (q.exists()) {
+            store_row((T *)a.out + at * D, acc, sum == 0.0f ? 0.0f : 1.0f / sum, D);
+            if (a.lse && half == 0) a.lse[at] = sum == 0.0f ? INFINITY : top + log2f(sum);
+        }
+    }
+}
+
+// Joins the parts of a row, a wave to a row and head.
+constexpr int kJoinThreads = 256;
+
+template <typename T>
+__global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttentionArgs a) {
+    const int lane = threadIdx.x & (kWave - 1), D = (int)a.D;
+    const int64_t all = a.R * a.H;
+    for (int64_t at = (int64_t)blockIdx.x * (kJoinThreads / kWave) + threadIdx.x / kWave; at < all;
+         at += (int64_t)gridDim.x * (kJoinThreads / kWave)) {
+        // a lane takes a part's statistics
+        const bool has = lane < a.parts;
+        const float mine = has ? a.partial_sum[lane * all + at] : 0.0f;
+        const float at_top = has && mine != 0.0f ? a.partial_top[lane * all + at] : -INFINITY;
+        float top = at_top;
+#pragma unroll
+        for (int o = kWave / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, kWave));
+        const float weight = at_top == -INFINITY && mine == 0.0f ? 0.0f : exp2_of(at_top - top);
+        float sum = mine * weight;
+#pragma unroll
+        for (int o = kWave / 2; o > 0; o >>= 1) sum += __shfl_xor(sum, o, kWave);
+        float r[2] = {0.0f, 0.0f};
+        for (int p = 0; p < a.parts; ++p) {
+            const float w = __shfl(weight, p, kWave);
+            if (__shfl(mine, p, kWave) == 0.0f) continue;
+            const float *from = a.partial + (p * all + at) * D;
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (lane + e * kWave < D) r[e] = fmaf(w, from[lane + e * kWave], r[e]);
+        }
+        const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            if (lane + e * kWave < D) ((T *)a.out)[at * D + lane + e * kWave] = (T)(r[e] * f);
+        if (a.lse && lane == 0) a.lse[at] = sum == 0.0f ? INFINITY : top + log2f(sum);
+    }
+}
+
+// ---- backward ----
+
+// dq, and delta = dout.out of every row, which dk and dv take from here.
+template <typename T, int DP, int WAVES, bool DIRECT>
+__global__ __launch_bounds__(WAVES * kWave, (kQuerySide<T, DP, DIRECT>)) void attention_dq_kernel(AttentionArgs a, unsigned total) {
+    using L = Tile<T, DP>;
+    constexpr int BM = 32 * WAVES, BN = kTileRows<T, WAVES>, NB = BN / 32;
+    TILE_PAIRS(ktile, vtile, BN * L::kPitch);
+    const int wave = uniform((int)threadIdx.x / kWave), half = (threadIdx.x & (kWave - 1)) >> 5;
+    const int D = (int)a.D;
+    const RowReader<T, DP> rows;
+    const TurnedReader<T, DP> turned;
+    const Runs runs = {a.offsets, a.S, a.R, a.G.d};
+    const float c = a.scale * kLog2e;
+    for (unsigned id = blockIdx.x; id < total; id += gridDim.x) {
+        const unsigned heads = (unsigned)a.Hk, rest = id / heads;
+        const int hk = (int)(id - rest * heads);
+        Slot s = find<BM>(runs, (int)rest);
+        if (s.tile >= s.tiles) continue;
+        s.tile = s.tiles - 1 - s.tile;
+        Queries<T> q;
+        q.locate(a, s, hk, s.tile * BM, wave * 32);
+        const int64_t at = q.row * a.H + q.head;
+        f32x16 acc[L::kBlocks] = {};
+        if (s.run > 0 && s.run <= a.S) {
+            RowPacks<T, DP> mine, dout;
+            load_row<T, DP>(dout, (const T *)a.dout + at * D, D, q.exists());
+            load_row<T, DP>(mine, (const T *)a.out + at * D, D, q.exists());
+            float delta = 0.0f;
+#pragma unroll
+            for (int ks = 0; ks < L::kSteps; ++ks)
+#pragma unroll
+                for (int e = 0; e < kPack<T>; ++e) delta = fmaf((float)dout[ks].v[e], (float)mine[ks].v[e], delta);
+            delta += other_half(delta);
+            const float lse = q.exists() ? a.lse[at] : INFINITY;
+            if (q.exists() && half == 0) a.delta[at] = delta;
+            if (a.dq) {
+                load_row<T, DP>(mine, (const T *)a.q + q.row * a.ldq + q.head * D, D, q.exists());
+                const int tiles = (seen_by_tile<BM>(a, s, q.keys) + BN - 1) / BN;
+                const T *k = (const T *)a.k + q.key0 * a.ldk + hk * D, *v = (const T *)a.v + q.key0 * a.ldv + hk * D;
+                Fill<T, DP, BN, WAVES, DIRECT> fk, fv;
+                __syncthreads();
+                walk<DIRECT>(
+                    0, tiles,
+                    [&](int t, int u) {
+                        const int j = t * BN, left = q.keys - j;
+                        fk.load(ktile[u], KeyRows<T>{k + j * a.ldk, a.ldk, left}, D, wave);
+                        fv.load(vtile[u], KeyRows<T>{v + j * a.ldv, a.ldv, left}, D, wave);
+                    },
+                    [&](int u) {
+                        fk.put(ktile[u], wave);
+                        fv.put(vtile[u], wave);
+                    },
+                    [&](int t, int u) {
+                        const int j0 = t * BN;
+                        if (j0 >= q.seen_most) return;
+                        const bool border = j0 + BN > q.seen_least;
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) {
+                            f32x16 sc = {}, dp = {};
+#pragma unroll
+                            for (int ks = 0; ks < L::kSteps; ++ks) {
+                                multiply<T>(mine[ks], rows.read(ktile[u], b, ks), sc);
+                                multiply<T>(dout[ks], rows.read(vtile[u], b, ks), dp);
+                            }
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) sc[i] = exp2_of(fmaf(sc[i], c, -lse));
+                            if (border) {
+#pragma unroll
+                                for (int i = 0; i < 16; ++i)
+                                    if (j0 + b * 32 + register_row(i) >= q.seen) sc[i] = 0.0f;
+                            }
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) sc[i] *= dp[i] - delta;
+#pragma unroll
+                            for (int g = 0; g < L::kGroups; ++g) {
+                                const Pack<T> ds = group_of<T>(sc, g);
+#pragma unroll
+                                for (int d = 0; d < L::kBlocks; ++d)
+                                    multiply<T>(ds, turned.read(ktile[u], b, g, d), acc[d]);
+                            }
+                        }
+                    });
+            }
+        } else if (q.exists() && half == 0) {
+            a.delta[at] = 0.0f;
+        }
+        if (a.dq && q.exists()) store_row((T *)a.dq + at * D, acc, a.scale, D);
+    }
+}
+
+// dk and dv: the block's keys against the packed rows that see them.
+template <typename T, int DP, int WAVES, bool DIRECT>
+__global__ __launch_bounds__(WAVES * kWave, (kKeySide<T, DP, DIRECT>)) void attention_dkdv_kernel(AttentionArgs a, unsigned total) {
+    using L = Tile<T, DP>;
+    constexpr int BM = 32 * WAVES, BN = kTileRows<T, WAVES>, NB = BN / 32;
+    TILE_PAIRS(qtile, dtile, BN * L::kPitch);
+    TILE_PAIRS(lse_of, delta_of, kWave * 4);
+    const int wave = uniform((int)threadIdx.x / kWave);
+    const int D = (int)a.D;
+    const RowReader<T, DP> rows;
+    const TurnedReader<T, DP> turned;
+    const Runs runs = {a.key_offsets, a.S, a.K, 1}, queries = {a.offsets, a.S, a.R, 1};
+    const float c = a.scale * kLog2e;
+    for (unsigned id = blockIdx.x; id < total; id += gridDim.x) {
+        const unsigned heads = (unsigned)a.Hk, rest = id / heads, parts = (unsigned)a.key_parts;
+        const int hk = (int)(id - rest * heads), part = (int)(rest % parts);
+        const Slot s = find<BM>(runs, (int)(rest / parts));
+        if (s.tile >= s.tiles) continue;
+        const int j0 = s.tile * BM + wave * 32, j = j0 + (threadIdx.x & 31);
+        const bool exists = j < s.rows;
+        f32x16 dk[L::kBlocks] = {}, dv[L::kBlocks] = {};
+        if (s.run > 0 && s.run <= a.S) {
+            const int64_t row0 = uniform(queries.bound(s.run));
+            const int nrows = uniform((int)max(int64_t(0), queries.bound(s.run + 1) - row0)), packed = nrows * a.G.d;
+            // packed rows from first_seeing(j) on see key j
+            const int64_t behind = a.causal ? (int64_t)nrows - s.rows : INT32_MIN;
+            auto first_seeing = [&](int key) {
+                return (int)max(int64_t(0), min((int64_t)packed, (key + behind) * a.G.d));
+            };
+            const int from = first_seeing(s.tile * BM), mine_from = first_seeing(j), wave_from = first_seeing(j0),
+                      wave_full = first_seeing(j0 + 31);
+            const int start = from / BN, tiles = max(0, (packed + BN - 1) / BN - start);
+            const int per = (tiles + a.key_parts - 1) / a.key_parts;
+            const int t0 = start + min(tiles, part * per), t1 = min(start + tiles, t0 + per);
+            RowPacks<T, DP> kmine, vmine;
+            const int64_t key = s.row0 + min(j, s.rows - 1);
+            load_row<T, DP>(kmine, (const T *)a.k + key * a.ldk + hk * D, D, exists);
+            load_row<T, DP>(vmine, (const T *)a.v + key * a.ldv + hk * D, D, exists);
+            Fill<T, DP, BN, WAVES, DIRECT> fq, fd;
+            float lse = 0.0f, delta = 0.0f;
+            __syncthreads();
+            walk<DIRECT>(
+                t0, t1,
+                [&](int t, int u) {
+                    const int m0 = t * BN, i0 = quotient(a.G, m0), left = packed - m0;
+                    const int64_t row = row0 + i0;
+                    fq.load(qtile[u],
+                            PackedRows<T>{(const T *)a.q + row * a.ldq + hk * a.G.d * D, a.ldq, left, m0, i0, D, a.G}, D,
+                            wave);
+                    fd.load(dtile[u],
+                            PackedRows<T>{(const T *)a.dout + (row * a.H + hk * a.G.d) * D, a.H * a.D, left, m0, i0, D,
+                                          a.G},
+                            D, wave);
+                    // the rows' statistics, one lane each; rows that do not exist
+                    // take zeros, and their operands are zeros
+                    if (wave == 0) {
+                        const int m = m0 + (int)threadIdx.x, i = quotient(a.G, m);
+                        const bool in = (int)threadIdx.x < min(BN, left);
+                        const int64_t from = row * a.H + hk * a.G.d;
+                        const int at = (int)((i - i0) * a.H) + m - i * a.G.d;
+                        if constexpr (DIRECT) {
+                            copy_floats(lse_of[u], a.lse + from, at, in);
+                            copy_floats(delta_of[u], a.delta + from, at, in);
+                        } else {
+                            lse = in ? a.lse[from + at] : 0.0f;
+                            delta = in ? a.delta[from + at] : 0.0f;
+                        }
+                    }
+                },
+                [&](int u) {
+                    fq.put(qtile[u], wave);
+                    fd.put(dtile[u], wave);
+                    if (wave == 0) {
+                        ((__attribute__((address_space(3))) float *)lse_of[u])[threadIdx.x] = lse;
+                        ((__attribute__((address_space(3))) float *)delta_of[u])[threadIdx.x] = delta;
+                    }
+                },
+                [&](int t, int u) {
+                    const int m0 = t * BN;
+                    if (m0 + BN <= wave_from) return;
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        f32x16 sc = {}, dp = {};
+#pragma unroll
+                        for (int ks = 0; ks < L::kSteps; ++ks) {
+                            multiply<T>(kmine[ks], rows.read(qtile[u], b, ks), sc);
+                            multiply<T>(vmine[ks], rows.read(dtile[u], b, ks), dp);
+                        }
+                        const f32x16 ls = register_floats(lse_of[u], b), de = register_floats(delta_of[u], b);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) sc[i] = exp2_of(fmaf(sc[i], c, -ls[i]));
+                        if (m0 + b * 32 < wave_full) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                if (m0 + b * 32 + register_row(i) < mine_from) sc[i] = 0.0f;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) dp[i] = sc[i] * (dp[i] - de[i]);
+#pragma unroll
+                        for (int g = 0; g < L::kGroups; ++g) {
+                            const Pack<T> p = group_of<T>(sc, g), ds = group_of<T>(dp, g);
+#pragma unroll
+                            for (int d = 0; d < L::kBlocks; ++d) {
+                                multiply<T>(p, turned.read(dtile[u], b, g, d), dv[d]);
+                                multiply<T>(ds, turned.read(qtile[u], b, g, d), dk[d]);
+                            }
+                        }
+                    }
+                });
+        }
+        const int64_t at = ((s.row0 + j) * a.Hk + hk) * D, shift = part * a.K * a.Hk * a.D;
+        if (exists && a.key_parts > 1) {
+            if (a.dk) store_row(a.partial_dk + shift + at, dk, a.scale, D);
+            if (a.dv) store_row(a.partial_dv + shift + at, dv, 1.0f, D);
+        } else if (exists) {
+            if (a.dk) store_row((T *)a.dk + at, dk, a.scale, D);
+            if (a.dv) store_row((T *)a.dv + at, dv, 1.0f, D);
+        }
+    }
+}
+
+// Adds the parts of dk or dv in their order.
+constexpr int kAddThreads = 256;
+
+template <typename T>
+__global__ __launch_bounds__(kAddThreads) void attention_add_kernel(const float *from, T *to, int64_t n, int parts) {
+    for (int64_t i = ((int64_t)blockIdx.x * kAddThreads + threadIdx.x) * 4; i < n;
+         i += (int64_t)gridDim.x * kAddThreads * 4) {
+        float s[4] = {};
+        for (int p = 0; p < parts; ++p)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (i + e < n) s[e] += from[p * n + i + e];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (i + e < n) to[i + e] = (T)s[e];
+    }
+}
+
+// ---- the launches ----
+
+constexpr int64_t kMaxBlocks = 1 << 20;
+
+// Tiles of LEN rows: the most that the runs of a call can have.
+inline unsigned slots(int64_t packed, int64_t S, int len) { return (unsigned)(packed / len + S + 2); }
+
+template <typename T, int DP, int WAVES, bool DIRECT>
+hipError_t forward_launch(const AttentionArgs &a, hipStream_t s) {
+    const unsigned total = slots(a.R * a.G.d, a.S, 32 * WAVES) * (unsigned)(a.Hk * a.parts);
+    const unsigned blocks = (unsigned)std::min<int64_t>(total, kMaxBlocks);
+    attention_kernel<T, DP, WAVES, DIRECT><<<blocks, WAVES * kWave, 0, s>>>(a, total);
+    return hipGetLastError();
+}
+
+template <typename T, int DP, int WAVES, bool DIRECT>
+hipError_t dq_launch(const AttentionArgs &a, hipStream_t s) {
+    const unsigned total = slots(a.R * a.G.d, a.S, 32 * WAVES) * (unsigned)a.Hk;
+    const unsigned blocks = (unsigned)std::min<int64_t>(total, kMaxBlocks);
+    attention_dq_kernel<T, DP, WAVES, DIRECT><<<blocks, WAVES * kWave, 0, s>>>(a, total);
+    return hipGetLastError();
+}
+
+template <typename T, int DP, int WAVES, bool DIRECT>
+hipError_t dkdv_launch(const AttentionArgs &a, hipStream_t s) {
+    const unsigned total = slots(a.K, a.S, 32 * WAVES) * (unsigned)(a.Hk * a.key_parts);
+    const unsigned blocks = (unsigned)std::min<int64_t>(total, kMaxBlocks);
+    attention_dkdv_kernel<T, DP, WAVES, DIRECT><<<blocks, WAVES * kWave, 0, s>>>(a, total);
+    return hipGetLastError();
+}
+
+template <typename T, int DP, int WAVES, bool DIRECT>
+hipError_t launch_one(const AttentionArgs &a, AttentionPass pass, hipStream_t s) {
+    if (pass == AttentionPass::kForward) return forward_launch<T, DP, WAVES, DIRECT>(a, s);
+    if (pass == AttentionPass::kQueries) return dq_launch<T, DP, WAVES, DIRECT>(a, s);
+    return dkdv_launch<T, DP, WAVES, DIRECT>(a, s);
+}
+
+template <typename T, int DP>
+hipError_t launch_width(const AttentionArgs &a, AttentionPass pass, bool large, bool direct, hipStream_t s) {
+    if (large) return direct ? launch_one<T, DP, 4, true>(a, pass, s) : launch_one<T, DP, 4, false>(a, pass, s);
+    return direct ? launch_one<T, DP, 1, true>(a, pass, s) : launch_one<T, DP, 1, false>(a, pass, s);
+}
+
+}  // namespace
+
+template <typename T>
+hipError_t launch_attention_pass(const AttentionArgs &a, AttentionPass pass, bool large, bool direct, hipStream_t s) {
+    if (a.D <= 32) return launch_width<T, 32>(a, pass, large, direct, s);
+    if (a.D <= 64) return launch_width<T, 64>(a, pass, large, direct, s);
+    if (a.D <= 96) return launch_width<T, 96>(a, pass, large, direct, s);
+    return launch_width<T, 128>(a, pass, large, direct, s);
+}
+
+template <typename T>
+hipError_t launch_attention_join(const AttentionArgs &a, hipStream_t s) {
+    const int64_t waves = kJoinThreads / kWave, blocks = (a.R * a.H + waves - 1) / waves;
+    attention_join_kernel<T><<<(unsigned)std::min(blocks, kMaxBlocks), kJoinThreads, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_attention_add(const AttentionArgs &a, hipStream_t s) {
+    const int64_t n = a.K * a.Hk * a.D, per = kAddThreads * 4;
+    const unsigned blocks = (unsigned)std::min((n + per - 1) / per, kMaxBlocks);
+    if (a.dk) attention_add_kernel<T><<<blocks, kAddThreads, 0, s>>>(a.partial_dk, (T *)a.dk, n, a.key_parts);
+    if (a.dv) attention_add_kernel<T><<<blocks, kAddThreads, 0, s>>>(a.partial_dv, (T *)a.dv, n, a.key_parts);
+    return hipGetLastError();
+}
+
+#define ATTENTION_OF(T)                                                                                          \
+    template hipError_t launch_attention_pass<T>(const AttentionArgs &, AttentionPass, bool, bool, hipStream_t); \
+    template hipError_t launch_attention_join<T>(const AttentionArgs &, hipStream_t);                            \
+    template hipError_t launch_attention_add<T>(const AttentionArgs &, hipStream_t)
+
+}  // namespace gspmm

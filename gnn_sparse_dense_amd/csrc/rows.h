@@ -1,6 +1,6 @@
 // Device-side helpers and argument structs of the row operators: the routed
-// exchange (rows sorted by expert and back), the segment product and the
-// layer norm.  Rows are packed row-major in fp32, bf16 or fp16; arithmetic is
+// exchange (rows sorted by expert and back), the segment product, the layer
+// norm, attention within segments and dropout.  Rows are packed row-major in fp32, bf16 or fp16; arithmetic is
 // fp32 throughout and every output is rounded once, when it is stored.
 #pragma once
 
@@ -166,5 +166,68 @@ struct SegmentArgs {
 int64_t segment_workspace_floats(int64_t R, int64_t E, int64_t I, int64_t O, int type);
 hipError_t launch_segment(const SegmentArgs &a, bool transposed, int type, hipStream_t s);
 hipError_t launch_segment_dw(const SegmentArgs &a, int type, hipStream_t s);
+
+// ---- attention within segments (attention.hip) ----
+
+constexpr int kAttentionMaxWidth = 128;
+
+struct Divisor {
+    uint32_t magic;
+    int shift, d;
+};
+
+enum class AttentionPass { kForward, kQueries, kKeys };
+
+struct AttentionArgs {
+    const int64_t *offsets;  // [S + 1] into the rows of q
+    const int64_t *key_offsets;  // [S + 1] into those of k and v
+    int64_t R;               // rows of q
+    int64_t K;               // rows of k and v
+    int64_t S;
+    int64_t H;
+    int64_t Hk;
+    int64_t D;
+    Divisor G;               // H / Hk
+    const void *q;           // [R, H, D], rows ldq elements apart
+    const void *k;           // [K, Hk, D], ldk
+    const void *v;           // [K, Hk, D], ldv
+    int64_t ldq, ldk, ldv;
+    float scale;
+    int causal;
+    void *out;               // [R, H, D] (backward: read)
+    float *lse;              // [R, H] or nullptr: base-2 logarithm of the sum of 2^score, scores in base 2;
+                             // infinity where a row sees nothing
+    int parts;               // of the keys; above 1:
+    float *partial;          // [parts, R, H, D], unscaled
+    float *partial_top;      // [parts, R, H]
+    float *partial_sum;      // [parts, R, H]
+    const void *dout;        // [R, H, D]
+    float *delta;            // [R, H]
+    void *dq;                // [R, H, D] or nullptr
+    void *dk;                // [K, Hk, D] or nullptr
+    void *dv;                // [K, Hk, D] or nullptr
+    int key_parts;           // of the rows; above 1:
+    float *partial_dk;       // [key_parts, K, Hk, D]
+    float *partial_dv;       // [key_parts, K, Hk, D]
+};
+int64_t attention_workspace_floats(int64_t R, int64_t K, int64_t S, int64_t H, int64_t Hk, int64_t D);
+int64_t attention_backward_workspace_floats(int64_t R, int64_t K, int64_t S, int64_t H, int64_t Hk, int64_t D);
+hipError_t launch_attention(const AttentionArgs &a, float *workspace, int type, hipStream_t s);
+hipError_t launch_attention_backward(const AttentionArgs &a, float *workspace, int type, hipStream_t s);
+
+// ---- dropout (dropout.hip) ----
+
+struct DropoutArgs {
+    const void *x;           // [n]
+    const void *residual;    // [n] or nullptr (0)
+    void *y;                 // [n]
+    int64_t n;
+    const int64_t *seed;     // one number
+    int64_t offset;
+    uint32_t below;          // words below it drop their element
+    bool none;               // every element is dropped
+    float scale;             // 1 / (1 - p)
+};
+hipError_t launch_dropout(const DropoutArgs &a, int type, hipStream_t s);
 
 }  // namespace gspmm

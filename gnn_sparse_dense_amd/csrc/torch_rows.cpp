@@ -1,5 +1,6 @@
 // Differentiable row operators: torch autograd nodes around the C calls of
-// spmm.h (route, dispatch, combine, segment product, layer norm).  Host code
+// spmm.h (route, dispatch, combine, segment product, layer norm, attention
+// within segments, dropout).  Host code
 // only; the module checks tensors, allocates outputs through torch and
 // enqueues on torch's current stream.
 //
@@ -14,6 +15,8 @@
 #include <torch/csrc/autograd/functions/basic_ops.h>
 #include <torch/extension.h>
 
+#include <algorithm>
+#include <cmath>
 #include <stdexcept>
 #include <string>
 #include <unordered_set>
@@ -458,6 +461,154 @@ Tensor layer_norm(const Tensor &x, const std::optional<Tensor> &weight_, const s
                                        : normed(x.contiguous(), packed(weight), packed(bias), eps, {});
 }
 
+// ---- attention within segments ----
+
+// Rows whose heads stand next to each other are taken as they are, at any
+// distance (the parts of a joint projection); others are packed first.
+Tensor rows_apart(const Tensor &t) {
+    const bool heads = t.size(2) == 1 || t.stride(2) == 1;
+    const bool row = t.size(1) == 1 || t.stride(1) == t.size(2);
+    const bool apart = t.size(0) <= 1 || t.stride(0) >= t.size(1) * t.size(2);
+    return t.numel() && heads && row && apart && t.stride(0) < INT32_MAX ? t : t.contiguous();
+}
+
+int64_t apart(const Tensor &t) {
+    const int64_t width = t.size(1) * t.size(2);
+    return t.size(0) > 1 ? std::max(t.stride(0), width) : width;
+}
+
+struct Heads {
+    Tensor q, k, v, offsets, key_offsets;
+    bool causal;
+    double scale;
+
+    int64_t S() const { return offsets.size(0) - 1; }
+};
+
+Tensor attended(const Heads &h, const Tensor &lse) {
+    const int64_t R = h.q.size(0), H = h.q.size(1), D = h.q.size(2), K = h.k.size(0), Hk = h.k.size(1);
+    int64_t bytes;
+    check(spmm_segment_attention_workspace(R, K, h.S(), H, Hk, D, code(h.q), &bytes));
+    const Tensor work = scratch(bytes, h.q), out = at::empty(h.q.sizes(), h.q.options());
+    check(spmm_segment_attention(ptr(h.q), apart(h.q), ptr(h.k), apart(h.k), ptr(h.v), apart(h.v),
+                                 ptr<int64_t>(h.offsets), ptr<int64_t>(h.key_offsets), ptr(out), ptr<float>(lse), R, K,
+                                 h.S(), H, Hk, D, h.scale, h.causal, code(h.q), ptr(work), bytes, stream_of(h.q)));
+    return out;
+}
+
+struct SegmentAttention : torch::autograd::Function<SegmentAttention> {
+    static Tensor forward(AutogradContext *ctx, const Tensor &q, const Tensor &k, const Tensor &v, const Heads &given) {
+        const Heads h = {rows_apart(q), rows_apart(k), rows_apart(v), given.offsets, given.key_offsets, given.causal,
+                         given.scale};
+        const Tensor lse = at::empty({q.size(0), q.size(1)}, q.options().dtype(at::kFloat));
+        const Tensor out = attended(h, lse);
+        ctx->save_for_backward({h.q, h.k, h.v, h.offsets, h.key_offsets, out, lse});
+        ctx->saved_data["causal"] = h.causal;
+        ctx->saved_data["scale"] = h.scale;
+        return out;
+    }
+
+    static variable_list backward(AutogradContext *ctx, variable_list grads) {
+        refuse_nodes_outside_capture(grads[0]);
+        const variable_list saved = ctx->get_saved_variables();
+        const Heads h = {saved[0], saved[1], saved[2], saved[3], saved[4], ctx->saved_data["causal"].toBool(),
+                         ctx->saved_data["scale"].toDouble()};
+        const Tensor &out = saved[5], &lse = saved[6], dout = grads[0].contiguous();
+        const int64_t R = h.q.size(0), H = h.q.size(1), D = h.q.size(2), K = h.k.size(0), Hk = h.k.size(1);
+        Tensor dq, dk, dv;
+        if (ctx->needs_input_grad(0)) dq = at::empty(h.q.sizes(), h.q.options());
+        if (ctx->needs_input_grad(1)) dk = at::empty(h.k.sizes(), h.k.options());
+        if (ctx->needs_input_grad(2)) dv = at::empty(h.v.sizes(), h.v.options());
+        int64_t bytes;
+        check(spmm_segment_attention_backward_workspace(R, K, h.S(), H, Hk, D, code(h.q), &bytes));
+        const Tensor work = scratch(bytes, h.q);
+        check(spmm_segment_attention_backward(ptr(h.q), apart(h.q), ptr(h.k), apart(h.k), ptr(h.v), apart(h.v),
+                                              ptr<int64_t>(h.offsets), ptr<int64_t>(h.key_offsets), ptr(out),
+                                              ptr<float>(lse), ptr(dout), ptr(dq), ptr(dk), ptr(dv), R, K, h.S(), H,
+                                              Hk, D, h.scale, h.causal, code(h.q), ptr(work), bytes, stream_of(h.q)));
+        return once(grads, {dq, dk, dv, Tensor()}, {{0, 1, 2}, {0, 1, 2}, {0, 1, 2}});
+    }
+};
+
+Tensor segment_attention(const Tensor &q, const Tensor &k, const Tensor &v, const Tensor &offsets_,
+                         const std::optional<Tensor> &key_offsets_, bool causal, std::optional<double> scale) {
+    rows_type("q", q, 3);
+    rows_type("k", k, 3);
+    rows_type("v", v, 3);
+    if (k.scalar_type() != q.scalar_type() || v.scalar_type() != q.scalar_type())
+        throw py::type_error("q (" + name_of(q.scalar_type()) + "), k (" + name_of(k.scalar_type()) + ") and v (" +
+                             name_of(v.scalar_type()) + ") must have one type");
+    check_like("q", q, q.sizes(), q.device());
+    check_like("k", k, {k.size(0), k.size(1), q.size(2)}, q.device());
+    check_like("v", v, k.sizes(), q.device());
+    if (offsets_.dim() != 1 || offsets_.size(0) < 2)
+        throw py::value_error("offsets has shape " + name_of(offsets_.sizes()) + ", expected (segments + 1,)");
+    check_offsets(offsets_, offsets_.size(0) - 1, q.device());
+    const Tensor offsets = offsets_.contiguous();
+    Tensor key_offsets = offsets;
+    if (key_offsets_) {
+        if (key_offsets_->scalar_type() != at::kLong)
+            throw py::type_error("key_offsets must be int64, got " + name_of(key_offsets_->scalar_type()));
+        check_like("key_offsets", *key_offsets_, offsets.sizes(), q.device());
+        key_offsets = key_offsets_->contiguous();
+    } else if (q.size(0) != k.size(0)) {
+        throw py::value_error("q has " + std::to_string(q.size(0)) + " rows and k " + std::to_string(k.size(0)) +
+                              ": key_offsets are needed");
+    }
+    const double by = scale.value_or(1.0 / std::sqrt((double)q.size(2)));
+    if (wants_grad(q, k, v)) return SegmentAttention::apply(q, k, v, Heads{{}, {}, {}, offsets, key_offsets, causal, by});
+    return attended({rows_apart(q), rows_apart(k), rows_apart(v), offsets, key_offsets, causal, by}, {});
+}
+
+// ---- dropout ----
+
+Tensor dropped(const Tensor &x, const Tensor &residual, const Tensor &seed, double p, int64_t offset) {
+    const Tensor y = at::empty(x.sizes(), x.options());
+    check(spmm_dropout(ptr(x), ptr(residual), ptr(y), x.numel(), p, ptr<int64_t>(seed), offset, code(x),
+                       stream_of(x)));
+    return y;
+}
+
+struct Dropout : torch::autograd::Function<Dropout> {
+    static Tensor forward(AutogradContext *ctx, const Tensor &x, const std::optional<Tensor> &residual,
+                          const Tensor &seed, double p, int64_t offset) {
+        ctx->save_for_backward({seed});
+        ctx->saved_data["p"] = p;
+        ctx->saved_data["offset"] = offset;
+        ctx->saved_data["residual"] = residual.has_value();
+        return dropped(x.contiguous(), packed(residual.value_or(Tensor())), seed, p, offset);
+    }
+
+    static variable_list backward(AutogradContext *ctx, variable_list grads) {
+        refuse_nodes_outside_capture(grads[0]);
+        const Tensor seed = ctx->get_saved_variables()[0];
+        Tensor dx;
+        if (ctx->needs_input_grad(0))
+            dx = dropped(grads[0].contiguous(), {}, seed, ctx->saved_data["p"].toDouble(),
+                         ctx->saved_data["offset"].toInt());
+        // the residual's gradient is dy itself, graph and all
+        const Tensor dresidual = ctx->saved_data["residual"].toBool() ? grads[0] : Tensor();
+        return once(grads, {dx, dresidual, Tensor(), Tensor(), Tensor()}, {{}});
+    }
+};
+
+Tensor dropout(const Tensor &x, double p, const Tensor &seed, int64_t offset, const std::optional<Tensor> &residual_) {
+    rows_type("x", x, x.dim());
+    check_like("x", x, x.sizes(), x.device());
+    const Tensor residual = residual_.value_or(Tensor());
+    if (residual.defined()) {
+        if (residual.scalar_type() != x.scalar_type())
+            throw py::type_error("residual must be " + name_of(x.scalar_type()) + ", got " +
+                                 name_of(residual.scalar_type()));
+        check_like("residual", residual, x.sizes(), x.device());
+    }
+    if (seed.scalar_type() != at::kLong) throw py::type_error("seed must be int64, got " + name_of(seed.scalar_type()));
+    if (seed.numel() != 1) throw py::value_error("seed must have one element, got " + std::to_string(seed.numel()));
+    check_like("seed", seed, seed.sizes(), x.device());
+    return wants_grad(x, residual) ? Dropout::apply(x, residual_, seed, p, offset)
+                                   : dropped(x.contiguous(), packed(residual), seed, p, offset);
+}
+
 }  // namespace
 
 PYBIND11_MODULE(_rows, m) {
@@ -475,4 +626,6 @@ PYBIND11_MODULE(_rows, m) {
     m.def("combine", &combine);
     m.def("segment_matmul", &segment_matmul);
     m.def("layer_norm", &layer_norm);
+    m.def("segment_attention", &segment_attention);
+    m.def("dropout", &dropout);
 }

@@ -1,5 +1,6 @@
 """Row operators: what a layer around the aggregation does with its rows when
-each row belongs to one or more experts (or node types), and the layer norm.
+each row belongs to one or more experts (or node types), the layer norm,
+attention within segments and dropout.
 
     route = RowRoute(expert, E)              # expert [T, k] int64: each row's experts
     xs = dispatch(route, x)                  # [T * k, N]: rows in expert order
@@ -7,14 +8,19 @@ each row belongs to one or more experts (or node types), and the layer norm.
     out = combine(route, h, weight)          # [T, O]: summed back, weighted
     y = layer_norm(out, gamma, beta)
 
+and, among the rows of each graph or sequence of a packed batch,
+
+    a = segment_attention(q, k, v, offsets)  # q [R, H, D], k and v [K, Hk, D]
+    y = dropout(a, 0.1, seed, 0, residual)   # no mask is stored
+
 Rows are fp32, bf16 or fp16 matrices; sums are fp32 and outputs are rounded
-once.  All five run on torch's current stream of the tensors' device,
+once.  All run on torch's current stream of the tensors' device,
 allocate through torch and never wait for the GPU, so they can be captured
 into a graph (a backward pass only while no eager graph of the same leaves
 lives that was built on the default stream, since torch ties a leaf's gradient
 to the stream it was first used on: refused for every leaf that the pass leads
 to from one of these operators).
-dispatch, combine, segment_matmul and layer_norm are differentiable (once);
+All but RowRoute are differentiable (once);
 the spmm_* functions are the C calls on the caller's tensors.
 """
 from __future__ import annotations
@@ -227,6 +233,65 @@ def spmm_layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias) -> N
                                          _ptr(dweight), _ptr(dbias), R, N, kind, at, n, _current_stream(x)))
 
 
+def _check_heads(q, k, v, offsets, key_offsets):
+    kind = _check_rows_type("q", q, 3)
+    _check_rows_type("k", k, 3)
+    R, H, D = q.shape
+    K, Hk = k.shape[:2]
+    for name, t, shape in (("q", q, (R, H, D)), ("k", k, (K, Hk, D)), ("v", v, (K, Hk, D))):
+        _check_tensor(name, t, (q.dtype,), shape, q.device)
+    S = offsets.shape[0] - 1
+    _check_tensor("offsets", offsets, (torch.int64,), (S + 1,), q.device)
+    _check_tensor("key_offsets", key_offsets, (torch.int64,), (S + 1,), q.device)
+    return (R, K, S, H, Hk, D), kind
+
+
+def spmm_segment_attention(q, k, v, offsets, key_offsets, out, lse=None, causal: bool = False, scale: float = 1.0) -> None:
+    """out [R, H, D] = attention of q [R, H, D] to k and v [K, Hk, D] within
+    the segments; lse (fp32 [R, H]) is what the backward pass reads."""
+    sizes, kind = _check_heads(q, k, v, offsets, key_offsets)
+    R, K, S, H, Hk, D = sizes
+    _check_tensor("out", out, (q.dtype,), q.shape, q.device)
+    if lse is not None:
+        _check_tensor("lse", lse, (torch.float32,), (R, H), q.device)
+    ws, at, n = _workspace(q.device, "spmm_segment_attention_workspace", *sizes, kind)
+    _check(_lib.spmm_segment_attention(_ptr(q), H * D, _ptr(k), Hk * D, _ptr(v), Hk * D, _ptr(offsets),
+                                       _ptr(key_offsets), _ptr(out), _ptr(lse), *sizes, float(scale), int(causal),
+                                       kind, at, n, _current_stream(q)))
+
+
+def spmm_segment_attention_backward(q, k, v, offsets, key_offsets, out, lse, dout, dq, dk, dv, causal: bool = False,
+                                    scale: float = 1.0) -> None:
+    """Gradients of the attention; any of dq [R, H, D], dk and dv [K, Hk, D]
+    may be None."""
+    sizes, kind = _check_heads(q, k, v, offsets, key_offsets)
+    R, K, S, H, Hk, D = sizes
+    _check_tensor("out", out, (q.dtype,), q.shape, q.device)
+    _check_tensor("lse", lse, (torch.float32,), (R, H), q.device)
+    _check_tensor("dout", dout, (q.dtype,), q.shape, q.device)
+    for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
+        if t is not None:
+            _check_tensor(name, t, (q.dtype,), like.shape, q.device)
+    ws, at, n = _workspace(q.device, "spmm_segment_attention_backward_workspace", *sizes, kind)
+    _check(_lib.spmm_segment_attention_backward(_ptr(q), H * D, _ptr(k), Hk * D, _ptr(v), Hk * D, _ptr(offsets),
+                                                _ptr(key_offsets), _ptr(out), _ptr(lse), _ptr(dout), _ptr(dq),
+                                                _ptr(dk), _ptr(dv), *sizes, float(scale), int(causal), kind, at, n,
+                                                _current_stream(q)))
+
+
+def spmm_dropout(x, residual, y, p: float, seed, offset: int = 0) -> None:
+    """y = residual (or None: 0) + the kept elements of x / (1 - p); seed is
+    int64 [1] on the GPU."""
+    kind = _check_rows_type("x", x, x.dim())
+    _check_tensor("x", x, (x.dtype,), x.shape, x.device)
+    _check_tensor("y", y, (x.dtype,), x.shape, x.device)
+    if residual is not None:
+        _check_tensor("residual", residual, (x.dtype,), x.shape, x.device)
+    _check_tensor("seed", seed, (torch.int64,), (1,), x.device)
+    _check(_lib.spmm_dropout(_ptr(x), _ptr(residual), _ptr(y), x.numel(), float(p), _ptr(seed), int(offset), kind,
+                             _current_stream(x)))
+
+
 # ------------------------------------------------------- differentiable calls
 
 class RowRoute:
@@ -280,3 +345,31 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5):
     sqrt(var + eps) * weight + bias with the biased variance; weight and bias
     [N] in fp32 or x's type (None: 1 and 0).  Differentiable in all three."""
     return _rows.layer_norm(x, weight, bias, eps)
+
+
+def segment_attention(q, k, v, offsets, key_offsets=None, causal: bool = False, scale=None):
+    """out [R, H, D]: each row of q [R, H, D] attends to the keys of its
+    segment, the softmax of scale * q.k (None: D ** -0.5) times v, with k and v
+    [K, Hk, D] of q's type, H a multiple of Hk (H / Hk heads share a key head)
+    and D up to 128.  offsets int64 [S + 1] on the GPU bounds the segments'
+    rows, as in segment_matmul; key_offsets theirs in k and v (None: offsets).
+    causal: with n rows and m keys in a segment, its row i sees its keys
+    j <= i + m - n, so a single new row sees all of its sequence.  Rows that see
+    nothing, and rows outside the segments, are zero.  q, k and v may be parts
+    of a wider row (a joint projection): they are read in place where their
+    heads are packed.  Differentiable in q, k and v."""
+    return _rows.segment_attention(q, k, v, offsets, key_offsets, causal, scale)
+
+
+def dropout(x, p: float, seed, offset: int = 0, residual=None):
+    """residual + x / (1 - p) where an element is kept (a share 1 - p of them),
+    residual (None: 0) where it is dropped; x and residual of one shape (any)
+    and type.  No mask is stored: seed (an int64 tensor of one element on the
+    GPU, or a Python int), offset and an element's number in x say whether it
+    is kept, forward and backward alike.  Give each step another seed (the
+    tensor may change between the replays of a captured step, but not between
+    a forward pass and its backward pass) and each call of a step another
+    offset.  Differentiable in x and residual."""
+    if not isinstance(seed, torch.Tensor):
+        seed = torch.full((1,), int(seed), dtype=torch.int64, device=x.device)
+    return _rows.dropout(x, p, seed, offset, residual)

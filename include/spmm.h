@@ -459,7 +459,8 @@ spmm_plan_t spmm_plan_permute(spmm_plan_t plan, const int64_t *perm);
 /*
  * Row operators: what a layer around the aggregation does with its rows when
  * each row belongs to one or more experts (or node types): sorting rows by
- * expert and back, a product per expert, and the layer norm.
+ * expert and back, a product per expert, and the layer norm; attention among
+ * the rows of each graph or sequence of a batch, and dropout.
  *
  * Rows are packed row-major matrices of one element type (enum spmm_type);
  * sums are fp32 and every output element is rounded once.  Weights are fp32
@@ -549,6 +550,60 @@ int spmm_layer_norm_workspace(int64_t R, int64_t N, int type, int64_t *bytes);
 int spmm_layer_norm_backward(const void *dy, const void *x, const void *weight, int weight_type, const float *mean,
                              const float *rstd, void *dx, void *dweight, void *dbias, int64_t R, int64_t N, int type,
                              void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * Attention among the rows of each segment (the nodes of one graph of a
+ * batch, the tokens of one sequence of a packed batch).  Segment s has the
+ * rows offsets[s] <= i < offsets[s + 1] of q [R, H, D] and the keys
+ * key_offsets[s] <= j < key_offsets[s + 1] of k and v [K, Hk, D] (int64
+ * [S + 1] on the device, non-decreasing; bounds outside the rows are clamped,
+ * a decreasing list leaves rows unwritten but touches nothing outside; one
+ * list may serve both).  H is a multiple of Hk: head h reads key head
+ * h / (H / Hk).  Over the keys that row i sees (causal == 0: those of its
+ * segment; else, with n rows and m keys in the segment, key j of it where
+ * j <= i + m - n, both counted from the segment's start: the last row sees
+ * all keys)
+ *   out[i] = sum_j p_ij v[j],  p_ij = exp(scale q[i].k[j]) / sum_j exp(..)
+ * and zero where there are none (also for rows outside the segments, whose
+ * contents reach nothing; within a segment an infinity or NaN of a row or key
+ * may reach all of the segment's rows, also those that do not see it).
+ * Row r of q starts ldq >= H * D elements behind row r - 1, of k and v
+ * ldk, ldv >= Hk * D; out and all gradients are packed.  lse (fp32 [R, H] or
+ * NULL) is kept for
+ *   spmm_segment_attention_backward: dq, dk, dv (any may be NULL) from dout
+ *   and the forward pass's out and lse.
+ * Probabilities and their gradients are rounded to `type` where they enter a
+ * matrix product; sums and softmax statistics are fp32.
+ * scale > 0; D <= 128; R * H and K * Hk < 2^31 - 4097, S * Hk < 2^24,
+ * H < 2^16.
+ */
+int spmm_segment_attention_workspace(int64_t R, int64_t K, int64_t S, int64_t H, int64_t Hk, int64_t D, int type,
+                                     int64_t *bytes);
+int spmm_segment_attention(const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv,
+                           const int64_t *offsets, const int64_t *key_offsets, void *out, float *lse, int64_t R,
+                           int64_t K, int64_t S, int64_t H, int64_t Hk, int64_t D, double scale, int causal, int type,
+                           void *workspace, int64_t workspace_bytes, void *stream);
+int spmm_segment_attention_backward_workspace(int64_t R, int64_t K, int64_t S, int64_t H, int64_t Hk, int64_t D,
+                                              int type, int64_t *bytes);
+int spmm_segment_attention_backward(const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv,
+                                    const int64_t *offsets, const int64_t *key_offsets, const void *out,
+                                    const float *lse, const void *dout, void *dq, void *dk, void *dv, int64_t R,
+                                    int64_t K, int64_t S, int64_t H, int64_t Hk, int64_t D, double scale, int causal,
+                                    int type, void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * Dropout of n elements: y[i] = residual[i] + (kept(i) ? x[i] / (1 - p) : 0)
+ * (residual NULL: 0), one fused multiply-add per element.  kept(i) depends on
+ * i, seed[0], offset and p alone: word i % 4 of Philox 4x32 with 10 rounds of
+ * the counter (i / 4 in its low, offset in its high 64 bits) and the key
+ * seed[0] is at least p * 2^32, rounded to an integer.  Dropped elements of x
+ * are not read into y; p = 1 drops all.  The gradient of x is the same call on
+ * dy without a residual.  seed is one int64 on the device, so that a captured
+ * call follows it; offset tells the calls of one step apart.
+ * 0 <= p <= 1, n < 2^59.
+ */
+int spmm_dropout(const void *x, const void *residual, void *y, int64_t n, double p, const int64_t *seed,
+                 int64_t offset, int type, void *stream);
 
 /* The calling thread's last status; copies its message (NUL-terminated,
  * truncated to cap bytes) into buf when buf != NULL and cap > 0. */
