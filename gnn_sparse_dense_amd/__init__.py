@@ -53,7 +53,8 @@ EXPORTED = (
     "spmm_route_combine_backward", "spmm_segment_product", "spmm_segment_product_dx", "spmm_segment_workspace",
     "spmm_segment_product_dw", "spmm_layer_norm", "spmm_layer_norm_workspace", "spmm_layer_norm_backward",
     "spmm_segment_attention_workspace", "spmm_segment_attention", "spmm_segment_attention_backward_workspace",
-    "spmm_segment_attention_backward", "spmm_dropout",
+    "spmm_segment_attention_backward", "spmm_dropout", "spmm_linear_cross_entropy_workspace",
+    "spmm_linear_cross_entropy", "spmm_linear_cross_entropy_backward",
 )
 
 SPMM_F32, SPMM_BF16, SPMM_F16 = 0, 1, 2
@@ -65,7 +66,9 @@ _ROW_OPERATORS = (
     "spmm_route_build", "spmm_route_dispatch", "spmm_route_combine", "spmm_route_combine_backward",
     "spmm_segment_product", "spmm_segment_product_dx", "spmm_segment_product_dw",
     "spmm_layer_norm", "spmm_layer_norm_backward",
-    "segment_attention", "dropout", "spmm_segment_attention", "spmm_segment_attention_backward", "spmm_dropout",
+    "segment_attention", "dropout", "linear_cross_entropy", "spmm_segment_attention",
+    "spmm_segment_attention_backward", "spmm_dropout", "spmm_linear_cross_entropy",
+    "spmm_linear_cross_entropy_backward",
 )
 
 
@@ -189,6 +192,9 @@ def _load() -> ctypes.CDLL:
         "spmm_segment_attention_backward_workspace": [i64] * 6 + [i32, pi64],
         "spmm_segment_attention_backward": heads + [p] * 6 + [i64] * 6 + [f64, i32, i32, p, i64, p],
         "spmm_dropout": [p, p, p, i64, f64, p, i64, i32, p],
+        "spmm_linear_cross_entropy_workspace": [i64, i64, i64, i32, pi64, pi64, pi64],
+        "spmm_linear_cross_entropy": [p, p, p, p, i64, i64, i64, i32, i32, p, i64, p, i64, p],
+        "spmm_linear_cross_entropy_backward": [p, p, p, p, p, p, i64, i64, i64, i32, i32, p, i64, p, i64, p],
     }.items():
         fn = getattr(lib, name)
         fn.argtypes, fn.restype = args, i32

@@ -44,6 +44,7 @@ SOURCES = [
     "attention_f32.hip",
     "attention_bf16.hip",
     "attention_f16.hip",
+    "loss.hip",
 ]
 
 COMMON = [

@@ -2210,3 +2210,107 @@ SPMM_API int spmm_dropout(const void *x, const void *residual, void *y, int64_t 
     a.scale = a.none ? 0.0f : (float)(1.0 / (1.0 - p));
     return launched(launch_dropout(a, type, reinterpret_cast<hipStream_t>(stream)), "dropout launch");
 }
+
+static int check_loss(int64_t R, int64_t I, int64_t V, int type) {
+    if (R < 0) return fail(SPMM_E_INVALID_ARG, "negative size");
+    if (I < 1 || V < 1) return fail(SPMM_E_INVALID_ARG, "I and V must be positive");
+    if (R >= INT_MAX || I >= (1 << 24) || V >= INT_MAX)
+        return fail(SPMM_E_UNSUPPORTED, "R and V must be below 2^31 - 1, and I below 2^24");
+    if (V >= (int64_t(1) << 50) / I || R >= (int64_t(1) << 50) / V || R >= (int64_t(1) << 50) / I)
+        return fail(SPMM_E_UNSUPPORTED, "x, w or their product have too many elements");
+    return check_types(type, false, 0);
+}
+
+static int check_reduction(int reduction) {
+    if (reduction != SPMM_LOSS_ROWS && reduction != SPMM_LOSS_SUM && reduction != SPMM_LOSS_MEAN)
+        return fail(SPMM_E_INVALID_ARG, "unknown reduction %d", reduction);
+    return SPMM_OK;
+}
+
+SPMM_API int spmm_linear_cross_entropy_workspace(int64_t R, int64_t I, int64_t V, int type, int64_t *state_bytes,
+                                                 int64_t *bytes, int64_t *backward_bytes) {
+    if (!state_bytes || !bytes || !backward_bytes) return fail(SPMM_E_INVALID_ARG, "output is NULL");
+    if (const int st = check_loss(R, I, V, type)) return st;
+    *state_bytes = loss_state_bytes(R);
+    *bytes = loss_workspace_floats(R, V) * (int64_t)sizeof(float);
+    *backward_bytes = loss_backward_workspace_bytes(R, I, V, type);
+    return succeed();
+}
+
+SPMM_API int spmm_linear_cross_entropy(const void *x, const void *w, const int64_t *target, float *loss, int64_t R,
+                                       int64_t I, int64_t V, int reduction, int type, void *state,
+                                       int64_t state_bytes, void *workspace, int64_t workspace_bytes, void *stream) {
+    if (const int st = check_loss(R, I, V, type)) return st;
+    if (const int st = check_reduction(reduction)) return st;
+    const int64_t kept = loss_state_bytes(R), need = loss_workspace_floats(R, V) * (int64_t)sizeof(float);
+    if (state_bytes < kept)
+        return fail(SPMM_E_INVALID_ARG, "state of %lld bytes, %lld are needed", (long long)state_bytes,
+                    (long long)kept);
+    if (const int st = check_workspace(need, workspace_bytes)) return st;
+    const int64_t size = type_size(type), losses = reduction == SPMM_LOSS_ROWS ? R : 1;
+    int device;
+    if (const int st = check_arrays({{"x", x, R * I * size, (size_t)size, false},
+                                     {"w", w, R ? V * I * size : 0, (size_t)size, false},
+                                     {"target", target, R * 8, 8, false},
+                                     {"loss", loss, losses * 4, 4, true},
+                                     {"state", state, kept, 8, true},
+                                     {"workspace", workspace, need, 4, true}},
+                                    &device))
+        return st;
+    DeviceGuard dg(device);
+    LossArgs a = {};
+    a.x = x;
+    a.w = w;
+    a.target = target;
+    a.R = R;
+    a.I = I;
+    a.V = V;
+    a.per_row = reduction == SPMM_LOSS_ROWS;
+    a.mean = reduction == SPMM_LOSS_MEAN;
+    (a.per_row ? a.row_loss : a.loss) = loss;
+    return launched(launch_loss(a, state, static_cast<float *>(workspace), type, reinterpret_cast<hipStream_t>(stream)),
+                    "linear cross entropy launch");
+}
+
+SPMM_API int spmm_linear_cross_entropy_backward(const void *x, const void *w, const int64_t *target,
+                                                const float *dloss, void *dx, void *dw, int64_t R, int64_t I,
+                                                int64_t V, int reduction, int type, const void *state,
+                                                int64_t state_bytes, void *workspace, int64_t workspace_bytes,
+                                                void *stream) {
+    if (const int st = check_loss(R, I, V, type)) return st;
+    if (const int st = check_reduction(reduction)) return st;
+    if (!dx && !dw) return fail(SPMM_E_INVALID_ARG, "dx and dw are both NULL");
+    const int64_t kept = loss_state_bytes(R), need = loss_backward_workspace_bytes(R, I, V, type);
+    if (state_bytes < kept)
+        return fail(SPMM_E_INVALID_ARG, "state of %lld bytes, %lld are needed", (long long)state_bytes,
+                    (long long)kept);
+    if (const int st = check_workspace(need, workspace_bytes)) return st;
+    if (R == 0 && !dw) return succeed();
+    const int64_t size = type_size(type), losses = reduction == SPMM_LOSS_ROWS ? R : 1;
+    int device;
+    if (const int st = check_arrays({{"x", x, R * I * size, (size_t)size, false},
+                                     {"w", w, R ? V * I * size : 0, (size_t)size, false},
+                                     {"target", target, R * 8, 8, false},
+                                     {"dloss", dloss, losses * 4, 4, false},
+                                     {"dx", dx, dx ? R * I * size : 0, (size_t)size, true},
+                                     {"dw", dw, dw ? V * I * size : 0, (size_t)size, true},
+                                     {"state", state, kept, 8, false},
+                                     {"workspace", workspace, need, 4, true}},
+                                    &device))
+        return st;
+    DeviceGuard dg(device);
+    LossArgs a = {};
+    a.x = x;
+    a.w = w;
+    a.target = target;
+    a.R = R;
+    a.I = I;
+    a.V = V;
+    a.per_row = reduction == SPMM_LOSS_ROWS;
+    a.mean = reduction == SPMM_LOSS_MEAN;
+    a.dloss = dloss;
+    a.dx = dx;
+    a.dw = dw;
+    return launched(launch_loss_backward(a, state, workspace, type, reinterpret_cast<hipStream_t>(stream)),
+                    "linear cross entropy backward launch");
+}

@@ -1,6 +1,6 @@
 // Device-side helpers and argument structs of the row operators: the routed
 // exchange (rows sorted by expert and back), the segment product, the layer
-// norm, attention within segments and dropout.  Rows are packed row-major in fp32, bf16 or fp16; arithmetic is
+// norm, attention within segments, dropout and a classifier's loss.  Rows are packed row-major in fp32, bf16 or fp16; arithmetic is
 // fp32 throughout and every output is rounded once, when it is stored.
 #pragma once
 
@@ -229,5 +229,42 @@ struct DropoutArgs {
     float scale;             // 1 / (1 - p)
 };
 hipError_t launch_dropout(const DropoutArgs &a, int type, hipStream_t s);
+
+// ---- the loss of a linear classifier (loss.hip) ----
+
+struct LossArgs {
+    const void *x;           // [R, I]
+    const void *w;           // [V, I]
+    const int64_t *target;   // [R]; outside [0, V): no loss
+    int64_t R;
+    int64_t I;
+    int64_t V;
+    bool per_row;            // dloss and the loss are [R]; else one number,
+    bool mean;               // the sum or the mean over the rows with a class
+    float *loss;             // one number (!per_row)
+    float *row_loss;         // [R] (per_row)
+    float *stats;            // [2, R], the n listed rows' maxima and inverse sums
+    int *rows;               // [R], the rows with a class
+    int64_t *count;          // how many
+    float *tile_top;         // [column tiles, R]
+    float *tile_sum;
+    float *picked;           // [R], the listed rows' logit of their class
+    int *block_count;
+    float *block_loss;       // or nullptr (per_row)
+    const float *dloss;
+    void *dx;                // [R, I] or nullptr
+    void *dw;                // [V, I] or nullptr
+    float *unit;             // per_row: power of two that dloss is held in
+    void *d;                 // [R, ldd], a piece's gradient of the logits
+    int64_t ldd;
+    void *packed;            // [R, I], the listed rows of x
+    float *dx_sum;           // [R, I]
+    float *dw_partial;
+};
+int64_t loss_state_bytes(int64_t R);
+int64_t loss_workspace_floats(int64_t R, int64_t V);
+int64_t loss_backward_workspace_bytes(int64_t R, int64_t I, int64_t V, int type);
+hipError_t launch_loss(const LossArgs &a, void *state, float *workspace, int type, hipStream_t s);
+hipError_t launch_loss_backward(const LossArgs &a, const void *state, void *workspace, int type, hipStream_t s);
 
 }  // namespace gspmm

@@ -89,6 +89,7 @@ struct Operand {
     int64_t outer;      // rows that exist
     int64_t inner;      // elements of a row that exist
     const T *end;       // end of the array
+    const int *rows = nullptr;      // KC: tile row r is row rows[r] from ptr (GATHER)
 };
 
 // Copies an operand's steps straight into LDS, 16 bytes per lane: for rows
@@ -98,8 +99,11 @@ struct Operand {
 // buffer); tile rows (KC) and columns (KS) that do not exist read what
 // follows in the same array, or zero behind its end: they only reach outputs
 // that are not stored.
-template <typename T, bool KC, int B, int WAVES>
+// GATHER (KC): rows by their list, within 2^31 - 1 bytes of ptr; the rows behind
+// the last one repeat it.
+template <typename T, bool KC, int B, int WAVES, bool GATHER = false>
 struct Copy {
+    static_assert(KC || !GATHER);
     static constexpr int kCopies = B * kStepBytes / 1024 / WAVES;
     static constexpr int kRowsPerCopy = KC ? 1024 / kStepBytes * WAVES : 1024 * WAVES / (B * (int)sizeof(T));
 
@@ -109,6 +113,7 @@ struct Copy {
     uint32_t at, next_copy; // byte offset of the lane's chunk of copy 0, and from one copy to the next
     int first;              // the lane's first summed element of copy 0 within a step
     int left;               // summed elements from the next step on
+    uint32_t listed[GATHER ? kCopies : 1];
 
     __device__ inline Copy(const Operand<T> &o, int wave) {
         const int byte = wave * 1024 + (threadIdx.x & (kWave - 1)) * 16;
@@ -122,6 +127,11 @@ struct Copy {
             left = uniform((int)o.inner);
             step_bytes = kStepBytes;
             at = row * row_bytes + chunk * 16;
+            if constexpr (GATHER) {
+#pragma unroll
+                for (int i = 0; i < kCopies; ++i)
+                    listed[i] = (uint32_t)o.rows[min(int64_t(row + i * kRowsPerCopy), o.outer - 1)] * row_bytes + chunk * 16;
+            }
         } else {
             constexpr int kRow = B * (int)sizeof(T);
             const int k = byte / kRow;
@@ -140,9 +150,11 @@ struct Copy {
 #pragma unroll
         for (int i = 0; i < kCopies; ++i) {
             const bool in = first + (KC ? 0 : i * kRowsPerCopy) < left;
+            uint32_t from = at + i * next_copy;
+            if constexpr (GATHER) from = listed[i];
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
                 rsrc, (__attribute__((address_space(3))) void *)(lds + (i * WAVES + wave) * 1024), 16,
-                in ? at + i * next_copy : 0x80000000u, 0, 0, 0);
+                in ? from : 0x80000000u, 0, 0, 0);
         }
         base += step_bytes;
         bytes -= step_bytes;
@@ -156,19 +168,21 @@ struct Copy {
 // on into the next, which exists; both only reach outputs that are not
 // stored.  The last step, and every step of rows below a pack, loads exactly
 // the elements that exist.
-template <typename T, bool KC, int B, int WAVES, bool WHOLE>
+template <typename T, bool KC, int B, int WAVES, bool WHOLE, bool GATHER = false>
 __device__ inline void fetch(const Operand<T> &o, int64_t k0, Pack<T> (&r)[B * kChunks / (WAVES * kWave)]) {
     constexpr int kPerRow = KC ? kStepBytes / 16 : B * (int)sizeof(T) / 16;
 #pragma unroll
     for (int i = 0; i < B * kChunks / (WAVES * kWave); ++i) {
         const int idx = threadIdx.x + i * WAVES * kWave, row = idx / kPerRow, c = idx % kPerRow * kPack<T>;
         if constexpr (WHOLE) {
-            const int64_t out = KC ? min(int64_t(row), o.outer - 1) : k0 + row;
+            int64_t out = KC ? min(int64_t(row), o.outer - 1) : k0 + row;
             const int64_t in = KC ? k0 + c : min(int64_t(c), o.inner - 1);
+            if constexpr (GATHER) out = o.rows[out];
             r[i] = load_pack(o.ptr + out * o.ld + in);
         } else {
-            const int64_t out = KC ? row : k0 + row, in = KC ? k0 + c : c;
-            const int64_t n = out < o.outer ? o.inner - in : 0;
+            int64_t out = KC ? row : k0 + row;
+            const int64_t in = KC ? k0 + c : c, n = out < o.outer ? o.inner - in : 0;
+            if constexpr (GATHER) out = o.rows[min(out, o.outer - 1)];
             r[i] = load_pack(o.ptr + out * o.ld + in, n);
         }
     }
@@ -282,14 +296,18 @@ struct Stages {
     __shared__ __attribute__((aligned(1024))) char name##3[bytes];                                  \
     const Stages name = {{(LdsByte *)name##0, (LdsByte *)name##1, (LdsByte *)name##2, (LdsByte *)name##3}}
 
-// The accumulators of a wave's part of a tile: rows 32 i and columns 32 j from
-// the wave's corner, laid out as multiply() leaves them.
+// The sums of a wave's part of a tile: rows 32 i and columns 32 j from the
+// wave's corner, laid out as multiply() leaves them.
 template <typename S>
-using Sums = f32x16[S::MI][S::NI];
+struct Sums {
+    f32x16 at[S::MI][S::NI];
+};
 
-// acc += A . B over K summed elements; LDS is free for other use afterwards.
-template <typename T, typename S, bool AKC, bool BKC, bool DIRECT>
-__device__ inline void tile_sums(const Stages &lds, const Operand<T> &a, const Operand<T> &b, int64_t K, Sums<S> &acc) {
+// out += A . B over K summed elements; LDS is free for other use afterwards.
+// GATHER: A's rows by their list.
+template <typename T, typename S, bool AKC, bool BKC, bool DIRECT, bool GATHER = false>
+__device__ inline void tile_sums(const Stages &lds, const Operand<T> &a, const Operand<T> &b, int64_t K, Sums<S> &out) {
+    f32x16 (&acc)[S::MI][S::NI] = out.at;
     constexpr int MI = S::MI, NI = S::NI, kA = S::BM * kStepBytes;
     const int wave = uniform((int)threadIdx.x / kWave);
     const int m0 = wave / S::WC * (MI * 32), n0 = wave % S::WC * (NI * 32);
@@ -322,7 +340,7 @@ __device__ inline void tile_sums(const Stages &lds, const Operand<T> &a, const O
         // stage t.  Copies behind the last step read nothing and write zeros,
         // so that every step waits for the same number of them; the loop body
         // has no branch, so that a read waits for the copies of its own stage.
-        Copy<T, AKC, S::BM, S::kWaves> ca(a, wave);
+        Copy<T, AKC, S::BM, S::kWaves, GATHER> ca(a, wave);
         Copy<T, BKC, S::BN, S::kWaves> cb(b, wave);
         constexpr int kCopies = decltype(ca)::kCopies + decltype(cb)::kCopies;
         // dw's large tiles have twice the LDS reads of y's: one copy (0x20) and
@@ -378,10 +396,10 @@ __device__ inline void tile_sums(const Stages &lds, const Operand<T> &a, const O
         auto fetch_step = [&](int t) {
             const int64_t k0 = (int64_t)t * kStep<T>;
             if (t < whole) {
-                fetch<T, AKC, S::BM, S::kWaves, true>(a, k0, ra);
+                fetch<T, AKC, S::BM, S::kWaves, true, GATHER>(a, k0, ra);
                 fetch<T, BKC, S::BN, S::kWaves, true>(b, k0, rb);
             } else {
-                fetch<T, AKC, S::BM, S::kWaves, false>(a, k0, ra);
+                fetch<T, AKC, S::BM, S::kWaves, false, GATHER>(a, k0, ra);
                 fetch<T, BKC, S::BN, S::kWaves, false>(b, k0, rb);
             }
         };
@@ -410,13 +428,15 @@ __device__ inline void tile_sums(const Stages &lds, const Operand<T> &a, const O
     }
 }
 
-// out[0..rows) x [0..cols) of a tile = acc.  The outputs go through LDS (the
+// out[0..rows) x [0..cols) of a tile = the sums.  The outputs go through LDS (the
 // stages, read out by now) so that a store covers whole rows of the tile: a lane
 // holds 4 columns of one row, and 32 rows to a store would reach the L2 as
-// 16-byte pieces.  Chunk c of row r stands at c ^ r.
-template <typename OUT, typename S>
-__device__ inline void tile_store(const Stages &lds, const Sums<S> &acc, OUT *out, int64_t ldo, int64_t rows,
-                                  int64_t cols, bool stream) {
+// 16-byte pieces.  Chunk c of row r stands at c ^ r.  `list`: row r goes to row
+// list[r] of out.
+template <typename OUT, typename S, bool LISTED = false>
+__device__ inline void tile_store(const Stages &lds, const Sums<S> &sums, OUT *out, int64_t ldo, int64_t rows,
+                                  int64_t cols, bool stream, const int *list = nullptr) {
+    const f32x16 (&acc)[S::MI][S::NI] = sums.at;
     constexpr int MI = S::MI, NI = S::NI;
     const int wave = uniform((int)threadIdx.x / kWave);
     const int n0 = wave % S::WC * (NI * 32);
@@ -458,8 +478,35 @@ __device__ inline void tile_store(const Stages &lds, const Sums<S> &acc, OUT *ou
         const auto o = lds_load<Pack<OUT>>(lds.at[r0 / kStageRows] + r % kStageRows * kRow +
                                            ((chunk ^ (r & (kRowChunks - 1))) << 4));
         if (r >= rows) continue;
-        if (stream) store_pack_stream(out + r * ldo + c, o, cols - c);
-        else store_pack(out + r * ldo + c, o, cols - c);
+        const int64_t to = LISTED ? list[r] : r;
+        if (stream) store_pack_stream(out + to * ldo + c, o, cols - c);
+        else store_pack(out + to * ldo + c, o, cols - c);
+    }
+}
+
+// out[0..rows) x [0..cols) of a tile = the sums (ADD: added to out) in fp32, straight from
+// the registers: the stages do not hold a large tile of fp32.
+template <typename S, bool ADD>
+__device__ inline void tile_store_fp32(const Sums<S> &sums, float *out, int64_t ldo, int64_t rows, int64_t cols) {
+    const f32x16 (&acc)[S::MI][S::NI] = sums.at;
+    const int wave = uniform((int)threadIdx.x / kWave), lane = threadIdx.x & (kWave - 1);
+    const int m0 = wave / S::WC * (S::MI * 32), n0 = wave % S::WC * (S::NI * 32);
+#pragma unroll
+    for (int i = 0; i < S::MI; ++i) {
+        const int r = m0 + i * 32 + (lane & 31);
+        if (r >= rows) continue;
+#pragma unroll
+        for (int j = 0; j < S::NI; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int c = n0 + j * 32 + q * 8 + (lane >> 5) * 4;
+                float *p = out + r * ldo + c;
+                Pack<float> v;
+                if constexpr (ADD) v = load_pack(p, cols - c);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v.v[e] = ADD ? v.v[e] + acc[i][j][q * 4 + e] : acc[i][j][q * 4 + e];
+                store_pack(p, v, cols - c);
+            }
     }
 }
 
@@ -467,9 +514,9 @@ __device__ inline void tile_store(const Stages &lds, const Sums<S> &acc, OUT *ou
 template <typename T, typename OUT, typename S, bool AKC, bool BKC, bool DIRECT>
 __device__ inline void tile_product(const Stages &lds, const Operand<T> &a, const Operand<T> &b, int64_t K, OUT *out,
                                     int64_t ldo, int64_t rows, int64_t cols, bool stream) {
-    f32x16 acc[S::MI][S::NI] = {};
-    tile_sums<T, S, AKC, BKC, DIRECT>(lds, a, b, K, acc);
-    tile_store<OUT, S>(lds, acc, out, ldo, rows, cols, stream);
+    Sums<S> sums = {};
+    tile_sums<T, S, AKC, BKC, DIRECT>(lds, a, b, K, sums);
+    tile_store<OUT, S>(lds, sums, out, ldo, rows, cols, stream);
 }
 
 }  // namespace

@@ -1,6 +1,6 @@
 // Differentiable row operators: torch autograd nodes around the C calls of
 // spmm.h (route, dispatch, combine, segment product, layer norm, attention
-// within segments, dropout).  Host code
+// within segments, dropout, a classifier's loss).  Host code
 // only; the module checks tensors, allocates outputs through torch and
 // enqueues on torch's current stream.
 //
@@ -609,6 +609,78 @@ Tensor dropout(const Tensor &x, double p, const Tensor &seed, int64_t offset, co
                                    : dropped(x.contiguous(), packed(residual), seed, p, offset);
 }
 
+// ---- the loss of a linear classifier ----
+
+struct LossSizes {
+    int64_t state, forward, backward;
+
+    LossSizes(const Tensor &x, const Tensor &w) {
+        check(spmm_linear_cross_entropy_workspace(x.size(0), x.size(1), w.size(0), code(x), &state, &forward,
+                                                  &backward));
+    }
+};
+
+Tensor lost(const Tensor &x, const Tensor &w, const Tensor &target, int64_t reduction, const Tensor &state,
+            const LossSizes &sizes) {
+    const Tensor work = scratch(sizes.forward, x);
+    const auto opts = x.options().dtype(at::kFloat);
+    const Tensor loss = reduction == SPMM_LOSS_ROWS ? at::empty({x.size(0)}, opts) : at::empty({}, opts);
+    check(spmm_linear_cross_entropy(ptr(x), ptr(w), ptr<int64_t>(target), ptr<float>(loss), x.size(0), x.size(1),
+                                    w.size(0), (int)reduction, code(x), ptr(state), sizes.state, ptr(work),
+                                    sizes.forward, stream_of(x)));
+    return loss;
+}
+
+struct LinearCrossEntropy : torch::autograd::Function<LinearCrossEntropy> {
+    static Tensor forward(AutogradContext *ctx, const Tensor &x_, const Tensor &w_, const Tensor &target,
+                          int64_t reduction) {
+        const Tensor x = x_.contiguous(), w = w_.contiguous();
+        const LossSizes sizes(x, w);
+        const Tensor state = scratch(sizes.state, x);
+        ctx->save_for_backward({x, w, target, state});
+        ctx->saved_data["reduction"] = reduction;
+        return lost(x, w, target, reduction, state, sizes);
+    }
+
+    static variable_list backward(AutogradContext *ctx, variable_list grads) {
+        refuse_nodes_outside_capture(grads[0]);
+        const variable_list saved = ctx->get_saved_variables();
+        const Tensor &x = saved[0], &w = saved[1], &target = saved[2], &state = saved[3], dloss = grads[0].contiguous();
+        const LossSizes sizes(x, w);
+        const Tensor work = scratch(sizes.backward, x);
+        Tensor dx, dw;
+        if (ctx->needs_input_grad(0)) dx = at::empty(x.sizes(), x.options());
+        if (ctx->needs_input_grad(1)) dw = at::empty(w.sizes(), w.options());
+        check(spmm_linear_cross_entropy_backward(ptr(x), ptr(w), ptr<int64_t>(target), ptr<float>(dloss), ptr(dx),
+                                                 ptr(dw), x.size(0), x.size(1), w.size(0),
+                                                 (int)ctx->saved_data["reduction"].toInt(), code(x), ptr(state),
+                                                 sizes.state, ptr(work), sizes.backward, stream_of(x)));
+        return once(grads, {dx, dw, Tensor(), Tensor()}, {{0, 1}, {0, 1}});
+    }
+};
+
+Tensor linear_cross_entropy(const Tensor &x, const Tensor &w, const Tensor &target_, const std::string &reduction) {
+    rows_type("x", x, 2);
+    rows_type("w", w, 2);
+    if (w.scalar_type() != x.scalar_type())
+        throw py::type_error("w must be " + name_of(x.scalar_type()) + ", got " + name_of(w.scalar_type()));
+    check_like("x", x, x.sizes(), x.device());
+    check_like("w", w, {w.size(0), x.size(1)}, x.device());
+    if (target_.scalar_type() != at::kLong)
+        throw py::type_error("target must be int64, got " + name_of(target_.scalar_type()));
+    check_like("target", target_, {x.size(0)}, x.device());
+    const int64_t by = reduction == "none"   ? SPMM_LOSS_ROWS
+                       : reduction == "sum"  ? SPMM_LOSS_SUM
+                       : reduction == "mean" ? SPMM_LOSS_MEAN
+                                             : -1;
+    if (by < 0) throw py::value_error("reduction must be 'none', 'sum' or 'mean', got '" + reduction + "'");
+    const Tensor target = target_.contiguous();
+    if (wants_grad(x, w)) return LinearCrossEntropy::apply(x, w, target, by);
+    const Tensor rows = x.contiguous(), classes = w.contiguous();
+    const LossSizes sizes(rows, classes);
+    return lost(rows, classes, target, by, scratch(sizes.state, rows), sizes);
+}
+
 }  // namespace
 
 PYBIND11_MODULE(_rows, m) {
@@ -628,4 +700,5 @@ PYBIND11_MODULE(_rows, m) {
     m.def("layer_norm", &layer_norm);
     m.def("segment_attention", &segment_attention);
     m.def("dropout", &dropout);
+    m.def("linear_cross_entropy", &linear_cross_entropy);
 }

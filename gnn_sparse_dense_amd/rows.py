@@ -1,6 +1,6 @@
 """Row operators: what a layer around the aggregation does with its rows when
 each row belongs to one or more experts (or node types), the layer norm,
-attention within segments and dropout.
+attention within segments, dropout and the loss of a linear classifier.
 
     route = RowRoute(expert, E)              # expert [T, k] int64: each row's experts
     xs = dispatch(route, x)                  # [T * k, N]: rows in expert order
@@ -12,6 +12,10 @@ and, among the rows of each graph or sequence of a packed batch,
 
     a = segment_attention(q, k, v, offsets)  # q [R, H, D], k and v [K, Hk, D]
     y = dropout(a, 0.1, seed, 0, residual)   # no mask is stored
+
+and the loss of a linear classifier over them, whose logits are not kept:
+
+    loss = linear_cross_entropy(y, w, target)  # w [V, N], target int64 [R]
 
 Rows are fp32, bf16 or fp16 matrices; sums are fp32 and outputs are rounded
 once.  All run on torch's current stream of the tensors' device,
@@ -292,6 +296,56 @@ def spmm_dropout(x, residual, y, p: float, seed, offset: int = 0) -> None:
                              _current_stream(x)))
 
 
+_REDUCTIONS = {"none": 0, "sum": 1, "mean": 2}
+
+
+@functools.lru_cache(maxsize=256)
+def _loss_bytes(R: int, I: int, V: int, kind: int):
+    """Bytes of the state and of the two workspaces."""
+    n = [ctypes.c_int64() for _ in range(3)]
+    _check(_lib.spmm_linear_cross_entropy_workspace(R, I, V, kind, *(ctypes.byref(b) for b in n)))
+    return tuple(b.value for b in n)
+
+
+def _check_loss(x, w, target, losses, name, reduction):
+    kind = _check_rows_type("x", x)
+    _check_rows_type("w", w)
+    R, I = x.shape
+    _check_tensor("x", x, (x.dtype,), x.shape, x.device)
+    _check_tensor("w", w, (x.dtype,), (w.shape[0], I), x.device)
+    _check_tensor("target", target, (torch.int64,), (R,), x.device)
+    if reduction not in _REDUCTIONS:
+        raise ValueError(f"reduction must be 'none', 'sum' or 'mean', got {reduction!r}")
+    _check_tensor(name, losses, (torch.float32,), (R,) if reduction == "none" else (), x.device)
+    return (R, I, w.shape[0]), kind
+
+
+def spmm_linear_cross_entropy(x, w, target, loss, reduction: str = "mean"):
+    """loss (fp32, [R] for "none", else a scalar) of x [R, I] against the
+    classes' rows w [V, I]; returns the state that the backward pass reads."""
+    sizes, kind = _check_loss(x, w, target, loss, "loss", reduction)
+    kept, n, _ = _loss_bytes(*sizes, kind)
+    state = torch.empty(kept, dtype=torch.uint8, device=x.device)
+    ws = torch.empty(n, dtype=torch.uint8, device=x.device)
+    _check(_lib.spmm_linear_cross_entropy(_ptr(x), _ptr(w), _ptr(target), _ptr(loss), *sizes, _REDUCTIONS[reduction],
+                                          kind, _ptr(state), kept, _ptr(ws), n, _current_stream(x)))
+    return state
+
+
+def spmm_linear_cross_entropy_backward(x, w, target, dloss, dx, dw, state, reduction: str = "mean") -> None:
+    """Gradients of the loss; either of dx [R, I] and dw [V, I] may be None."""
+    sizes, kind = _check_loss(x, w, target, dloss, "dloss", reduction)
+    kept, _, n = _loss_bytes(*sizes, kind)
+    for name, t, like in (("dx", dx, x), ("dw", dw, w)):
+        if t is not None:
+            _check_tensor(name, t, (x.dtype,), like.shape, x.device)
+    _check_tensor("state", state, (torch.uint8,), (kept,), x.device)
+    ws = torch.empty(n, dtype=torch.uint8, device=x.device)
+    _check(_lib.spmm_linear_cross_entropy_backward(_ptr(x), _ptr(w), _ptr(target), _ptr(dloss), _ptr(dx), _ptr(dw),
+                                                   *sizes, _REDUCTIONS[reduction], kind, _ptr(state), kept, _ptr(ws),
+                                                   n, _current_stream(x)))
+
+
 # ------------------------------------------------------- differentiable calls
 
 class RowRoute:
@@ -373,3 +427,13 @@ def dropout(x, p: float, seed, offset: int = 0, residual=None):
     if not isinstance(seed, torch.Tensor):
         seed = torch.full((1,), int(seed), dtype=torch.int64, device=x.device)
     return _rows.dropout(x, p, seed, offset, residual)
+
+
+def linear_cross_entropy(x, w, target, reduction: str = "mean"):
+    """Softmax cross entropy of the logits x . w^T without keeping them, for
+    x [R, I], a row of w [V, I] for each class and target int64 [R]: the loss
+    of each row ("none", fp32 [R]), their "sum" or their "mean".  A target
+    outside [0, V) means no class: the row has no loss, no gradient and does
+    not count in the mean (which is zero over no rows).  Differentiable in x
+    and w."""
+    return _rows.linear_cross_entropy(x, w, target, reduction)

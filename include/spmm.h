@@ -460,7 +460,8 @@ spmm_plan_t spmm_plan_permute(spmm_plan_t plan, const int64_t *perm);
  * Row operators: what a layer around the aggregation does with its rows when
  * each row belongs to one or more experts (or node types): sorting rows by
  * expert and back, a product per expert, and the layer norm; attention among
- * the rows of each graph or sequence of a batch, and dropout.
+ * the rows of each graph or sequence of a batch, dropout, and the loss of a
+ * linear classifier.
  *
  * Rows are packed row-major matrices of one element type (enum spmm_type);
  * sums are fp32 and every output element is rounded once.  Weights are fp32
@@ -604,6 +605,35 @@ int spmm_segment_attention_backward(const void *q, int64_t ldq, const void *k, i
  */
 int spmm_dropout(const void *x, const void *residual, void *y, int64_t n, double p, const int64_t *seed,
                  int64_t offset, int type, void *stream);
+
+/*
+ * Softmax cross entropy of a linear classifier, without its logits: for the
+ * rows x [R, I] with a class t = target[r] (int64 [R]) in [0, V), and the
+ * classes' rows w [V, I],
+ *   loss[r] = log sum_v exp(x[r].w[v]) - x[r].w[t].
+ * A target outside [0, V) means no class: such a row has no loss and a zero
+ * gradient, and what stands in it reaches nothing.  `reduction`: the loss of
+ * each row (fp32 [R], zero without a class), or the sum or the mean (over the
+ * rows with a class; zero where there are none) in one fp32.
+ *   spmm_linear_cross_entropy_backward: dx [R, I] and dw [V, I] (either may be
+ *   NULL) from dloss (fp32 [R] or one) and the forward pass's state.
+ * The gradient of the logits is rounded to `type` where it enters a matrix
+ * product; sums are fp32.  state (aligned to 8 bytes) is written by the
+ * forward and read by the backward pass; the workspace of the backward pass
+ * holds the gradient of the logits for as many classes at a time as fit
+ * 512 MB (256 at least).
+ * R, V < 2^31 - 1, I < 2^24.
+ */
+enum spmm_loss_reduction { SPMM_LOSS_ROWS = 0, SPMM_LOSS_SUM = 1, SPMM_LOSS_MEAN = 2 };
+int spmm_linear_cross_entropy_workspace(int64_t R, int64_t I, int64_t V, int type, int64_t *state_bytes,
+                                        int64_t *bytes, int64_t *backward_bytes);
+int spmm_linear_cross_entropy(const void *x, const void *w, const int64_t *target, float *loss, int64_t R, int64_t I,
+                              int64_t V, int reduction, int type, void *state, int64_t state_bytes, void *workspace,
+                              int64_t workspace_bytes, void *stream);
+int spmm_linear_cross_entropy_backward(const void *x, const void *w, const int64_t *target, const float *dloss,
+                                       void *dx, void *dw, int64_t R, int64_t I, int64_t V, int reduction, int type,
+                                       const void *state, int64_t state_bytes, void *workspace,
+                                       int64_t workspace_bytes, void *stream);
 
 /* The calling thread's last status; copies its message (NUL-terminated,
  * truncated to cap bytes) into buf when buf != NULL and cap > 0. */
