@@ -11,7 +11,7 @@ hipError_t launch_attention_pass(const AttentionArgs &a, AttentionPass pass, boo
 template <typename T>
 hipError_t launch_attention_join(const AttentionArgs &a, hipStream_t s);
 template <typename T>
-hipError_t launch_attention_add(const AttentionArgs &a, hipStream_t s);
+hipError_t launch_attention_add(const AttentionArgs &a, bool large, hipStream_t s);
 
 namespace {
 
@@ -46,9 +46,21 @@ int query_parts(int64_t R, int64_t K, int64_t S, int64_t H, int64_t Hk) {
     return (int)parts_of(tiles(R * (H / Hk), S, large) * Hk, large ? 512 : 2048, K, S, 64);
 }
 
+// Packed rows of a part of a key tile's rows: a third of what a compute unit has to
+// take of all tiles (the mean tile's rows; half of them are seen if causal), and
+// the most parts that a tile is cut into.
+constexpr int64_t kUnits = 256;
+constexpr int kMostParts = 16;
+
+int64_t part_rows(int64_t R, int64_t K, int64_t S, int64_t H, int64_t Hk) {
+    const int64_t rows = R * (H / Hk) / std::max<int64_t>(1, S);
+    const int64_t share = tiles(K, S, large_tiles(K, S)) * Hk * rows / (3 * kUnits);
+    return std::max<int64_t>(512, share);
+}
+
 int key_parts(int64_t R, int64_t K, int64_t S, int64_t H, int64_t Hk) {
-    const bool large = large_tiles(K, S);
-    return (int)parts_of(tiles(K, S, large) * Hk, large ? 512 : 2048, R * (H / Hk), S, 16);
+    const int64_t rows = R * (H / Hk) / std::max<int64_t>(1, S);      // the longest segment's are taken to be thrice the mean
+    return (int)std::max<int64_t>(1, std::min<int64_t>(kMostParts, 3 * rows / part_rows(R, K, S, H, Hk)));
 }
 
 }  // namespace
@@ -93,6 +105,7 @@ hipError_t launch_attention_backward(const AttentionArgs &args, float *workspace
     a.G = divisor(a.H / a.Hk);
     a.parts = 1;
     a.key_parts = key_parts(a.R, a.K, a.S, a.H, a.Hk);
+    a.part_rows = part_rows(a.R, a.K, a.S, a.H, a.Hk) / (a.causal ? 2 : 1);
     a.delta = workspace;
     a.partial_dk = workspace + a.R * a.H;
     a.partial_dv = a.partial_dk + a.key_parts * a.K * a.Hk * a.D;
@@ -109,9 +122,9 @@ hipError_t launch_attention_backward(const AttentionArgs &args, float *workspace
     const bool direct = direct_rows(a.q, a.ldq, a.D, size) && direct_rows(a.dout, a.H * a.D, a.D, size);
     if (const hipError_t e = pass(AttentionPass::kKeys, large_tiles(a.K, a.S), direct)) return e;
     if (a.key_parts == 1) return hipSuccess;
-    return type == SPMM_F32    ? launch_attention_add<float>(a, s)
-           : type == SPMM_BF16 ? launch_attention_add<__bf16>(a, s)
-                               : launch_attention_add<_Float16>(a, s);
+    return type == SPMM_F32    ? launch_attention_add<float>(a, large_tiles(a.K, a.S), s)
+           : type == SPMM_BF16 ? launch_attention_add<__bf16>(a, large_tiles(a.K, a.S), s)
+                               : launch_attention_add<_Float16>(a, large_tiles(a.K, a.S), s);
 }
 
 }  // namespace gspmm

@@ -126,7 +126,7 @@ struct KeyRows {
     int64_t ld;
     int left;           // rows that exist
 
-    __device__ inline int64_t at(int r) const { return r < left ? r * ld : -1; }
+    __device__ inline int64_t at(int r) const { return r * ld; }
 };
 
 // Consecutive packed rows of one key head, from packed row m0 of a segment;
@@ -140,35 +140,57 @@ struct PackedRows {
 
     __device__ inline int64_t at(int r) const {
         const int m = m0 + r, i = quotient(G, m);
-        return r < left ? (i - i0) * ld + (m - i * G.d) * D : -1;
+        return (i - i0) * ld + (m - i * G.d) * D;
     }
 };
 
 // Fills ROWS rows of a tile, zeros where a row or an element does not exist.
-// DIRECT: copied straight into LDS; else through registers, load() ahead of
-// the use of what put() overwrites.
+// DIRECT: copied straight into LDS from the offsets that aim() left; else through
+// registers, load() ahead of the use of what put() overwrites.
 template <typename T, int DP, int ROWS, int WAVES, bool DIRECT>
 struct Fill {
     using L = Tile<T, DP>;
     static constexpr int kCopies = ROWS * L::kPitch / 1024 / WAVES;
+    static constexpr uint32_t kNowhere = 0x80000000u;    // behind 2^31 - 1 bytes the copy writes zeros
     Pack<T> r[DIRECT ? 1 : kCopies];
+    uint32_t off[DIRECT ? kCopies : 1];
+
+    static __device__ inline int row_of(int i, int wave) {
+        return ((i * WAVES + wave) * 1024 + (threadIdx.x & (kWave - 1)) * 16) / L::kPitch;
+    }
+    static __device__ inline int element_of(int i, int wave) {
+        const int byte = (i * WAVES + wave) * 1024 + (threadIdx.x & (kWave - 1)) * 16;
+        return ((byte % L::kPitch / 16) ^ L::place(byte / L::kPitch)) * kPack<T>;
+    }
+
+    template <typename Rows>
+    __device__ inline void aim(const Rows &rows, int D, int wave) {
+        if constexpr (DIRECT) {
+#pragma unroll
+            for (int i = 0; i < kCopies; ++i) {
+                const int e = element_of(i, wave);
+                off[i] = e < D ? (uint32_t)(rows.at(row_of(i, wave)) + e) * (uint32_t)sizeof(T) : kNowhere;
+            }
+        }
+    }
 
     template <typename Rows>
     __device__ inline void load(LdsByte *lds, const Rows &rows, int D, int wave) {
-        const char *base = (const char *)uniform((int64_t)rows.base);
-        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)base, 0, 0x7fffffff, 0x00020000);
+        if constexpr (DIRECT) {
+            const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)uniform((int64_t)rows.base), 0, 0x7fffffff,
+                                                                0x00020000);
 #pragma unroll
-        for (int i = 0; i < kCopies; ++i) {
-            const int byte = (i * WAVES + wave) * 1024 + (threadIdx.x & (kWave - 1)) * 16;
-            const int row = byte / L::kPitch, e = ((byte % L::kPitch / 16) ^ L::place(row)) * kPack<T>;
-            const int64_t at = rows.at(row);
-            if constexpr (DIRECT) {
-                // behind 2^31 - 1 bytes the copy writes zeros
-                const uint32_t off = at >= 0 && e < D ? (uint32_t)(at + e) * (uint32_t)sizeof(T) : 0x80000000u;
+            for (int i = 0; i < kCopies; ++i) {
+                const uint32_t from = row_of(i, wave) < rows.left ? off[i] : kNowhere;
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                    rsrc, (__attribute__((address_space(3))) void *)(lds + (i * WAVES + wave) * 1024), 16, off, 0, 0, 0);
-            } else {
-                r[i] = load_pack(rows.base + (at >= 0 ? at + e : 0), at >= 0 ? D - e : 0);
+                    rsrc, (__attribute__((address_space(3))) void *)(lds + (i * WAVES + wave) * 1024), 16, from, 0, 0, 0);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kCopies; ++i) {
+                const int row = row_of(i, wave), e = element_of(i, wave);
+                const bool in = row < rows.left;
+                r[i] = load_pack(rows.base + (in ? rows.at(row) + e : 0), in ? D - e : 0);
             }
         }
     }
@@ -430,6 +452,8 @@ __global__ __launch_bounds__(WAVES * kWave, (kQuerySide<T, DP, DIRECT>)) void at
             load_row<T, DP>(mine, (const T *)a.q + q.row * a.ldq + q.head * D, D, q.exists());
             const T *k = (const T *)a.k + q.key0 * a.ldk + hk * D, *v = (const T *)a.v + q.key0 * a.ldv + hk * D;
             Fill<T, DP, BN, WAVES, DIRECT> fk, fv;
+            fk.aim(KeyRows<T>{k, a.ldk, BN}, D, wave);
+            fv.aim(KeyRows<T>{v, a.ldv, BN}, D, wave);
             __syncthreads();
             walk<DIRECT>(
                 t0, t1,
@@ -586,6 +610,8 @@ __global__ __launch_bounds__(WAVES * kWave, (kQuerySide<T, DP, DIRECT>)) void at
                 const int tiles = (seen_by_tile<BM>(a, s, q.keys) + BN - 1) / BN;
                 const T *k = (const T *)a.k + q.key0 * a.ldk + hk * D, *v = (const T *)a.v + q.key0 * a.ldv + hk * D;
                 Fill<T, DP, BN, WAVES, DIRECT> fk, fv;
+                fk.aim(KeyRows<T>{k, a.ldk, BN}, D, wave);
+                fv.aim(KeyRows<T>{v, a.ldv, BN}, D, wave);
                 __syncthreads();
                 walk<DIRECT>(
                     0, tiles,
@@ -636,142 +662,341 @@ __global__ __launch_bounds__(WAVES * kWave, (kQuerySide<T, DP, DIRECT>)) void at
     }
 }
 
+// Parts that the packed rows of a key tile are taken in: they differ in how many
+// see the tile, and a part is to be a third of a compute unit's share of the call.
+__device__ inline int parts_of_tile(const AttentionArgs &a, int tiles, int tile_rows) {
+    return max(1, min(a.key_parts, (int)(((int64_t)tiles * tile_rows + a.part_rows - 1) / a.part_rows)));
+}
+
+// What a key tile knows of the rows of its segment.
+struct SeenBy {
+    int64_t row0;
+    int packed, start, tiles;     // tiles of packed rows from `start` on see the tile
+    int64_t behind;
+
+    __device__ inline SeenBy(const AttentionArgs &a, const Slot &s, int key, int tile_rows) {
+        const Runs queries = {a.offsets, a.S, a.R, 1};
+        row0 = uniform(queries.bound(s.run));
+        const int rows = uniform((int)max(int64_t(0), queries.bound(s.run + 1) - row0));
+        packed = rows * a.G.d;
+        behind = a.causal ? (int64_t)rows - s.rows : INT32_MIN;
+        start = first(a, key) / tile_rows;
+        tiles = max(0, (packed + tile_rows - 1) / tile_rows - start);
+    }
+
+    // Packed rows from this one on see key j of the segment.
+    __device__ inline int first(const AttentionArgs &a, int j) const {
+        return (int)max(int64_t(0), min((int64_t)packed, (j + behind) * a.G.d));
+    }
+};
+
+// What dk and dv read of a tile of packed rows: q and dout in LDS, and the rows'
+// lse and delta.
+template <typename T, int DP, int BN, int WAVES, bool DIRECT>
+struct RowTiles {
+    const AttentionArgs &a;
+    int64_t row0;
+    int hk, packed, wave;
+    Fill<T, DP, BN, WAVES, DIRECT> fq, fd;
+    float lse, delta;
+
+    __device__ inline RowTiles(const AttentionArgs &args, int64_t first, int head, int rows, int w)
+        : a(args), row0(first), hk(head), packed(rows), wave(w), lse(0.0f), delta(0.0f) {
+        aim(0);
+    }
+
+    __device__ inline PackedRows<T> q(int m0) const {
+        const int i0 = quotient(a.G, m0);
+        return {(const T *)a.q + (row0 + i0) * a.ldq + hk * a.G.d * a.D, a.ldq, packed - m0, m0, i0, (int)a.D, a.G};
+    }
+    __device__ inline PackedRows<T> dout(int m0) const {
+        const int i0 = quotient(a.G, m0);
+        return {(const T *)a.dout + ((row0 + i0) * a.H + hk * a.G.d) * a.D, a.H * a.D, packed - m0, m0, i0, (int)a.D,
+                a.G};
+    }
+
+    __device__ inline void aim(int m0) {
+        fq.aim(q(m0), (int)a.D, wave);
+        fd.aim(dout(m0), (int)a.D, wave);
+    }
+
+    __device__ inline void load(int t, LdsByte *qt, LdsByte *dt, LdsByte *lse_of, LdsByte *delta_of) {
+        const int m0 = t * BN, left = packed - m0;
+        // tiles of whole groups stand alike, one ld apart
+        if (DIRECT && BN % a.G.d) aim(m0);
+        fq.load(qt, q(m0), (int)a.D, wave);
+        fd.load(dt, dout(m0), (int)a.D, wave);
+        // one lane to a row; rows that do not exist take zeros, and their
+        // operands are zeros
+        if (wave == 0) {
+            const int i0 = quotient(a.G, m0), m = m0 + (int)threadIdx.x, i = quotient(a.G, m);
+            const bool in = (int)threadIdx.x < min(BN, left);
+            const int64_t from = (row0 + i0) * a.H + hk * a.G.d;
+            const int at = (int)((i - i0) * a.H) + m - i * a.G.d;
+            if constexpr (DIRECT) {
+                copy_floats(lse_of, a.lse + from, at, in);
+                copy_floats(delta_of, a.delta + from, at, in);
+            } else {
+                lse = in ? a.lse[from + at] : 0.0f;
+                delta = in ? a.delta[from + at] : 0.0f;
+            }
+        }
+    }
+
+    __device__ inline void put(LdsByte *qt, LdsByte *dt, LdsByte *lse_of, LdsByte *delta_of) {
+        fq.put(qt, wave);
+        fd.put(dt, wave);
+        if (!DIRECT && wave == 0) {
+            ((__attribute__((address_space(3))) float *)lse_of)[threadIdx.x] = lse;
+            ((__attribute__((address_space(3))) float *)delta_of)[threadIdx.x] = delta;
+        }
+    }
+};
+
+// The sums of a wave's 32 keys over 32-row blocks of packed rows.
+template <typename T, int DP>
+struct KeySums {
+    using L = Tile<T, DP>;
+    struct TurnedRows {
+        Pack<T> at[L::kGroups][L::kBlocks];
+    };
+    struct Weights {
+        Pack<T> p[L::kGroups], ds[L::kGroups];
+    };
+    f32x16 dk[L::kBlocks] = {}, dv[L::kBlocks] = {};
+    RowPacks<T, DP> k, v;
+    RowReader<T, DP> rows;
+    TurnedReader<T, DP> turned;
+    float c;
+
+    __device__ inline void read(RowPacks<T, DP> &r, LdsByte *tile, int b) const {
+#pragma unroll
+        for (int ks = 0; ks < L::kSteps; ++ks) r[ks] = rows.read(tile, b, ks);
+    }
+    __device__ inline void read(TurnedRows &r, LdsByte *tile, int b) const {
+#pragma unroll
+        for (int g = 0; g < L::kGroups; ++g)
+#pragma unroll
+            for (int e = 0; e < L::kBlocks; ++e) r.at[g][e] = turned.read(tile, b, g, e);
+    }
+    static __device__ inline void product(const RowPacks<T, DP> &mine, const RowPacks<T, DP> &r, f32x16 &to) {
+        to = f32x16{};
+#pragma unroll
+        for (int ks = 0; ks < L::kSteps; ++ks) multiply<T>(mine[ks], r[ks], to);
+    }
+    // Rows ahead of `from` of a block that starts at m0 do not see the lane's key.
+    static __device__ inline void hide(f32x16 &sc, int m0, int from) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (m0 + register_row(i) < from) sc[i] = -INFINITY;
+    }
+    __device__ inline void probabilities(f32x16 &sc, LdsByte *lse_of, int b) const {
+        const f32x16 lse = register_floats(lse_of, b);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sc[i] = exp2_of(fmaf(sc[i], c, -lse[i]));
+    }
+    static __device__ inline void add(f32x16 (&to)[L::kBlocks], const Pack<T> (&w)[L::kGroups], const TurnedRows &r) {
+#pragma unroll
+        for (int g = 0; g < L::kGroups; ++g)
+#pragma unroll
+            for (int e = 0; e < L::kBlocks; ++e) multiply<T>(w[g], r.at[g][e], to[e]);
+    }
+
+    // A block whose rows of q have been read: each product runs beside the reads
+    // of the next one's operand and the arithmetic that does not wait for it.
+    // ahead() reads q of the block after it; border: see hide().
+    template <typename Ahead>
+    __device__ inline void block(RowPacks<T, DP> &q, LdsByte *qt, LdsByte *dt, LdsByte *lse_of, LdsByte *delta_of, int b,
+                                 bool border, int m0, int from, Ahead ahead) {
+        RowPacks<T, DP> d;
+        TurnedRows dturned, qturned;
+        f32x16 sc, dp;
+        Weights w;
+        read(d, dt, b);
+        product(k, q, sc);
+        if (border) hide(sc, m0, from);
+        __builtin_amdgcn_sched_barrier(0);
+        read(dturned, dt, b);
+        product(v, d, dp);
+        probabilities(sc, lse_of, b);
+#pragma unroll
+        for (int g = 0; g < L::kGroups; ++g) w.p[g] = group_of<T>(sc, g);
+        spread();
+        __builtin_amdgcn_sched_barrier(0);
+        read(qturned, qt, b);
+        add(dv, w.p, dturned);
+        const f32x16 delta = register_floats(delta_of, b);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) dp[i] = sc[i] * (dp[i] - delta[i]);
+#pragma unroll
+        for (int g = 0; g < L::kGroups; ++g) w.ds[g] = group_of<T>(dp, g);
+        spread();
+        __builtin_amdgcn_sched_barrier(0);
+        ahead();
+        add(dk, w.ds, qturned);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+
+    // Reads first, then the products with the rest spread between them.
+    static __device__ inline void spread() {
+        constexpr int kProducts = L::kSteps;
+        __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+#pragma unroll
+        for (int i = 0; i < kProducts; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+            __builtin_amdgcn_sched_group_barrier(0x002, 8, 0);
+        }
+    }
+};
+
 // dk and dv: the block's keys against the packed rows that see them.
+//
+// Where one wave to a SIMD holds its keys and their sums (16-bit rows of more than
+// 64 elements), it reads ahead: a block's turned rows while its exponentials run,
+// and the next block's rows while the products with the turned ones run.
 template <typename T, int DP, int WAVES, bool DIRECT>
 __global__ __launch_bounds__(WAVES * kWave, (kKeySide<T, DP, DIRECT>)) void attention_dkdv_kernel(AttentionArgs a, unsigned total) {
     using L = Tile<T, DP>;
+    using K = KeySums<T, DP>;
     constexpr int BM = 32 * WAVES, BN = kTileRows<T, WAVES>, NB = BN / 32;
+    constexpr bool kAhead = DIRECT && sizeof(T) == 2 && WAVES == 4 && DP > 64;
     TILE_PAIRS(qtile, dtile, BN * L::kPitch);
     TILE_PAIRS(lse_of, delta_of, kWave * 4);
     const int wave = uniform((int)threadIdx.x / kWave);
     const int D = (int)a.D;
-    const RowReader<T, DP> rows;
-    const TurnedReader<T, DP> turned;
-    const Runs runs = {a.key_offsets, a.S, a.K, 1}, queries = {a.offsets, a.S, a.R, 1};
-    const float c = a.scale * kLog2e;
+    const Runs runs = {a.key_offsets, a.S, a.K, 1};
     for (unsigned id = blockIdx.x; id < total; id += gridDim.x) {
-        const unsigned heads = (unsigned)a.Hk, rest = id / heads, parts = (unsigned)a.key_parts;
-        const int hk = (int)(id - rest * heads), part = (int)(rest % parts);
-        const Slot s = find<BM>(runs, (int)(rest / parts));
+        const unsigned heads = (unsigned)a.Hk, rest = id / heads, most = (unsigned)a.key_parts;
+        // tiles use few of their parts: they start at another one in each, so that
+        // the XCDs, which take blocks in turn, get alike
+        const int hk = (int)(id - rest * heads), slot = (int)(rest / most), part = (int)((rest + slot) % most);
+        const Slot s = find<BM>(runs, slot);
         if (s.tile >= s.tiles) continue;
+        int parts = 1;
         const int j0 = s.tile * BM + wave * 32, j = j0 + (threadIdx.x & 31);
         const bool exists = j < s.rows;
-        f32x16 dk[L::kBlocks] = {}, dv[L::kBlocks] = {};
+        K sums;
+        sums.c = a.scale * kLog2e;
         if (s.run > 0 && s.run <= a.S) {
-            const int64_t row0 = uniform(queries.bound(s.run));
-            const int nrows = uniform((int)max(int64_t(0), queries.bound(s.run + 1) - row0)), packed = nrows * a.G.d;
-            // packed rows from first_seeing(j) on see key j
-            const int64_t behind = a.causal ? (int64_t)nrows - s.rows : INT32_MIN;
-            auto first_seeing = [&](int key) {
-                return (int)max(int64_t(0), min((int64_t)packed, (key + behind) * a.G.d));
-            };
-            const int from = first_seeing(s.tile * BM), mine_from = first_seeing(j), wave_from = first_seeing(j0),
-                      wave_full = first_seeing(j0 + 31);
-            const int start = from / BN, tiles = max(0, (packed + BN - 1) / BN - start);
-            const int per = (tiles + a.key_parts - 1) / a.key_parts;
-            const int t0 = start + min(tiles, part * per), t1 = min(start + tiles, t0 + per);
-            RowPacks<T, DP> kmine, vmine;
+            const SeenBy by(a, s, s.tile * BM, BN);
+            const int mine_from = by.first(a, j), wave_from = by.first(a, j0), wave_full = by.first(a, j0 + 31);
+            parts = parts_of_tile(a, by.tiles, BN);
+            if (part >= parts) continue;
+            const int per = (by.tiles + parts - 1) / parts;
+            const int t0 = by.start + min(by.tiles, part * per), t1 = min(by.start + by.tiles, t0 + per);
             const int64_t key = s.row0 + min(j, s.rows - 1);
-            load_row<T, DP>(kmine, (const T *)a.k + key * a.ldk + hk * D, D, exists);
-            load_row<T, DP>(vmine, (const T *)a.v + key * a.ldv + hk * D, D, exists);
-            Fill<T, DP, BN, WAVES, DIRECT> fq, fd;
-            float lse = 0.0f, delta = 0.0f;
+            load_row<T, DP>(sums.k, (const T *)a.k + key * a.ldk + hk * D, D, exists);
+            load_row<T, DP>(sums.v, (const T *)a.v + key * a.ldv + hk * D, D, exists);
+            RowTiles<T, DP, BN, WAVES, DIRECT> tiles(a, by.row0, hk, by.packed, wave);
             __syncthreads();
-            walk<DIRECT>(
-                t0, t1,
-                [&](int t, int u) {
-                    const int m0 = t * BN, i0 = quotient(a.G, m0), left = packed - m0;
-                    const int64_t row = row0 + i0;
-                    fq.load(qtile[u],
-                            PackedRows<T>{(const T *)a.q + row * a.ldq + hk * a.G.d * D, a.ldq, left, m0, i0, D, a.G}, D,
-                            wave);
-                    fd.load(dtile[u],
-                            PackedRows<T>{(const T *)a.dout + (row * a.H + hk * a.G.d) * D, a.H * a.D, left, m0, i0, D,
-                                          a.G},
-                            D, wave);
-                    // the rows' statistics, one lane each; rows that do not exist
-                    // take zeros, and their operands are zeros
-                    if (wave == 0) {
-                        const int m = m0 + (int)threadIdx.x, i = quotient(a.G, m);
-                        const bool in = (int)threadIdx.x < min(BN, left);
-                        const int64_t from = row * a.H + hk * a.G.d;
-                        const int at = (int)((i - i0) * a.H) + m - i * a.G.d;
-                        if constexpr (DIRECT) {
-                            copy_floats(lse_of[u], a.lse + from, at, in);
-                            copy_floats(delta_of[u], a.delta + from, at, in);
-                        } else {
-                            lse = in ? a.lse[from + at] : 0.0f;
-                            delta = in ? a.delta[from + at] : 0.0f;
+            if constexpr (kAhead) {
+                auto load = [&](int t, int u) { tiles.load(t, qtile[u], dtile[u], lse_of[u], delta_of[u]); };
+                RowPacks<T, DP> q;
+                if (t0 < t1) {
+                    load(t0, 0);
+                    wait_copies<0>();
+                    load(t0 + 1, 1);
+                    sums.read(q, qtile[0], 0);
+                    for (int t = t0; t < t1; t += 2) {
+#pragma unroll
+                        for (int i = 0; i < 2 * NB; ++i) {
+                            const int u = i / NB, b = i % NB, m0 = (t + u) * BN + b * 32;
+                            if (b == 0 && t + u >= t1) break;
+                            auto ahead = [&] {
+                                if (b == NB - 1) {
+                                    // this tile is read out, and the next one here
+                                    wait_copies<0>();
+                                    load(t + u + 2, u);
+                                    sums.read(q, qtile[1 - u], 0);
+                                } else {
+                                    sums.read(q, qtile[u], b + 1);
+                                }
+                            };
+                            sums.block(q, qtile[u], dtile[u], lse_of[u], delta_of[u], b, m0 < wave_full, m0, mine_from,
+                                       ahead);
                         }
                     }
-                },
-                [&](int u) {
-                    fq.put(qtile[u], wave);
-                    fd.put(dtile[u], wave);
-                    if (wave == 0) {
-                        ((__attribute__((address_space(3))) float *)lse_of[u])[threadIdx.x] = lse;
-                        ((__attribute__((address_space(3))) float *)delta_of[u])[threadIdx.x] = delta;
-                    }
-                },
-                [&](int t, int u) {
-                    const int m0 = t * BN;
-                    if (m0 + BN <= wave_from) return;
+                    wait_copies<0>();
+                }
+            } else {
+                walk<DIRECT>(
+                    t0, t1, [&](int t, int u) { tiles.load(t, qtile[u], dtile[u], lse_of[u], delta_of[u]); },
+                    [&](int u) { tiles.put(qtile[u], dtile[u], lse_of[u], delta_of[u]); },
+                    [&](int t, int u) {
+                        if (t * BN + BN <= wave_from) return;
 #pragma unroll
-                    for (int b = 0; b < NB; ++b) {
-                        f32x16 sc = {}, dp = {};
+                        for (int b = 0; b < NB; ++b) {
+                            const int m0 = t * BN + b * 32;
+                            f32x16 sc = {}, dp = {};
 #pragma unroll
-                        for (int ks = 0; ks < L::kSteps; ++ks) {
-                            multiply<T>(kmine[ks], rows.read(qtile[u], b, ks), sc);
-                            multiply<T>(vmine[ks], rows.read(dtile[u], b, ks), dp);
-                        }
-                        const f32x16 ls = register_floats(lse_of[u], b), de = register_floats(delta_of[u], b);
+                            for (int ks = 0; ks < L::kSteps; ++ks) {
+                                multiply<T>(sums.k[ks], sums.rows.read(qtile[u], b, ks), sc);
+                                multiply<T>(sums.v[ks], sums.rows.read(dtile[u], b, ks), dp);
+                            }
+                            if (m0 < wave_full) K::hide(sc, m0, mine_from);
+                            sums.probabilities(sc, lse_of[u], b);
+                            const f32x16 delta = register_floats(delta_of[u], b);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) sc[i] = exp2_of(fmaf(sc[i], c, -ls[i]));
-                        if (m0 + b * 32 < wave_full) {
+                            for (int i = 0; i < 16; ++i) dp[i] = sc[i] * (dp[i] - delta[i]);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                if (m0 + b * 32 + register_row(i) < mine_from) sc[i] = 0.0f;
-                        }
+                            for (int g = 0; g < L::kGroups; ++g) {
+                                const Pack<T> p = group_of<T>(sc, g), ds = group_of<T>(dp, g);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) dp[i] = sc[i] * (dp[i] - de[i]);
-#pragma unroll
-                        for (int g = 0; g < L::kGroups; ++g) {
-                            const Pack<T> p = group_of<T>(sc, g), ds = group_of<T>(dp, g);
-#pragma unroll
-                            for (int d = 0; d < L::kBlocks; ++d) {
-                                multiply<T>(p, turned.read(dtile[u], b, g, d), dv[d]);
-                                multiply<T>(ds, turned.read(qtile[u], b, g, d), dk[d]);
+                                for (int e = 0; e < L::kBlocks; ++e) {
+                                    multiply<T>(p, sums.turned.read(dtile[u], b, g, e), sums.dv[e]);
+                                    multiply<T>(ds, sums.turned.read(qtile[u], b, g, e), sums.dk[e]);
+                                }
                             }
                         }
-                    }
-                });
+                    });
+            }
         }
         const int64_t at = ((s.row0 + j) * a.Hk + hk) * D, shift = part * a.K * a.Hk * a.D;
-        if (exists && a.key_parts > 1) {
-            if (a.dk) store_row(a.partial_dk + shift + at, dk, a.scale, D);
-            if (a.dv) store_row(a.partial_dv + shift + at, dv, 1.0f, D);
-        } else if (exists) {
-            if (a.dk) store_row((T *)a.dk + at, dk, a.scale, D);
-            if (a.dv) store_row((T *)a.dv + at, dv, 1.0f, D);
+        if (exists && parts > 1) {
+            if (a.dk) store_row(a.partial_dk + shift + at, sums.dk, a.scale, D);
+            if (a.dv) store_row(a.partial_dv + shift + at, sums.dv, 1.0f, D);
+        } else if (exists && part == 0) {
+            if (a.dk) store_row((T *)a.dk + at, sums.dk, a.scale, D);
+            if (a.dv) store_row((T *)a.dv + at, sums.dv, 1.0f, D);
         }
     }
 }
 
-// Adds the parts of dk or dv in their order.
-constexpr int kAddThreads = 256;
+// Adds the parts of dk and dv in their order, a block to 16 keys of a tile and head.
+constexpr int kAddThreads = 256, kAddKeys = 16;
 
-template <typename T>
-__global__ __launch_bounds__(kAddThreads) void attention_add_kernel(const float *from, T *to, int64_t n, int parts) {
-    for (int64_t i = ((int64_t)blockIdx.x * kAddThreads + threadIdx.x) * 4; i < n;
-         i += (int64_t)gridDim.x * kAddThreads * 4) {
-        float s[4] = {};
-        for (int p = 0; p < parts; ++p)
+template <typename T, int LEN, int ROWS>
+__global__ __launch_bounds__(kAddThreads) void attention_add_kernel(AttentionArgs a, unsigned total) {
+    const Runs runs = {a.key_offsets, a.S, a.K, 1};
+    const int D = (int)a.D, quads = (D + 3) / 4;
+    const int64_t all = a.K * a.Hk * D;
+    for (unsigned id = blockIdx.x; id < total; id += gridDim.x) {
+        const unsigned heads = (unsigned)a.Hk, rest = id / heads, slot = rest / (LEN / kAddKeys);
+        const int hk = (int)(id - rest * heads), first = (int)(rest - slot * (LEN / kAddKeys)) * kAddKeys;
+        const Slot s = find<LEN>(runs, (int)slot);
+        if (s.tile >= s.tiles || s.run == 0 || s.run > a.S) continue;
+        const SeenBy by(a, s, s.tile * LEN, ROWS);
+        const int parts = parts_of_tile(a, by.tiles, ROWS);
+        if (parts == 1) continue;
+        const int key = s.tile * LEN + first, keys = min(kAddKeys, s.rows - key);
+        for (int i = threadIdx.x; i < 2 * keys * quads; i += kAddThreads) {
+            const bool second = i >= keys * quads;
+            T *to = (T *)(second ? a.dv : a.dk);
+            if (!to) continue;
+            const int in = second ? i - keys * quads : i, row = in / quads, d = (in - row * quads) * 4;
+            const int64_t at = ((s.row0 + key + row) * a.Hk + hk) * D + d;
+            const float *from = (second ? a.partial_dv : a.partial_dk) + at;
+            float sum[4] = {};
+            for (int p = 0; p < parts; ++p, from += all) {
+                const Pack<float> v = load_pack(from, D - d);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sum[e] += v.v[e];
+            }
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (i + e < n) s[e] += from[p * n + i + e];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (i + e < n) to[i + e] = (T)s[e];
+                if (d + e < D) to[at + e] = (T)sum[e];
+        }
     }
 }
 
@@ -836,18 +1061,22 @@ hipError_t launch_attention_join(const AttentionArgs &a, hipStream_t s) {
     return hipGetLastError();
 }
 
-template <typename T>
-hipError_t launch_attention_add(const AttentionArgs &a, hipStream_t s) {
-    const int64_t n = a.K * a.Hk * a.D, per = kAddThreads * 4;
-    const unsigned blocks = (unsigned)std::min((n + per - 1) / per, kMaxBlocks);
-    if (a.dk) attention_add_kernel<T><<<blocks, kAddThreads, 0, s>>>(a.partial_dk, (T *)a.dk, n, a.key_parts);
-    if (a.dv) attention_add_kernel<T><<<blocks, kAddThreads, 0, s>>>(a.partial_dv, (T *)a.dv, n, a.key_parts);
+template <typename T, int WAVES>
+hipError_t add_launch(const AttentionArgs &a, hipStream_t s) {
+    const unsigned total = slots(a.K, a.S, 32 * WAVES) * (unsigned)a.Hk * (32 * WAVES / kAddKeys);
+    const unsigned blocks = (unsigned)std::min<int64_t>(total, kMaxBlocks);
+    attention_add_kernel<T, 32 * WAVES, kTileRows<T, WAVES>><<<blocks, kAddThreads, 0, s>>>(a, total);
     return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_attention_add(const AttentionArgs &a, bool large, hipStream_t s) {
+    return large ? add_launch<T, 4>(a, s) : add_launch<T, 1>(a, s);
 }
 
 #define ATTENTION_OF(T)                                                                                          \
     template hipError_t launch_attention_pass<T>(const AttentionArgs &, AttentionPass, bool, bool, hipStream_t); \
     template hipError_t launch_attention_join<T>(const AttentionArgs &, hipStream_t);                            \
-    template hipError_t launch_attention_add<T>(const AttentionArgs &, hipStream_t)
+    template hipError_t launch_attention_add<T>(const AttentionArgs &, bool, hipStream_t)
 
 }  // namespace gspmm

@@ -484,6 +484,12 @@ int64_t dw_chunk(int64_t R, int64_t N, int64_t I) {
     return whole(std::max<int64_t>(256, (R + want - 1) / want), 32);
 }
 
+// dx sums over a piece's classes, so that a tile's start and end weigh little: one
+// 256 x 256 tile to a compute unit is enough.
+bool large_dx(int64_t R, int64_t I, int64_t N, int size, bool direct) {
+    return direct && size == 2 && I > 128 && N >= 4096 && tiles_of(R, 256) * tiles_of(I, 256) >= kUnits * 3 / 4;
+}
+
 template <typename T, typename S, bool DIRECT, bool BACKWARD>
 hipError_t logits_launch(const LossArgs &a, int64_t v0, int64_t N, hipStream_t s) {
     const int64_t total = tiles_of(a.R, S::BM) * tiles_of(N, S::BN);
@@ -558,7 +564,7 @@ hipError_t backward(const LossArgs &args, hipStream_t s) {
         if (a.dx && a.R > 0) {
             const int add = pieces == 1 ? -1 : v0 ? 1 : 0;
             hipError_t e = hipSuccess;
-            if (size == 2 && tiles_for(a.R, a.I, size, direct) == Tiles::kLarge) {
+            if (large_dx(a.R, a.I, N, size, direct)) {
                 if constexpr (sizeof(T) == 2) e = dx_launch<T, Large, true>(a, v0, N, add, s);
             } else {
                 e = direct ? dx_launch<T, Medium, true>(a, v0, N, add, s) : dx_launch<T, Medium, false>(a, v0, N, add, s);

@@ -206,7 +206,8 @@ struct AttentionArgs {
     void *dq;                // [R, H, D] or nullptr
     void *dk;                // [K, Hk, D] or nullptr
     void *dv;                // [K, Hk, D] or nullptr
-    int key_parts;           // of the rows; above 1:
+    int64_t part_rows;       // packed rows of a part of the rows that see a key tile
+    int key_parts;           // the most of them; above 1:
     float *partial_dk;       // [key_parts, K, Hk, D]
     float *partial_dv;       // [key_parts, K, Hk, D]
 };
