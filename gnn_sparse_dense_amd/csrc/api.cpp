@@ -2232,7 +2232,7 @@ SPMM_API int spmm_linear_cross_entropy_workspace(int64_t R, int64_t I, int64_t V
     if (!state_bytes || !bytes || !backward_bytes) return fail(SPMM_E_INVALID_ARG, "output is NULL");
     if (const int st = check_loss(R, I, V, type)) return st;
     *state_bytes = loss_state_bytes(R);
-    *bytes = loss_workspace_floats(R, V) * (int64_t)sizeof(float);
+    *bytes = loss_workspace_bytes(R, I, V, type);
     *backward_bytes = loss_backward_workspace_bytes(R, I, V, type);
     return succeed();
 }
@@ -2242,7 +2242,7 @@ SPMM_API int spmm_linear_cross_entropy(const void *x, const void *w, const int64
                                        int64_t state_bytes, void *workspace, int64_t workspace_bytes, void *stream) {
     if (const int st = check_loss(R, I, V, type)) return st;
     if (const int st = check_reduction(reduction)) return st;
-    const int64_t kept = loss_state_bytes(R), need = loss_workspace_floats(R, V) * (int64_t)sizeof(float);
+    const int64_t kept = loss_state_bytes(R), need = loss_workspace_bytes(R, I, V, type);
     if (state_bytes < kept)
         return fail(SPMM_E_INVALID_ARG, "state of %lld bytes, %lld are needed", (long long)state_bytes,
                     (long long)kept);
@@ -2268,7 +2268,7 @@ SPMM_API int spmm_linear_cross_entropy(const void *x, const void *w, const int64
     a.per_row = reduction == SPMM_LOSS_ROWS;
     a.mean = reduction == SPMM_LOSS_MEAN;
     (a.per_row ? a.row_loss : a.loss) = loss;
-    return launched(launch_loss(a, state, static_cast<float *>(workspace), type, reinterpret_cast<hipStream_t>(stream)),
+    return launched(launch_loss(a, state, workspace, type, reinterpret_cast<hipStream_t>(stream)),
                     "linear cross entropy launch");
 }
 

@@ -34,6 +34,7 @@ namespace {
 constexpr float kLog2e = 1.44269504088896340736f;
 
 using Narrow = Shape<128, 64, 4, 1>;
+using Flat = Shape<64, 128, 1, 4>;
 
 // ---- the rows with a class ----
 
@@ -120,6 +121,9 @@ __device__ inline int register_col(int e) { return 8 * (e >> 2) + 4 * ((threadId
 
 __device__ inline float other_half(float v) { return __shfl_xor(v, 32, kWave); }
 
+// A class's column among the n from n0 on of a tile, -1 if it is another's.
+__device__ inline int in_tile(int64_t t, int n0, int n) { return t >= n0 && t < n0 + n ? (int)t - n0 : -1; }
+
 // What d's rows are multiplied with, and the sums with its inverse.
 template <typename T>
 constexpr float kHeld = __is_same(T, _Float16) ? 4096.0f : 1.0f;
@@ -143,36 +147,50 @@ __global__ __launch_bounds__(S::kThreads, 2) void loss_logits_kernel(LossArgs a,
         const int64_t row = uniform(at.row * S::BM), col = uniform(at.col * S::BN);
         Operand<T> A, B;
         A.ptr = (const T *)a.x;
-        A.ld = a.I;
+        A.ld = a.ld;
         A.outer = count - row;
-        A.inner = a.I;
-        A.end = A.ptr + a.R * a.I;
+        A.inner = a.ld;
+        A.end = A.ptr + a.R * a.ld;
         A.rows = a.rows + row;
-        B.ptr = (const T *)a.w + (v0 + col) * a.I;
-        B.ld = a.I;
+        B.ptr = (const T *)a.w + (v0 + col) * a.ld;
+        B.ld = a.ld;
         B.outer = N - col;
-        B.inner = a.I;
-        B.end = (const T *)a.w + a.V * a.I;
+        B.inner = a.ld;
+        B.end = (const T *)a.w + a.V * a.ld;
         __syncthreads();
         Sums<S> sums = {};
         f32x16 (&acc)[S::MI][S::NI] = sums.at;
-        tile_sums<T, S, true, true, DIRECT, true>(lds, A, B, a.I, sums);
+        tile_sums<T, S, true, true, DIRECT, true>(lds, A, B, a.ld, sums);
         const int left = (int)min(int64_t(S::BN), N - col);
+        // columns behind the last class: in the last tile alone
+        if (left < S::BN) {
+#pragma unroll
+            for (auto &line : acc)
+#pragma unroll
+                for (int j = 0; j < S::NI; ++j)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        if (n0 + j * 32 + register_col(e) >= left) line[j][e] = -INFINITY;
+        }
         if constexpr (BACKWARD) {
 #pragma unroll
             for (int i = 0; i < S::MI; ++i) {
                 const int64_t r = min(row + m0 + i * 32 + (lane & 31), count - 1);
                 const float top = a.stats[r], inverse = a.stats[a.R + r];
-                const int64_t t = a.target[a.rows[r]] - v0 - col;
+                const int t = in_tile(a.target[a.rows[r]] - v0 - col, n0, S::NI * 32);
                 const float g = a.per_row ? a.dloss[a.rows[r]] / *a.unit * kHeld<T> : kHeld<T>;
+                const float pg = inverse * g, from = top == -INFINITY ? 0.0f : top;
 #pragma unroll
-                for (int j = 0; j < S::NI; ++j)
+                for (auto &block : acc[i])
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const int c = n0 + j * 32 + register_col(e);
-                        const float p = __builtin_amdgcn_exp2f((acc[i][j][e] - top) * kLog2e) * inverse;
-                        acc[i][j][e] = c < left ? (p - (c == t ? 1.0f : 0.0f)) * g : 0.0f;
-                    }
+                    for (int e = 0; e < 16; ++e) block[e] = __builtin_amdgcn_exp2f((block[e] - from) * kLog2e) * pg;
+                if (__any(t >= 0)) {
+#pragma unroll
+                    for (int j = 0; j < S::NI; ++j)
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            if (j * 32 + register_col(e) == t) acc[i][j][e] -= g;
+                }
             }
             tile_store<T, S>(lds, sums, (T *)a.d + row * a.ldd + col, a.ldd, count - row, a.ldd - col, false);
         } else {
@@ -180,17 +198,26 @@ __global__ __launch_bounds__(S::kThreads, 2) void loss_logits_kernel(LossArgs a,
 #pragma unroll
             for (int i = 0; i < S::MI; ++i) {
                 const int in = m0 + i * 32 + (lane & 31);
-                const int64_t r = min(row + in, count - 1), t = a.target[a.rows[r]] - v0 - col;
+                const int64_t r = min(row + in, count - 1);
+                const int t = in_tile(a.target[a.rows[r]] - v0 - col, n0, S::NI * 32);
+                if (__any(t >= 0)) {
+                    float picked = 0.0f;
+                    bool mine = false;
+#pragma unroll
+                    for (int j = 0; j < S::NI; ++j)
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            if (j * 32 + register_col(e) == t) {
+                                picked = acc[i][j][e];
+                                mine = true;
+                            }
+                    if (mine && row + in < count) a.picked[r] = picked;
+                }
                 float top = -INFINITY, sum = 0.0f;
 #pragma unroll
                 for (int j = 0; j < S::NI; ++j)
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const int c = n0 + j * 32 + register_col(e);
-                        if (c == t && row + in < count) a.picked[r] = acc[i][j][e];
-                        if (c >= left) acc[i][j][e] = -INFINITY;
-                        top = fmaxf(top, acc[i][j][e]);
-                    }
+                    for (int e = 0; e < 16; ++e) top = fmaxf(top, acc[i][j][e]);
                 top = fmaxf(top, other_half(top));
                 const float from = top == -INFINITY ? 0.0f : top;
 #pragma unroll
@@ -223,22 +250,28 @@ __global__ __launch_bounds__(S::kThreads, 2) void loss_logits_kernel(LossArgs a,
 
 // ---- the rows' losses ----
 
-constexpr int kJoinRows = 32, kJoinGroups = 8, kJoinThreads = kJoinRows * kJoinGroups;
+constexpr int kJoinThreads = 256, kJoinRows = 32;
 
-// Joins the column tiles of 32 rows, eight tiles at a time.
+// Rows of a block: 32, or 8 where a row has many tiles (128 for 64 rows: 11 -> 5 us).
+int join_rows(int tiles) { return tiles > 32 ? 8 : kJoinRows; }
+
+// Joins the column tiles of ROWS rows, 256 / ROWS tiles at a time.
+template <int ROWS>
 __global__ __launch_bounds__(kJoinThreads) void loss_join_kernel(LossArgs a, int tiles) {
-    __shared__ float tops[kJoinGroups][kJoinRows], sums[kJoinGroups][kJoinRows];
+    constexpr int kGroups = kJoinThreads / ROWS;
+    __shared__ float tops[kGroups][ROWS], sums[kGroups][ROWS];
     const int64_t count = *a.count;
-    const int in = threadIdx.x % kJoinRows, group = threadIdx.x / kJoinRows;
-    for (int64_t block = blockIdx.x; block * kJoinRows < a.R; block += gridDim.x) {
-        const int64_t r = block * kJoinRows + in;
+    const int in = threadIdx.x % ROWS, group = threadIdx.x / ROWS;
+    for (int64_t block = blockIdx.x; block * ROWS < a.R; block += gridDim.x) {
+        const int64_t r = block * ROWS + in;
         float top = -INFINITY, sum = 0.0f;
         if (r < count) {
-            for (int t = group; t < tiles; t += kJoinGroups) {
-                const float next = fmaxf(top, a.tile_top[t * a.R + r]);
-                const float from = next == -INFINITY ? 0.0f : next;
+#pragma unroll 4
+            for (int t = group; t < tiles; t += kGroups) {
+                const float tile_top = a.tile_top[t * a.R + r], tile_sum = a.tile_sum[t * a.R + r];
+                const float next = fmaxf(top, tile_top), from = next == -INFINITY ? 0.0f : next;
                 sum = sum * __builtin_amdgcn_exp2f((top - from) * kLog2e) +
-                      a.tile_sum[t * a.R + r] * __builtin_amdgcn_exp2f((a.tile_top[t * a.R + r] - from) * kLog2e);
+                      tile_sum * __builtin_amdgcn_exp2f((tile_top - from) * kLog2e);
                 top = next;
             }
         }
@@ -248,14 +281,14 @@ __global__ __launch_bounds__(kJoinThreads) void loss_join_kernel(LossArgs a, int
         __syncthreads();
         if (threadIdx.x < kWave) {
             float loss = 0.0f;
-            if (threadIdx.x < kJoinRows && r < count) {
+            if (threadIdx.x < ROWS && r < count) {
                 top = -INFINITY;
                 sum = 0.0f;
 #pragma unroll
-                for (int g = 0; g < kJoinGroups; ++g) top = fmaxf(top, tops[g][in]);
+                for (int g = 0; g < kGroups; ++g) top = fmaxf(top, tops[g][in]);
                 const float from = top == -INFINITY ? 0.0f : top;
 #pragma unroll
-                for (int g = 0; g < kJoinGroups; ++g)
+                for (int g = 0; g < kGroups; ++g)
                     sum += sums[g][in] * __builtin_amdgcn_exp2f((tops[g][in] - from) * kLog2e);
                 loss = (top - a.picked[r]) + logf(sum);
                 a.stats[r] = top;
@@ -264,7 +297,7 @@ __global__ __launch_bounds__(kJoinThreads) void loss_join_kernel(LossArgs a, int
             }
             if (a.block_loss) {
 #pragma unroll
-                for (int o = kJoinRows / 2; o > 0; o >>= 1) loss += __shfl_xor(loss, o, kWave);
+                for (int o = ROWS / 2; o > 0; o >>= 1) loss += __shfl_xor(loss, o, kWave);
                 if (threadIdx.x == 0) a.block_loss[block] = loss;
             }
         }
@@ -313,12 +346,26 @@ constexpr int kPackThreads = 256;
 
 template <typename T>
 __global__ __launch_bounds__(kPackThreads) void loss_pack_kernel(LossArgs a) {
-    const int64_t count = *a.count, packs = (a.I + kPack<T> - 1) / kPack<T>;
+    const int64_t count = *a.count, packs = (a.ld + kPack<T> - 1) / kPack<T>;
     if (count == a.R) return;
     for (int64_t i = (int64_t)blockIdx.x * kPackThreads + threadIdx.x; i < count * packs;
          i += (int64_t)gridDim.x * kPackThreads) {
         const int64_t r = i / packs, c = i % packs * kPack<T>;
-        store_pack((T *)a.packed + r * a.I + c, load_pack((const T *)a.x + a.rows[r] * a.I + c, a.I - c), a.I - c);
+        store_pack((T *)a.packed + r * a.ld + c, load_pack((const T *)a.x + a.rows[r] * a.ld + c, a.ld - c), a.ld - c);
+    }
+}
+
+// Rows of I elements moved ld apart, zeros behind each; `listed`: those that have
+// a class alone.
+template <typename T>
+__global__ __launch_bounds__(kPackThreads) void loss_pad_kernel(LossArgs a, const T *from, T *to, int64_t rows, int64_t I,
+                                                                int64_t ld, bool listed) {
+    const int64_t packs = ld / kPack<T>;
+    for (int64_t i = (int64_t)blockIdx.x * kPackThreads + threadIdx.x; i < rows * packs;
+         i += (int64_t)gridDim.x * kPackThreads) {
+        const int64_t r = i / packs, c = i % packs * kPack<T>;
+        if (listed && !has_class(a, r)) continue;
+        store_pack(to + r * ld + c, load_pack(from + r * I + c, I - c), kPack<T>);
     }
 }
 
@@ -334,9 +381,15 @@ __global__ __launch_bounds__(kPackThreads) void loss_rest_kernel(LossArgs a, boo
         int64_t to = r;
         if (r >= zeros) {
             to = a.rows[r - zeros];
-            const float *from = a.dx_sum + (r - zeros) * a.I + c;
+            float sum[kPack<T>] = {};
+            for (int64_t p = 0; p < a.dx_parts; ++p) {
+                const float *from = a.dx_sum + (p * a.R + r - zeros) * a.I + c;
 #pragma unroll
-            for (int e = 0; e < kPack<T>; ++e) v.v[e] = (T)(c + e < a.I ? from[e] * f : 0.0f);
+                for (int e = 0; e < kPack<T>; ++e)
+                    if (c + e < a.I) sum[e] += from[e];
+            }
+#pragma unroll
+            for (int e = 0; e < kPack<T>; ++e) v.v[e] = (T)(sum[e] * f);
         } else {
             if (has_class(a, r)) continue;
 #pragma unroll
@@ -346,28 +399,31 @@ __global__ __launch_bounds__(kPackThreads) void loss_rest_kernel(LossArgs a, boo
     }
 }
 
-// A tile of dx = d w over a piece's classes: ADD is -1 where it is the whole of
-// dx, 0 and 1 for the first and the other pieces of the fp32 sums.
+// A tile of dx = d w over a part of a piece's classes: ADD is -1 where it is the
+// whole of dx, 0 and 1 for the first and the other pieces of the fp32 sums.
 template <typename T, typename S, bool DIRECT, int ADD>
-__global__ __launch_bounds__(S::kThreads, 2) void loss_dx_kernel(LossArgs a, int64_t v0, int64_t N, int64_t total) {
+__global__ __launch_bounds__(S::kThreads, 2) void loss_dx_kernel(LossArgs a, int64_t first, int64_t classes,
+                                                                 int64_t total) {
     TILE_STAGES(lds, S::kStageBytes);
     const int64_t count = *a.count, row_tiles = (count + S::BM - 1) / S::BM, col_tiles = (a.I + S::BN - 1) / S::BN;
-    // behind the last class d holds zeros up to whole packs
-    const int64_t K = (N + kPack<T> - 1) / kPack<T> * kPack<T>;
-    for (int64_t id = blockIdx.x; id < min(total, row_tiles * col_tiles); id += gridDim.x) {
-        const TileAt at = tile_at(id, row_tiles, col_tiles);
+    for (int64_t id = blockIdx.x; id < min(total, row_tiles * col_tiles * a.dx_parts); id += gridDim.x) {
+        const int64_t part = ADD < 0 ? 0 : id / (row_tiles * col_tiles), skip = part * a.dx_part;
+        const int64_t v0 = first + skip, N = ADD < 0 ? classes : max(int64_t(0), min(a.dx_part, classes - skip));
+        // behind the last class d holds zeros up to whole packs
+        const int64_t K = (N + kPack<T> - 1) / kPack<T> * kPack<T>;
+        const TileAt at = tile_at(id - part * row_tiles * col_tiles, row_tiles, col_tiles);
         const int64_t row = uniform(at.row * S::BM), col = uniform(at.col * S::BN);
         Operand<T> A, B;
-        A.ptr = (const T *)a.d + row * a.ldd;
+        A.ptr = (const T *)a.d + row * a.ldd + skip;
         A.ld = a.ldd;
         A.outer = count - row;
         A.inner = K;
         A.end = (const T *)a.d + a.R * a.ldd;
-        B.ptr = (const T *)a.w + v0 * a.I + col;
-        B.ld = a.I;
+        B.ptr = (const T *)a.w + v0 * a.ld + col;
+        B.ld = a.ld;
         B.outer = N;
         B.inner = a.I - col;
-        B.end = (const T *)a.w + a.V * a.I;
+        B.end = (const T *)a.w + a.V * a.ld;
         __syncthreads();
         Sums<S> sums = {};
         f32x16 (&acc)[S::MI][S::NI] = sums.at;
@@ -380,7 +436,7 @@ __global__ __launch_bounds__(S::kThreads, 2) void loss_dx_kernel(LossArgs a, int
                 for (auto &v : line) v *= f;
             tile_store<T, S, true>(lds, sums, (T *)a.dx + col, a.I, A.outer, B.inner, false, a.rows + row);
         } else {
-            tile_store_fp32<S, ADD == 1>(sums, a.dx_sum + row * a.I + col, a.I, A.outer, B.inner);
+            tile_store_fp32<S, ADD == 1>(sums, a.dx_sum + (part * a.R + row) * a.I + col, a.I, A.outer, B.inner);
         }
     }
 }
@@ -404,11 +460,11 @@ __global__ __launch_bounds__(S::kThreads, 2) void loss_dw_kernel(LossArgs a, int
         A.outer = n;
         A.inner = N - row;
         A.end = (const T *)a.d + a.R * a.ldd;
-        B.ptr = x + from * a.I + col;
-        B.ld = a.I;
+        B.ptr = x + from * a.ld + col;
+        B.ld = a.ld;
         B.outer = n;
         B.inner = a.I - col;
-        B.end = x + a.R * a.I;
+        B.end = x + a.R * a.ld;
         __syncthreads();
         Sums<S> sums = {};
         f32x16 (&acc)[S::MI][S::NI] = sums.at;
@@ -422,20 +478,39 @@ __global__ __launch_bounds__(S::kThreads, 2) void loss_dw_kernel(LossArgs a, int
         for (auto &line : acc)
 #pragma unroll
             for (auto &v : line) v *= f;
-        tile_store<T, S>(lds, sums, (T *)a.dw + (v0 + row) * a.I + col, a.I, A.inner, B.inner, false);
+        T *dw = (T *)a.dw + (v0 + row) * a.I + col;
+        // a stage of flat tiles does not hold 32 of their fp32 rows
+        if constexpr (sizeof(T) == 4 && S::BM == Flat::BM) tile_store_fp32<S, false>(sums, dw, a.I, A.inner, B.inner);
+        else tile_store<T, S>(lds, sums, dw, a.I, A.inner, B.inner, false);
     }
 }
 
-// Adds dw's partial sums in the order of their chunks.
+// Adds dw's partial sums: a block takes 32 elements, eight runs of their chunks at a
+// time, and adds the runs in their order.
+constexpr int kFoldRuns = 8, kFoldElements = kPackThreads / kFoldRuns;
+
 template <typename T>
 __global__ __launch_bounds__(kPackThreads) void loss_fold_kernel(LossArgs a, int64_t v0, int64_t n, int64_t chunk) {
-    const int64_t parts = (*a.count + chunk - 1) / chunk;
+    __shared__ float runs[kFoldRuns][kFoldElements];
+    const int64_t parts = (*a.count + chunk - 1) / chunk, per = (parts + kFoldRuns - 1) / kFoldRuns;
     const float f = loss_unit(a) / kHeld<T>;
-    for (int64_t i = (int64_t)blockIdx.x * kPackThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kPackThreads) {
+    const int in = threadIdx.x % kFoldElements, run = threadIdx.x / kFoldElements;
+    for (int64_t i0 = (int64_t)blockIdx.x * kFoldElements; i0 < n; i0 += (int64_t)gridDim.x * kFoldElements) {
+        const int64_t i = i0 + in;
         float t = 0.0f;
+        if (i < n) {
 #pragma unroll 8
-        for (int64_t p = 0; p < parts; ++p) t += a.dw_partial[p * n + i];
-        ((T *)a.dw)[v0 * a.I + i] = (T)(t * f);
+            for (int64_t p = run * per; p < min(parts, (run + 1) * per); ++p) t += a.dw_partial[p * n + i];
+        }
+        __syncthreads();
+        runs[run][in] = t;
+        __syncthreads();
+        if (run == 0 && i < n) {
+            t = 0.0f;
+#pragma unroll
+            for (int r = 0; r < kFoldRuns; ++r) t += runs[r][in];
+            ((T *)a.dw)[v0 * a.I + i] = (T)(t * f);
+        }
     }
 }
 
@@ -479,15 +554,27 @@ bool direct_rows(const void *p, int64_t rows, int64_t width, int size) {
 // dw: all rows at once where its tiles fill the chip twice or there are few rows,
 // else chunks of them, about two tiles of work for each compute unit.
 int64_t dw_chunk(int64_t R, int64_t N, int64_t I) {
-    const int64_t tiles = tiles_of(N, 128) * tiles_of(I, 128), want = std::max<int64_t>(1, 2 * kUnits / tiles);
+    const int64_t tiles = tiles_of(N, N <= 64 ? 64 : 128) * tiles_of(I, 128), want = std::max<int64_t>(1, 2 * kUnits / tiles);
     if (tiles >= 2 * kUnits || R <= 1024 || want == 1) return 0;
     return whole(std::max<int64_t>(256, (R + want - 1) / want), 32);
 }
 
-// dx sums over a piece's classes, so that a tile's start and end weigh little: one
-// 256 x 256 tile to a compute unit is enough.
-bool large_dx(int64_t R, int64_t I, int64_t N, int size, bool direct) {
-    return direct && size == 2 && I > 128 && N >= 4096 && tiles_of(R, 256) * tiles_of(I, 256) >= kUnits * 3 / 4;
+// dx: 256 x 256 tiles where a piece has enough classes for their start and end to
+// weigh little, and parts of the classes side by side, added up afterwards, where
+// the tiles do not fill the chip (parts of 1,024 classes at least).
+struct DxShape {
+    bool large;
+    int64_t parts, part;
+};
+
+DxShape dx_shape(int64_t R, int64_t I, int64_t N, int size, bool direct) {
+    DxShape d;
+    d.large = direct && size == 2 && I > 128 && R > 128 && N >= 4096;
+    const int tile = d.large ? 256 : 128;
+    const int64_t tiles = tiles_of(R, tile) * tiles_of(I, tile), want = d.large ? kUnits : 2 * kUnits;
+    d.parts = std::max<int64_t>(1, std::min({(want + tiles / 2) / std::max<int64_t>(1, tiles), N / 1024, int64_t(64)}));
+    d.part = whole(tiles_of(N, (int)d.parts), 64);
+    return d;
 }
 
 template <typename T, typename S, bool DIRECT, bool BACKWARD>
@@ -511,7 +598,7 @@ hipError_t logits(const LossArgs &a, int64_t v0, int64_t N, Tiles tiles, bool di
 
 template <typename T, typename S, bool DIRECT>
 hipError_t dx_launch(const LossArgs &a, int64_t v0, int64_t N, int add, hipStream_t s) {
-    const int64_t total = tiles_of(a.R, S::BM) * tiles_of(a.I, S::BN);
+    const int64_t total = tiles_of(a.R, S::BM) * tiles_of(a.I, S::BN) * a.dx_parts;
     const unsigned blocks = (unsigned)std::min(total, kMaxBlocks);
     if (add < 0) loss_dx_kernel<T, S, DIRECT, -1><<<blocks, S::kThreads, 0, s>>>(a, v0, N, total);
     else if (add == 0) loss_dx_kernel<T, S, DIRECT, 0><<<blocks, S::kThreads, 0, s>>>(a, v0, N, total);
@@ -526,19 +613,52 @@ hipError_t dw_launch(const LossArgs &a, int64_t v0, int64_t N, int64_t chunk, hi
     return hipGetLastError();
 }
 
+// Rows off 16 bytes are moved to whole ones first where the products outweigh the
+// copy of w: kPadRows rows.
+constexpr int64_t kPadRows = 256;
+
+int64_t padded_width(int64_t R, int64_t I, int size) {
+    const int64_t ld = whole(I, 16 / size);
+    return ld != I && R > kPadRows && R * ld * size < (int64_t(1) << 31) && 320 * ld * size < (int64_t(1) << 31) ? ld : I;
+}
+
+// Bytes of both moved arrays, x first.
+int64_t padded_bytes(int64_t R, int64_t I, int64_t V, int size) {
+    const int64_t ld = padded_width(R, I, size);
+    return ld == I ? 0 : whole(R * ld * size, 256) + whole(V * ld * size, 256);
+}
+
 template <typename T>
-hipError_t forward(const LossArgs &a, hipStream_t s) {
+hipError_t pad(LossArgs &a, hipStream_t s) {
+    a.ld = padded_width(a.R, a.I, sizeof(T));
+    if (a.ld == a.I) return hipSuccess;
+    T *x = (T *)a.padded, *w = x + whole(a.R * a.ld * sizeof(T), 256) / sizeof(T);
+    auto blocks = [&](int64_t rows) {
+        return (unsigned)std::min(std::max<int64_t>(1, rows * a.ld / kPack<T> / kPackThreads), int64_t(1) << 14);
+    };
+    loss_pad_kernel<T><<<blocks(a.R), kPackThreads, 0, s>>>(a, (const T *)a.x, x, a.R, a.I, a.ld, true);
+    loss_pad_kernel<T><<<blocks(a.V), kPackThreads, 0, s>>>(a, (const T *)a.w, w, a.V, a.I, a.ld, false);
+    a.x = x;
+    a.w = w;
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t forward(LossArgs a, hipStream_t s) {
     const int64_t blocks = std::max<int64_t>(1, tiles_of(a.R, kListRows));
     if (blocks > 1) loss_count_kernel<<<(unsigned)blocks, kListThreads, 0, s>>>(a);
     loss_list_kernel<<<(unsigned)blocks, kListThreads, 0, s>>>(a, (int)blocks);
     if (const hipError_t e = hipGetLastError()) return e;
-    const bool direct = direct_rows(a.x, a.R, a.I, sizeof(T)) && direct_rows(a.w, 320, a.I, sizeof(T));
+    if (const hipError_t e = pad<T>(a, s)) return e;
+    const bool direct = direct_rows(a.x, a.R, a.ld, sizeof(T)) && direct_rows(a.w, 320, a.ld, sizeof(T));
     const Tiles tiles = tiles_for(a.R, a.V, sizeof(T), direct);
-    const int64_t joins = tiles_of(a.R, kJoinRows);
+    const int cols = (int)tiles_of(a.V, tile_cols(tiles));
+    const int64_t joins = tiles_of(a.R, join_rows(cols));
     if (a.R > 0) {
         if (const hipError_t e = logits<T, false>(a, 0, a.V, tiles, direct, s)) return e;
-        loss_join_kernel<<<(unsigned)std::min(joins, kMaxBlocks), kJoinThreads, 0, s>>>(
-            a, (int)tiles_of(a.V, tile_cols(tiles)));
+        const unsigned n = (unsigned)std::min(joins, kMaxBlocks);
+        if (join_rows(cols) == 8) loss_join_kernel<8><<<n, kJoinThreads, 0, s>>>(a, cols);
+        else loss_join_kernel<kJoinRows><<<n, kJoinThreads, 0, s>>>(a, cols);
     }
     if (a.block_loss) loss_total_kernel<<<1, kTotalThreads, 0, s>>>(a, joins);
     return hipGetLastError();
@@ -550,24 +670,30 @@ hipError_t backward(const LossArgs &args, hipStream_t s) {
     const int size = sizeof(T);
     const int64_t piece = piece_of(a.R, a.V, size), pieces = tiles_of(a.V, (int)piece);
     a.ldd = piece;
-    const bool direct = direct_rows(a.x, a.R, a.I, size) && direct_rows(a.w, 320, a.I, size) &&
+    if (const hipError_t e = pad<T>(a, s)) return e;
+    const bool direct = direct_rows(a.x, a.R, a.ld, size) && direct_rows(a.w, 320, a.ld, size) &&
                         direct_rows(nullptr, 320, a.ldd, size);
     if (a.per_row) loss_unit_kernel<<<1, kTotalThreads, 0, s>>>(a);
-    const int64_t packs = a.R * tiles_of(a.I, kPack<T>);
+    const int64_t packs = a.R * tiles_of(a.ld, kPack<T>);
     const unsigned pack_blocks = (unsigned)std::min(std::max<int64_t>(1, packs / kPackThreads), int64_t(1) << 14);
     if (a.dw) loss_pack_kernel<T><<<pack_blocks, kPackThreads, 0, s>>>(a);
     if (const hipError_t e = hipGetLastError()) return e;
+    // the first piece is the largest: its parts serve all
+    const DxShape dx = dx_shape(a.R, a.I, std::min(piece, a.V), size, direct);
+    a.dx_parts = dx.parts;
+    a.dx_part = dx.part;
+    const bool summed = pieces > 1 || dx.parts > 1;
     for (int64_t v0 = 0; v0 < a.V; v0 += piece) {
         const int64_t N = std::min(piece, a.V - v0);
         if (a.R > 0)
             if (const hipError_t e = logits<T, true>(a, v0, N, tiles_for(a.R, N, size, direct), direct, s)) return e;
         if (a.dx && a.R > 0) {
-            const int add = pieces == 1 ? -1 : v0 ? 1 : 0;
             hipError_t e = hipSuccess;
-            if (large_dx(a.R, a.I, N, size, direct)) {
-                if constexpr (sizeof(T) == 2) e = dx_launch<T, Large, true>(a, v0, N, add, s);
+            if (dx.large) {
+                if constexpr (sizeof(T) == 2) e = dx_launch<T, Large, true>(a, v0, N, summed ? v0 != 0 : -1, s);
             } else {
-                e = direct ? dx_launch<T, Medium, true>(a, v0, N, add, s) : dx_launch<T, Medium, false>(a, v0, N, add, s);
+                e = direct ? dx_launch<T, Medium, true>(a, v0, N, summed ? v0 != 0 : -1, s)
+                           : dx_launch<T, Medium, false>(a, v0, N, summed ? v0 != 0 : -1, s);
             }
             if (e) return e;
         }
@@ -576,6 +702,8 @@ hipError_t backward(const LossArgs &args, hipStream_t s) {
             hipError_t e = hipSuccess;
             if (size == 2 && tiles_for(N, a.I, size, direct) == Tiles::kLarge) {
                 if constexpr (sizeof(T) == 2) e = dw_launch<T, Large, true>(a, v0, N, chunk, s);
+            } else if (N <= 64) {
+                e = direct ? dw_launch<T, Flat, true>(a, v0, N, chunk, s) : dw_launch<T, Flat, false>(a, v0, N, chunk, s);
             } else {
                 e = direct ? dw_launch<T, Medium, true>(a, v0, N, chunk, s)
                            : dw_launch<T, Medium, false>(a, v0, N, chunk, s);
@@ -583,12 +711,12 @@ hipError_t backward(const LossArgs &args, hipStream_t s) {
             if (e) return e;
             if (chunk) {
                 const int64_t n = N * a.I;
-                loss_fold_kernel<T><<<(unsigned)std::min(tiles_of(n, kPackThreads), kMaxBlocks), kPackThreads, 0, s>>>(
+                loss_fold_kernel<T><<<(unsigned)std::min(tiles_of(n, kFoldElements), kMaxBlocks), kPackThreads, 0, s>>>(
                     a, v0, n, chunk);
             }
         }
     }
-    if (a.dx && a.R > 0) loss_rest_kernel<T><<<pack_blocks, kPackThreads, 0, s>>>(a, pieces > 1);
+    if (a.dx && a.R > 0) loss_rest_kernel<T><<<pack_blocks, kPackThreads, 0, s>>>(a, summed);
     return hipGetLastError();
 }
 
@@ -598,33 +726,35 @@ hipError_t backward(const LossArgs &args, hipStream_t s) {
 int64_t loss_state_bytes(int64_t R) { return whole(3 * R * 4, 8) + 8; }
 
 // Each tile's maximum and sum, the class's logits, the blocks' counts and losses.
-int64_t loss_workspace_floats(int64_t R, int64_t V) {
-    return R * tiles_of(V, V <= 64 ? 64 : 128) * 2 + R + tiles_of(R, kListRows) + tiles_of(R, kJoinRows);
+static int64_t forward_floats(int64_t R, int64_t V) {
+    return R * tiles_of(V, V <= 64 ? 64 : 128) * 2 + R + std::max<int64_t>(1, tiles_of(R, kListRows)) +
+           tiles_of(R, 8);
 }
 
-void loss_forward_arrays(LossArgs &a, void *state, float *workspace, bool rows_only) {
+int64_t loss_workspace_bytes(int64_t R, int64_t I, int64_t V, int type) {
+    return 256 + padded_bytes(R, I, V, type == SPMM_F32 ? 4 : 2) + forward_floats(R, V) * (int64_t)sizeof(float);
+}
+
+static void state_arrays(LossArgs &a, void *state) {
     a.stats = static_cast<float *>(state);
     a.rows = reinterpret_cast<int *>(a.stats + 2 * a.R);
     a.count = reinterpret_cast<int64_t *>(static_cast<char *>(state) + whole(3 * a.R * 4, 8));
-    if (rows_only) return;
-    const int64_t tiles = a.R * tiles_of(a.V, a.V <= 64 ? 64 : 128);
-    a.tile_top = workspace;
-    a.tile_sum = a.tile_top + tiles;
-    a.picked = a.tile_sum + tiles;
-    a.block_count = reinterpret_cast<int *>(a.picked + a.R);
-    if (!a.row_loss) a.block_loss = a.picked + a.R + tiles_of(a.R, kListRows);
 }
 
 struct BackwardSizes {
-    int64_t d, packed, dx_sum, dw_partial;       // bytes, each whole 256s
+    int64_t d, packed, dx_sum, dw_partial, padded;       // bytes, each whole 256s
 };
 
 static BackwardSizes backward_sizes(int64_t R, int64_t I, int64_t V, int size) {
     const int64_t piece = piece_of(R, V, size);
     BackwardSizes b;
     b.d = whole(R * piece * size, 256);
-    b.packed = whole(R * I * size, 256);
-    b.dx_sum = piece < V ? whole(R * I * 4, 256) : 0;
+    b.packed = whole(R * padded_width(R, I, size) * size, 256);
+    b.padded = padded_bytes(R, I, V, size);
+    // the addresses are not known here: what either way of staging needs
+    const int64_t parts = std::max(dx_shape(R, I, std::min(piece, V), size, true).parts,
+                                   dx_shape(R, I, std::min(piece, V), size, false).parts);
+    b.dx_sum = piece < V || parts > 1 ? whole(parts * R * I * 4, 256) : 0;
     b.dw_partial = 0;
     for (const int64_t n : {std::min(piece, V), V % piece}) {
         const int64_t chunk = n ? dw_chunk(R, n, I) : 0;
@@ -635,12 +765,20 @@ static BackwardSizes backward_sizes(int64_t R, int64_t I, int64_t V, int size) {
 
 int64_t loss_backward_workspace_bytes(int64_t R, int64_t I, int64_t V, int type) {
     const BackwardSizes b = backward_sizes(R, I, V, type == SPMM_F32 ? 4 : 2);
-    return 256 + 256 + b.d + b.packed + b.dx_sum + b.dw_partial;      // room to start on 256 bytes, and the unit
+    return 256 + 256 + b.d + b.packed + b.dx_sum + b.dw_partial + b.padded;      // room to start on 256 bytes, and the unit
 }
 
-hipError_t launch_loss(const LossArgs &args, void *state, float *workspace, int type, hipStream_t s) {
+hipError_t launch_loss(const LossArgs &args, void *state, void *workspace, int type, hipStream_t s) {
     LossArgs a = args;
-    loss_forward_arrays(a, state, workspace, false);
+    state_arrays(a, state);
+    char *at = reinterpret_cast<char *>(whole((int64_t)(uintptr_t)workspace, 256));
+    a.padded = at;
+    a.tile_top = reinterpret_cast<float *>(at + padded_bytes(a.R, a.I, a.V, type == SPMM_F32 ? 4 : 2));
+    const int64_t tiles = a.R * tiles_of(a.V, a.V <= 64 ? 64 : 128);
+    a.tile_sum = a.tile_top + tiles;
+    a.picked = a.tile_sum + tiles;
+    a.block_count = reinterpret_cast<int *>(a.picked + a.R);
+    if (!a.row_loss) a.block_loss = a.picked + a.R + std::max<int64_t>(1, tiles_of(a.R, kListRows));
     if (type == SPMM_F32) return forward<float>(a, s);
     if (type == SPMM_BF16) return forward<__bf16>(a, s);
     return forward<_Float16>(a, s);
@@ -648,14 +786,15 @@ hipError_t launch_loss(const LossArgs &args, void *state, float *workspace, int 
 
 hipError_t launch_loss_backward(const LossArgs &args, const void *state, void *workspace, int type, hipStream_t s) {
     LossArgs a = args;
-    loss_forward_arrays(a, const_cast<void *>(state), nullptr, true);
+    state_arrays(a, const_cast<void *>(state));
     const BackwardSizes b = backward_sizes(a.R, a.I, a.V, type == SPMM_F32 ? 4 : 2);
     char *at = reinterpret_cast<char *>(whole((int64_t)(uintptr_t)workspace, 256));
     a.unit = reinterpret_cast<float *>(at);
     a.d = at += 256;
     a.packed = at += b.d;
     a.dx_sum = reinterpret_cast<float *>(at += b.packed);
-    a.dw_partial = reinterpret_cast<float *>(at + b.dx_sum);
+    a.dw_partial = reinterpret_cast<float *>(at += b.dx_sum);
+    a.padded = at + b.dw_partial;
     if (type == SPMM_F32) return backward<float>(a, s);
     if (type == SPMM_BF16) return backward<__bf16>(a, s);
     return backward<_Float16>(a, s);

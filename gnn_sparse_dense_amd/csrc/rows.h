@@ -258,14 +258,18 @@ struct LossArgs {
     float *unit;             // per_row: power of two that dloss is held in
     void *d;                 // [R, ldd], a piece's gradient of the logits
     int64_t ldd;
-    void *packed;            // [R, I], the listed rows of x
-    float *dx_sum;           // [R, I]
+    int64_t ld;              // elements from a row of x, and of w, to the next
+    void *padded;            // x and w with rows of whole 16 bytes, where theirs are not
+    void *packed;            // [R, ld], the listed rows of x
+    int64_t dx_parts;        // of a piece's classes, dx_part each
+    int64_t dx_part;
+    float *dx_sum;           // [dx_parts, R, I]
     float *dw_partial;
 };
 int64_t loss_state_bytes(int64_t R);
-int64_t loss_workspace_floats(int64_t R, int64_t V);
+int64_t loss_workspace_bytes(int64_t R, int64_t I, int64_t V, int type);
 int64_t loss_backward_workspace_bytes(int64_t R, int64_t I, int64_t V, int type);
-hipError_t launch_loss(const LossArgs &a, void *state, float *workspace, int type, hipStream_t s);
+hipError_t launch_loss(const LossArgs &a, void *state, void *workspace, int type, hipStream_t s);
 hipError_t launch_loss_backward(const LossArgs &a, const void *state, void *workspace, int type, hipStream_t s);
 
 }  // namespace gspmm

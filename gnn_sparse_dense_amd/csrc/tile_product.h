@@ -70,14 +70,21 @@ using Medium = Shape<128, 128, 2, 2>;
 // c ^ (r / 4 & 3), so that 16 lanes that read one chunk column of 16 rows
 // cover all 64 banks once.
 // KS (summed index = row), 16-bit: 32 rows of 2 B bytes; the 32-byte piece c
-// of row k at c ^ 2 (k & 3), so that the four rows a 16-lane transposing read
-// touches lie in different banks.  fp32: 16 rows of 4 B bytes, as they are.
+// of row k at c ^ 2 (k & 3) (B = 64, two rows to the banks: c ^ 2 (k / 2 & 1)), so
+// that the four rows a 16-lane transposing read touches lie in different banks.
+// fp32: 16 rows of 4 B bytes, as they are.
+
+template <int B>
+__device__ inline int turned_piece(int k) {
+    static_assert(B >= 64);
+    return B >= 128 ? (k & 3) << 1 : (k >> 1 & 1) << 1;
+}
 
 template <typename T, bool KC, int B>
 __device__ inline int chunk_offset(int outer, int chunk) {
     if constexpr (KC) return outer * kStepBytes + ((chunk ^ (outer >> 2 & 3)) << 4);
     else if constexpr (sizeof(T) == 4) return outer * B * 4 + (chunk << 4);
-    else return outer * B * 2 + (((chunk >> 1) ^ ((outer & 3) << 1)) << 5) + ((chunk & 1) << 4);
+    else return outer * B * 2 + (((chunk >> 1) ^ turned_piece<B>(outer)) << 5) + ((chunk & 1) << 4);
 }
 
 // One operand of a tile.  KC: `outer` rows (tile rows) of `inner` summed
@@ -136,7 +143,7 @@ struct Copy {
             constexpr int kRow = B * (int)sizeof(T);
             const int k = byte / kRow;
             int chunk = byte % kRow / 16;
-            if constexpr (sizeof(T) == 2) chunk = (((chunk >> 1) ^ ((k & 3) << 1)) << 1) | (chunk & 1);
+            if constexpr (sizeof(T) == 2) chunk = (((chunk >> 1) ^ turned_piece<B>(k)) << 1) | (chunk & 1);
             first = k;
             left = uniform((int)o.outer);
             step_bytes = (int64_t)kStep<T> * uniform((int)row_bytes);
@@ -222,7 +229,7 @@ struct Reader {
 #pragma unroll
             for (int i = 0; i < COUNT; ++i) {
                 const int piece = (m0 >> 4) + 2 * i + ((lane >> 4) & 1);
-                at[i] = k * B * 2 + ((piece ^ ((k & 3) << 1)) << 5) + ((l & 3) << 3);
+                at[i] = k * B * 2 + ((piece ^ turned_piece<B>(k)) << 5) + ((l & 3) << 3);
             }
         } else {
             at[0] = half * 4 * B * 4 + m * 4;
