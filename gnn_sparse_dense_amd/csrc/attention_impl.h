@@ -210,14 +210,15 @@ struct Fill {
 // before the first segment, the segments, the rows behind the last.
 struct Runs {
     const int64_t *offsets;
-    int64_t S, rows;
-    int scale;
+    int S, rows, scale;
 
-    __device__ inline int64_t bound(int64_t v) const {
+    __device__ inline Runs(const int64_t *o, int64_t s, int64_t r, int by) : offsets(o), S((int)s), rows((int)r), scale(by) {}
+
+    __device__ inline int bound(int v) const {
         if (v <= 0) return 0;
         if (v > S + 1) return rows;
         const int64_t b = offsets[v - 1];
-        return b < 0 ? 0 : b > rows ? rows : b;
+        return b < 0 ? 0 : b > rows ? rows : (int)b;
     }
 };
 
@@ -226,7 +227,7 @@ struct Runs {
 // by a search that looks at 64 runs at a time; a slot that its run does not need
 // has tile >= tiles.
 struct Slot {
-    int64_t run, row0;            // the run's first row
+    int run, row0;                // the run's first row
     int rows, packed;             // how many it has
     int tile, tiles;
 };
@@ -234,22 +235,24 @@ struct Slot {
 template <int LEN>
 __device__ inline Slot find(const Runs &a, int slot) {
     const int lane = threadIdx.x & (kWave - 1);
-    int64_t v = 0, n = a.S + 2;
+    int v = 0, n = a.S + 2;
     while (n > 1) {
-        const int64_t step = (n + kWave - 1) / kWave, to = lane * step;
+        const int step = (n + kWave - 1) / kWave, to = lane * step;
         const bool from = lane == 0 || (to < n && a.bound(v + to) * a.scale / LEN + v + to <= slot);
-        const int64_t past = (kWave - 1 - __builtin_clzll(__ballot(from))) * step;
+        const int past = (kWave - 1 - __builtin_clzll(__ballot(from))) * step;
         v += past;
         n = min(step, n - past);
     }
+    // lanes 0 and 1 load both bounds at once
+    const int bound = a.bound(v + (lane & 1));
     Slot s;
     s.run = uniform(v);
-    s.row0 = uniform(a.bound(v));
-    s.rows = uniform((int)max(int64_t(0), a.bound(v + 1) - s.row0));
+    s.row0 = __builtin_amdgcn_readlane(bound, 0);
+    s.rows = max(0, __builtin_amdgcn_readlane(bound, 1) - s.row0);
     s.packed = s.rows * a.scale;
     s.tiles = (s.packed + LEN - 1) / LEN;
-    const int64_t tile = slot - s.row0 * a.scale / LEN - s.run;
-    s.tile = tile < 0 || tile >= s.tiles ? s.tiles : (int)tile;
+    s.tile = slot - s.row0 * a.scale / LEN - s.run;
+    if (s.tile < 0 || s.tile > s.tiles) s.tile = s.tiles;
     return s;
 }
 
@@ -292,7 +295,7 @@ __device__ inline void copy_floats(LdsByte *lds, const float *from, int at, bool
 }
 
 // The lane's row of D elements (times f) from the blocks of multiply().
-template <typename OUT, int BLOCKS>
+template <bool WHOLE, typename OUT, int BLOCKS>
 __device__ inline void store_row(OUT *row, const f32x16 (&acc)[BLOCKS], float f, int D) {
     const int half = (threadIdx.x & (kWave - 1)) >> 5;
 #pragma unroll
@@ -303,9 +306,9 @@ __device__ inline void store_row(OUT *row, const f32x16 (&acc)[BLOCKS], float f,
             OUT v[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = (OUT)(acc[b][q * 4 + e] * f);
-            if (d + 4 <= D) {
+            if (WHOLE ? d < D : d + 4 <= D) {
                 __builtin_memcpy(row + d, v, sizeof(v));
-            } else {
+            } else if constexpr (!WHOLE) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     if (d + e < D) row[d + e] = v[e];
@@ -325,13 +328,14 @@ struct Queries {
     int keys;
 
     __device__ inline void locate(const AttentionArgs &a, const Slot &s, int hk, int m0, int rows_ahead) {
-        const Runs keyruns = {a.key_offsets, a.S, a.K, 1};
+        const Runs keyruns(a.key_offsets, a.S, a.K, 1);
         packed = s.packed;
-        key0 = uniform(keyruns.bound(s.run));
-        keys = uniform((int)max(int64_t(0), keyruns.bound(s.run + 1) - key0));
+        const int bound = keyruns.bound(s.run + (threadIdx.x & 1)), first = __builtin_amdgcn_readlane(bound, 0);
+        key0 = first;
+        keys = max(0, __builtin_amdgcn_readlane(bound, 1) - first);
         m = m0 + rows_ahead + (threadIdx.x & 31);
         const int mc = min(m, packed - 1), i = quotient(a.G, mc);
-        row = s.row0 + i;
+        row = (int64_t)s.row0 + i;
         head = hk * a.G.d + mc - i * a.G.d;
         const int ahead = keys - s.rows + 1;
         seen = sees(a, i, ahead);
@@ -356,13 +360,19 @@ __device__ inline int seen_by_tile(const AttentionArgs &a, const Slot &s, int ke
 template <typename T, int DP>
 using RowPacks = Pack<T>[Tile<T, DP>::kSteps];
 
-template <typename T, int DP>
+// WHOLE: D is a multiple of a pack.
+template <typename T, int DP, bool WHOLE>
 __device__ inline void load_row(RowPacks<T, DP> &r, const T *row, int D, bool exists) {
     const int half = (threadIdx.x & (kWave - 1)) >> 5;
 #pragma unroll
     for (int ks = 0; ks < Tile<T, DP>::kSteps; ++ks) {
         const int e = (2 * ks + half) * kPack<T>;
-        r[ks] = load_pack(row + (exists && e < D ? e : 0), exists ? D - e : 0);
+        if constexpr (WHOLE) {
+            r[ks] = Pack<T>{};
+            if (exists && e < D) r[ks] = load_pack(row + e);
+        } else {
+            r[ks] = load_pack(row + (exists && e < D ? e : 0), exists ? D - e : 0);
+        }
     }
 }
 
@@ -432,7 +442,7 @@ __global__ __launch_bounds__(WAVES * kWave, (kQuerySide<T, DP, DIRECT>)) void at
     const int D = (int)a.D;
     const RowReader<T, DP> rows;
     const TurnedReader<T, DP> turned;
-    const Runs runs = {a.offsets, a.S, a.R, a.G.d};
+    const Runs runs(a.offsets, a.S, a.R, a.G.d);
     const float c = a.scale * kLog2e;
     for (unsigned id = blockIdx.x; id < total; id += gridDim.x) {
         const unsigned heads = (unsigned)a.Hk, rest = id / heads, parts = (unsigned)a.parts;
@@ -449,7 +459,7 @@ __global__ __launch_bounds__(WAVES * kWave, (kQuerySide<T, DP, DIRECT>)) void at
             const int per = (tiles + a.parts - 1) / a.parts;
             const int t0 = part * per, t1 = min(tiles, t0 + per);
             RowPacks<T, DP> mine;
-            load_row<T, DP>(mine, (const T *)a.q + q.row * a.ldq + q.head * D, D, q.exists());
+            load_row<T, DP, DIRECT>(mine, (const T *)a.q + q.row * a.ldq + q.head * D, D, q.exists());
             const T *k = (const T *)a.k + q.key0 * a.ldk + hk * D, *v = (const T *)a.v + q.key0 * a.ldv + hk * D;
             Fill<T, DP, BN, WAVES, DIRECT> fk, fv;
             fk.aim(KeyRows<T>{k, a.ldk, BN}, D, wave);
@@ -520,13 +530,13 @@ __global__ __launch_bounds__(WAVES * kWave, (kQuerySide<T, DP, DIRECT>)) void at
         sum += other_half(sum);
         const int64_t at = q.row * a.H + q.head, all = a.R * a.H;
         if (q.exists() && a.parts > 1) {
-            store_row(a.partial + (part * all + at) * D, acc, 1.0f, D);
+            store_row<DIRECT>(a.partial + (part * all + at) * D, acc, 1.0f, D);
             if (half == 0) {
                 a.partial_top[part * all + at] = top;
                 a.partial_sum[part * all + at] = sum;
             }
         } else if (q.exists()) {
-            store_row((T *)a.out + at * D, acc, sum == 0.0f ? 0.0f : 1.0f / sum, D);
+            store_row<DIRECT>((T *)a.out + at * D, acc, sum == 0.0f ? 0.0f : 1.0f / sum, D);
             if (a.lse && half == 0) a.lse[at] = sum == 0.0f ? INFINITY : top + log2f(sum);
         }
     }
@@ -581,7 +591,7 @@ __global__ __launch_bounds__(WAVES * kWave, (kQuerySide<T, DP, DIRECT>)) void at
     const int D = (int)a.D;
     const RowReader<T, DP> rows;
     const TurnedReader<T, DP> turned;
-    const Runs runs = {a.offsets, a.S, a.R, a.G.d};
+    const Runs runs(a.offsets, a.S, a.R, a.G.d);
     const float c = a.scale * kLog2e;
     for (unsigned id = blockIdx.x; id < total; id += gridDim.x) {
         const unsigned heads = (unsigned)a.Hk, rest = id / heads;
@@ -595,8 +605,8 @@ __global__ __launch_bounds__(WAVES * kWave, (kQuerySide<T, DP, DIRECT>)) void at
         f32x16 acc[L::kBlocks] = {};
         if (s.run > 0 && s.run <= a.S) {
             RowPacks<T, DP> mine, dout;
-            load_row<T, DP>(dout, (const T *)a.dout + at * D, D, q.exists());
-            load_row<T, DP>(mine, (const T *)a.out + at * D, D, q.exists());
+            load_row<T, DP, DIRECT>(dout, (const T *)a.dout + at * D, D, q.exists());
+            load_row<T, DP, DIRECT>(mine, (const T *)a.out + at * D, D, q.exists());
             float delta = 0.0f;
 #pragma unroll
             for (int ks = 0; ks < L::kSteps; ++ks)
@@ -606,7 +616,7 @@ __global__ __launch_bounds__(WAVES * kWave, (kQuerySide<T, DP, DIRECT>)) void at
             const float lse = q.exists() ? a.lse[at] : INFINITY;
             if (q.exists() && half == 0) a.delta[at] = delta;
             if (a.dq) {
-                load_row<T, DP>(mine, (const T *)a.q + q.row * a.ldq + q.head * D, D, q.exists());
+                load_row<T, DP, DIRECT>(mine, (const T *)a.q + q.row * a.ldq + q.head * D, D, q.exists());
                 const int tiles = (seen_by_tile<BM>(a, s, q.keys) + BN - 1) / BN;
                 const T *k = (const T *)a.k + q.key0 * a.ldk + hk * D, *v = (const T *)a.v + q.key0 * a.ldv + hk * D;
                 Fill<T, DP, BN, WAVES, DIRECT> fk, fv;
@@ -658,7 +668,7 @@ __global__ __launch_bounds__(WAVES * kWave, (kQuerySide<T, DP, DIRECT>)) void at
         } else if (q.exists() && half == 0) {
             a.delta[at] = 0.0f;
         }
-        if (a.dq && q.exists()) store_row((T *)a.dq + at * D, acc, a.scale, D);
+        if (a.dq && q.exists()) store_row<DIRECT>((T *)a.dq + at * D, acc, a.scale, D);
     }
 }
 
@@ -675,9 +685,10 @@ struct SeenBy {
     int64_t behind;
 
     __device__ inline SeenBy(const AttentionArgs &a, const Slot &s, int key, int tile_rows) {
-        const Runs queries = {a.offsets, a.S, a.R, 1};
-        row0 = uniform(queries.bound(s.run));
-        const int rows = uniform((int)max(int64_t(0), queries.bound(s.run + 1) - row0));
+        const Runs queries(a.offsets, a.S, a.R, 1);
+        const int bound = queries.bound(s.run + (threadIdx.x & 1)), from = __builtin_amdgcn_readlane(bound, 0);
+        row0 = from;
+        const int rows = max(0, __builtin_amdgcn_readlane(bound, 1) - from);
         packed = rows * a.G.d;
         behind = a.causal ? (int64_t)rows - s.rows : INT32_MIN;
         start = first(a, key) / tile_rows;
@@ -865,7 +876,7 @@ __global__ __launch_bounds__(WAVES * kWave, (kKeySide<T, DP, DIRECT>)) void atte
     TILE_PAIRS(lse_of, delta_of, kWave * 4);
     const int wave = uniform((int)threadIdx.x / kWave);
     const int D = (int)a.D;
-    const Runs runs = {a.key_offsets, a.S, a.K, 1};
+    const Runs runs(a.key_offsets, a.S, a.K, 1);
     for (unsigned id = blockIdx.x; id < total; id += gridDim.x) {
         const unsigned heads = (unsigned)a.Hk, rest = id / heads, most = (unsigned)a.key_parts;
         // tiles use few of their parts: they start at another one in each, so that
@@ -885,9 +896,9 @@ __global__ __launch_bounds__(WAVES * kWave, (kKeySide<T, DP, DIRECT>)) void atte
             if (part >= parts) continue;
             const int per = (by.tiles + parts - 1) / parts;
             const int t0 = by.start + min(by.tiles, part * per), t1 = min(by.start + by.tiles, t0 + per);
-            const int64_t key = s.row0 + min(j, s.rows - 1);
-            load_row<T, DP>(sums.k, (const T *)a.k + key * a.ldk + hk * D, D, exists);
-            load_row<T, DP>(sums.v, (const T *)a.v + key * a.ldv + hk * D, D, exists);
+            const int64_t key = (int64_t)s.row0 + min(j, s.rows - 1);
+            load_row<T, DP, DIRECT>(sums.k, (const T *)a.k + key * a.ldk + hk * D, D, exists);
+            load_row<T, DP, DIRECT>(sums.v, (const T *)a.v + key * a.ldv + hk * D, D, exists);
             RowTiles<T, DP, BN, WAVES, DIRECT> tiles(a, by.row0, hk, by.packed, wave);
             __syncthreads();
             if constexpr (kAhead) {
@@ -952,13 +963,13 @@ __global__ __launch_bounds__(WAVES * kWave, (kKeySide<T, DP, DIRECT>)) void atte
                     });
             }
         }
-        const int64_t at = ((s.row0 + j) * a.Hk + hk) * D, shift = part * a.K * a.Hk * a.D;
+        const int64_t at = (((int64_t)s.row0 + j) * a.Hk + hk) * D, shift = part * a.K * a.Hk * a.D;
         if (exists && parts > 1) {
-            if (a.dk) store_row(a.partial_dk + shift + at, sums.dk, a.scale, D);
-            if (a.dv) store_row(a.partial_dv + shift + at, sums.dv, 1.0f, D);
+            if (a.dk) store_row<DIRECT>(a.partial_dk + shift + at, sums.dk, a.scale, D);
+            if (a.dv) store_row<DIRECT>(a.partial_dv + shift + at, sums.dv, 1.0f, D);
         } else if (exists && part == 0) {
-            if (a.dk) store_row((T *)a.dk + at, sums.dk, a.scale, D);
-            if (a.dv) store_row((T *)a.dv + at, sums.dv, 1.0f, D);
+            if (a.dk) store_row<DIRECT>((T *)a.dk + at, sums.dk, a.scale, D);
+            if (a.dv) store_row<DIRECT>((T *)a.dv + at, sums.dv, 1.0f, D);
         }
     }
 }
@@ -968,7 +979,7 @@ constexpr int kAddThreads = 256, kAddKeys = 16;
 
 template <typename T, int LEN, int ROWS>
 __global__ __launch_bounds__(kAddThreads) void attention_add_kernel(AttentionArgs a, unsigned total) {
-    const Runs runs = {a.key_offsets, a.S, a.K, 1};
+    const Runs runs(a.key_offsets, a.S, a.K, 1);
     const int D = (int)a.D, quads = (D + 3) / 4;
     const int64_t all = a.K * a.Hk * D;
     for (unsigned id = blockIdx.x; id < total; id += gridDim.x) {
@@ -985,7 +996,7 @@ __global__ __launch_bounds__(kAddThreads) void attention_add_kernel(AttentionArg
             T *to = (T *)(second ? a.dv : a.dk);
             if (!to) continue;
             const int in = second ? i - keys * quads : i, row = in / quads, d = (in - row * quads) * 4;
-            const int64_t at = ((s.row0 + key + row) * a.Hk + hk) * D + d;
+            const int64_t at = (((int64_t)s.row0 + key + row) * a.Hk + hk) * D + d;
             const float *from = (second ? a.partial_dv : a.partial_dk) + at;
             float sum[4] = {};
             for (int p = 0; p < parts; ++p, from += all) {
