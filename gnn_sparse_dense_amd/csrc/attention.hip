@@ -87,6 +87,7 @@ hipError_t launch_attention(const AttentionArgs &args, float *workspace, int typ
         a.partial_sum = a.partial_top + a.parts * a.R * a.H;
     }
     const bool large = large_tiles(a.R * a.G.d, a.S);
+    a.short_keys = a.K <= 64 * a.S;
     const bool direct = direct_rows(a.k, a.ldk, a.D, size) && direct_rows(a.v, a.ldv, a.D, size);
     const auto pass = AttentionPass::kForward;
     if (const hipError_t e = type == SPMM_F32    ? launch_attention_pass<float>(a, pass, large, direct, s)

@@ -320,7 +320,7 @@ __device__ inline void store_row(OUT *row, const f32x16 (&acc)[BLOCKS], float f,
 template <typename T>
 struct Queries {
     int m, packed;      // the lane's packed row, and how many there are
-    int64_t row;        // its row and head
+    int64_t row;        // its row, and head of the group
     int head;
     int seen;           // keys that it sees
     int seen_least, seen_most;      // over the wave's rows
@@ -386,22 +386,36 @@ constexpr int kQuerySide = sizeof(T) * DP > (DIRECT ? 256 : 128) ? 1 : 2;
 template <typename T, int DP, bool DIRECT>
 constexpr int kKeySide = sizeof(T) * DP > (DIRECT ? 128 : 64) ? 1 : 2;
 
-// Two stages of two tiles each, arrays of their own (see Stages).
-#define TILE_PAIRS(x, y, bytes)                                  \
-    __shared__ __attribute__((aligned(1024))) char x##0[bytes]; \
-    __shared__ __attribute__((aligned(1024))) char y##0[bytes]; \
-    __shared__ __attribute__((aligned(1024))) char x##1[bytes]; \
-    __shared__ __attribute__((aligned(1024))) char y##1[bytes]; \
-    LdsByte *const x[2] = {(LdsByte *)x##0, (LdsByte *)x##1};   \
+// One wave's short segments are one tile: with one stage of it twice as many waves
+// share a compute unit (4,096 graphs of 24 rows, 4 heads of 32 fp32, with gradients:
+// 373 -> 309 us).  Forward, one row against long segments keeps two (32 rows, 100,003
+// keys, 8 key heads of 128 bf16: 101 against 106 us).
+template <int WAVES>
+constexpr int kStagesOf = WAVES == 1 ? 1 : 2;
+
+// Stages of two tiles each, arrays of their own (see Stages).
+#define TILE_PAIRS(x, y, bytes, stages)                                             \
+    __shared__ __attribute__((aligned(1024))) char x##0[bytes];                    \
+    __shared__ __attribute__((aligned(1024))) char y##0[bytes];                    \
+    __shared__ __attribute__((aligned(1024))) char x##1[stages == 1 ? 16 : bytes]; \
+    __shared__ __attribute__((aligned(1024))) char y##1[stages == 1 ? 16 : bytes]; \
+    LdsByte *const x[2] = {(LdsByte *)x##0, (LdsByte *)x##1};                      \
     LdsByte *const y[2] = {(LdsByte *)y##0, (LdsByte *)y##1}
 
 // Walks the tiles [t0, t1) of two arrays: while tile t is used, tile t + 1 is
-// on its way into the other stage.
-template <bool DIRECT, typename LoadAll, typename PutAll, typename Use>
+// on its way into the other stage (or, with one, into registers if !DIRECT).
+template <bool DIRECT, int STAGES, typename LoadAll, typename PutAll, typename Use>
 __device__ inline void walk(int t0, int t1, LoadAll load, PutAll put, Use use) {
     if (t0 >= t1) return;
-    load(t0, 0);
-    if constexpr (DIRECT) {
+    if constexpr (DIRECT && STAGES == 1) {
+        for (int t = t0; t < t1; ++t) {
+            load(t, 0);
+            wait_copies<0>();
+            use(t, 0);
+            wait_copies<0>();
+        }
+    } else if constexpr (DIRECT) {
+        load(t0, 0);
         auto step = [&](int t, int u) {
             wait_copies<0>();
             load(t + 1, 1 - u);                          // behind the last tile: zeros, or a tile that is not used
@@ -414,7 +428,17 @@ __device__ inline void walk(int t0, int t1, LoadAll load, PutAll put, Use use) {
         }
         if (t < t1) step(t, 0);
         wait_copies<0>();
+    } else if constexpr (STAGES == 1) {
+        load(t0, 0);
+        for (int t = t0; t < t1; ++t) {
+            put(0);
+            __syncthreads();
+            if (t + 1 < t1) load(t + 1, 0);
+            use(t, 0);
+            __syncthreads();
+        }
     } else {
+        load(t0, 0);
         put(0);
         for (int t = t0; t < t1; t += 2) {
 #pragma unroll
@@ -433,11 +457,11 @@ __device__ inline void walk(int t0, int t1, LoadAll load, PutAll put, Use use) {
 
 // ---- forward ----
 
-template <typename T, int DP, int WAVES, bool DIRECT>
+template <typename T, int DP, int WAVES, bool DIRECT, int STAGES>
 __global__ __launch_bounds__(WAVES * kWave, (kQuerySide<T, DP, DIRECT>)) void attention_kernel(AttentionArgs a, unsigned total) {
     using L = Tile<T, DP>;
     constexpr int BM = 32 * WAVES, BN = kTileRows<T, WAVES>, NB = BN / 32;
-    TILE_PAIRS(ktile, vtile, BN * L::kPitch);
+    TILE_PAIRS(ktile, vtile, BN * L::kPitch, STAGES);
     const int wave = uniform((int)threadIdx.x / kWave), half = (threadIdx.x & (kWave - 1)) >> 5;
     const int D = (int)a.D;
     const RowReader<T, DP> rows;
@@ -465,7 +489,7 @@ __global__ __launch_bounds__(WAVES * kWave, (kQuerySide<T, DP, DIRECT>)) void at
             fk.aim(KeyRows<T>{k, a.ldk, BN}, D, wave);
             fv.aim(KeyRows<T>{v, a.ldv, BN}, D, wave);
             __syncthreads();
-            walk<DIRECT>(
+            walk<DIRECT, STAGES>(
                 t0, t1,
                 [&](int t, int u) {
                     const int j = t * BN, left = q.keys - j;
@@ -586,7 +610,7 @@ template <typename T, int DP, int WAVES, bool DIRECT>
 __global__ __launch_bounds__(WAVES * kWave, (kQuerySide<T, DP, DIRECT>)) void attention_dq_kernel(AttentionArgs a, unsigned total) {
     using L = Tile<T, DP>;
     constexpr int BM = 32 * WAVES, BN = kTileRows<T, WAVES>, NB = BN / 32;
-    TILE_PAIRS(ktile, vtile, BN * L::kPitch);
+    TILE_PAIRS(ktile, vtile, BN * L::kPitch, kStagesOf<WAVES>);
     const int wave = uniform((int)threadIdx.x / kWave), half = (threadIdx.x & (kWave - 1)) >> 5;
     const int D = (int)a.D;
     const RowReader<T, DP> rows;
@@ -623,7 +647,7 @@ __global__ __launch_bounds__(WAVES * kWave, (kQuerySide<T, DP, DIRECT>)) void at
                 fk.aim(KeyRows<T>{k, a.ldk, BN}, D, wave);
                 fv.aim(KeyRows<T>{v, a.ldv, BN}, D, wave);
                 __syncthreads();
-                walk<DIRECT>(
+                walk<DIRECT, kStagesOf<WAVES>>(
                     0, tiles,
                     [&](int t, int u) {
                         const int j = t * BN, left = q.keys - j;
@@ -872,8 +896,8 @@ __global__ __launch_bounds__(WAVES * kWave, (kKeySide<T, DP, DIRECT>)) void atte
     using K = KeySums<T, DP>;
     constexpr int BM = 32 * WAVES, BN = kTileRows<T, WAVES>, NB = BN / 32;
     constexpr bool kAhead = DIRECT && sizeof(T) == 2 && WAVES == 4 && DP > 64;
-    TILE_PAIRS(qtile, dtile, BN * L::kPitch);
-    TILE_PAIRS(lse_of, delta_of, kWave * 4);
+    TILE_PAIRS(qtile, dtile, BN * L::kPitch, kStagesOf<WAVES>);
+    TILE_PAIRS(lse_of, delta_of, kWave * 4, kStagesOf<WAVES>);
     const int wave = uniform((int)threadIdx.x / kWave);
     const int D = (int)a.D;
     const Runs runs(a.key_offsets, a.S, a.K, 1);
@@ -884,16 +908,15 @@ __global__ __launch_bounds__(WAVES * kWave, (kKeySide<T, DP, DIRECT>)) void atte
         const int hk = (int)(id - rest * heads), slot = (int)(rest / most), part = (int)((rest + slot) % most);
         const Slot s = find<BM>(runs, slot);
         if (s.tile >= s.tiles) continue;
-        int parts = 1;
         const int j0 = s.tile * BM + wave * 32, j = j0 + (threadIdx.x & 31);
-        const bool exists = j < s.rows;
+        const bool exists = j < s.rows, inside = s.run > 0 && s.run <= a.S;
+        const SeenBy by(a, s, s.tile * BM, BN);
+        const int parts = inside ? parts_of_tile(a, by.tiles, BN) : 1;
+        if (part >= parts) continue;
         K sums;
         sums.c = a.scale * kLog2e;
-        if (s.run > 0 && s.run <= a.S) {
-            const SeenBy by(a, s, s.tile * BM, BN);
+        if (inside) {
             const int mine_from = by.first(a, j), wave_from = by.first(a, j0), wave_full = by.first(a, j0 + 31);
-            parts = parts_of_tile(a, by.tiles, BN);
-            if (part >= parts) continue;
             const int per = (by.tiles + parts - 1) / parts;
             const int t0 = by.start + min(by.tiles, part * per), t1 = min(by.start + by.tiles, t0 + per);
             const int64_t key = (int64_t)s.row0 + min(j, s.rows - 1);
@@ -931,7 +954,7 @@ __global__ __launch_bounds__(WAVES * kWave, (kKeySide<T, DP, DIRECT>)) void atte
                     wait_copies<0>();
                 }
             } else {
-                walk<DIRECT>(
+                walk<DIRECT, kStagesOf<WAVES>>(
                     t0, t1, [&](int t, int u) { tiles.load(t, qtile[u], dtile[u], lse_of[u], delta_of[u]); },
                     [&](int u) { tiles.put(qtile[u], dtile[u], lse_of[u], delta_of[u]); },
                     [&](int t, int u) {
@@ -967,7 +990,7 @@ __global__ __launch_bounds__(WAVES * kWave, (kKeySide<T, DP, DIRECT>)) void atte
         if (exists && parts > 1) {
             if (a.dk) store_row<DIRECT>(a.partial_dk + shift + at, sums.dk, a.scale, D);
             if (a.dv) store_row<DIRECT>(a.partial_dv + shift + at, sums.dv, 1.0f, D);
-        } else if (exists && part == 0) {
+        } else if (exists) {
             if (a.dk) store_row<DIRECT>((T *)a.dk + at, sums.dk, a.scale, D);
             if (a.dv) store_row<DIRECT>((T *)a.dv + at, sums.dv, 1.0f, D);
         }
@@ -1022,7 +1045,8 @@ template <typename T, int DP, int WAVES, bool DIRECT>
 hipError_t forward_launch(const AttentionArgs &a, hipStream_t s) {
     const unsigned total = slots(a.R * a.G.d, a.S, 32 * WAVES) * (unsigned)(a.Hk * a.parts);
     const unsigned blocks = (unsigned)std::min<int64_t>(total, kMaxBlocks);
-    attention_kernel<T, DP, WAVES, DIRECT><<<blocks, WAVES * kWave, 0, s>>>(a, total);
+    if (WAVES == 1 && a.short_keys) attention_kernel<T, DP, WAVES, DIRECT, 1><<<blocks, WAVES * kWave, 0, s>>>(a, total);
+    else attention_kernel<T, DP, WAVES, DIRECT, 2><<<blocks, WAVES * kWave, 0, s>>>(a, total);
     return hipGetLastError();
 }
 

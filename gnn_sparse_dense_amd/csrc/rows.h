@@ -188,6 +188,7 @@ struct AttentionArgs {
     int64_t Hk;
     int64_t D;
     Divisor G;               // H / Hk
+    int short_keys;          // segments have few keys
     const void *q;           // [R, H, D], rows ldq elements apart
     const void *k;           // [K, Hk, D], ldk
     const void *v;           // [K, Hk, D], ldv
