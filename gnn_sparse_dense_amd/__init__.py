@@ -188,9 +188,9 @@ def _load() -> ctypes.CDLL:
         "spmm_layer_norm_workspace": [i64, i64, i32, pi64],
         "spmm_layer_norm_backward": [p, p, p, i32, p, p, p, p, p, i64, i64, i32, p, i64, p],
         "spmm_segment_attention_workspace": [i64] * 6 + [i32, pi64],
-        "spmm_segment_attention": heads + [p, p] + [i64] * 6 + [f64, i32, i32, p, i64, p],
+        "spmm_segment_attention": heads + [p, p, p] + [i64] * 6 + [f64, i32, i32, p, i64, p],
         "spmm_segment_attention_backward_workspace": [i64] * 6 + [i32, pi64],
-        "spmm_segment_attention_backward": heads + [p] * 6 + [i64] * 6 + [f64, i32, i32, p, i64, p],
+        "spmm_segment_attention_backward": heads + [p] * 7 + [i64] * 6 + [f64, i32, i32, p, i64, p],
         "spmm_dropout": [p, p, p, i64, f64, p, i64, i32, p],
         "spmm_linear_cross_entropy_workspace": [i64, i64, i64, i32, pi64, pi64, pi64],
         "spmm_linear_cross_entropy": [p, p, p, p, i64, i64, i64, i32, i32, p, i64, p, i64, p],

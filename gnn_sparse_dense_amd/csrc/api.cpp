@@ -2064,8 +2064,8 @@ SPMM_API int spmm_segment_attention_workspace(int64_t R, int64_t K, int64_t S, i
 }
 
 SPMM_API int spmm_segment_attention(const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv,
-                                    const int64_t *offsets, const int64_t *key_offsets, void *out, float *lse,
-                                    int64_t R, int64_t K, int64_t S, int64_t H, int64_t Hk, int64_t D, double scale,
+                                    const int64_t *offsets, const int64_t *key_offsets, void *out, void *rest,
+                                    float *lse, int64_t R, int64_t K, int64_t S, int64_t H, int64_t Hk, int64_t D, double scale,
                                     int causal, int type, void *workspace, int64_t workspace_bytes, void *stream) {
     if (const int st = check_attention(R, K, S, H, Hk, D, type)) return st;
     if (!((float)scale * 1.44269504f > 0.0f && std::isfinite((float)scale * 1.44269504f)))
@@ -2084,6 +2084,7 @@ SPMM_API int spmm_segment_attention(const void *q, int64_t ldq, const void *k, i
                                      {"k", k, rows_apart_bytes(K, ldk, Hk * D, size), (size_t)size, false},
                                      {"v", v, rows_apart_bytes(K, ldv, Hk * D, size), (size_t)size, false},
                                      {"out", out, R * H * D * size, (size_t)size, true},
+                                     {"rest", rest, rest ? R * H * D * size : 0, (size_t)size, true},
                                      {"lse", lse, lse ? R * H * 4 : 0, 4, true},
                                      {"workspace", workspace, need, 4, true}},
                                     &device))
@@ -2107,6 +2108,7 @@ SPMM_API int spmm_segment_attention(const void *q, int64_t ldq, const void *k, i
     a.scale = (float)scale;
     a.causal = causal != 0;
     a.out = out;
+    a.rest = rest;
     a.lse = lse;
     return launched(launch_attention(a, static_cast<float *>(workspace), type, reinterpret_cast<hipStream_t>(stream)),
                     "attention launch");
@@ -2122,8 +2124,8 @@ SPMM_API int spmm_segment_attention_backward_workspace(int64_t R, int64_t K, int
 
 SPMM_API int spmm_segment_attention_backward(const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v,
                                              int64_t ldv, const int64_t *offsets, const int64_t *key_offsets,
-                                             const void *out, const float *lse, const void *dout, void *dq, void *dk,
-                                             void *dv, int64_t R, int64_t K, int64_t S, int64_t H, int64_t Hk,
+                                             const void *out, const void *rest, const float *lse, const void *dout,
+                                             void *dq, void *dk, void *dv, int64_t R, int64_t K, int64_t S, int64_t H, int64_t Hk,
                                              int64_t D, double scale, int causal, int type, void *workspace,
                                              int64_t workspace_bytes, void *stream) {
     if (const int st = check_attention(R, K, S, H, Hk, D, type)) return st;
@@ -2144,6 +2146,7 @@ SPMM_API int spmm_segment_attention_backward(const void *q, int64_t ldq, const v
                                      {"k", k, rows_apart_bytes(K, ldk, Hk * D, size), (size_t)size, false},
                                      {"v", v, rows_apart_bytes(K, ldv, Hk * D, size), (size_t)size, false},
                                      {"out", out, queries, (size_t)size, false},
+                                     {"rest", rest, rest ? queries : 0, (size_t)size, false},
                                      {"lse", lse, R * H * 4, 4, false},
                                      {"dout", dout, queries, (size_t)size, false},
                                      {"dq", dq, dq ? queries : 0, (size_t)size, true},
@@ -2171,6 +2174,7 @@ SPMM_API int spmm_segment_attention_backward(const void *q, int64_t ldq, const v
     a.scale = (float)scale;
     a.causal = causal != 0;
     a.out = const_cast<void *>(out);
+    a.rest = const_cast<void *>(rest);
     a.lse = const_cast<float *>(lse);
     a.dout = dout;
     a.dq = dq;

@@ -316,6 +316,17 @@ __device__ inline void store_row(OUT *row, const f32x16 (&acc)[BLOCKS], float f,
         }
 }
 
+// What the rounding of out leaves off, for the backward pass: dout.out is subtracted
+// from every dout.v, where out's own rounding would weigh as much as ds's.
+template <bool WHOLE, typename T, int BLOCKS>
+__device__ inline void store_rest(T *row, f32x16 (&acc)[BLOCKS], float f, int D) {
+#pragma unroll
+    for (int b = 0; b < BLOCKS; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[b][i] = acc[b][i] * f - (float)(T)(acc[b][i] * f);
+    store_row<WHOLE>(row, acc, 1.0f, D);
+}
+
 // What both query-side kernels know of a tile of packed rows.
 template <typename T>
 struct Queries {
@@ -560,7 +571,9 @@ __global__ __launch_bounds__(WAVES * kWave, (kQuerySide<T, DP, DIRECT>)) void at
                 a.partial_sum[part * all + at] = sum;
             }
         } else if (q.exists()) {
-            store_row<DIRECT>((T *)a.out + at * D, acc, sum == 0.0f ? 0.0f : 1.0f / sum, D);
+            const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+            store_row<DIRECT>((T *)a.out + at * D, acc, f, D);
+            if (a.rest) store_rest<DIRECT>((T *)a.rest + at * D, acc, f, D);
             if (a.lse && half == 0) a.lse[at] = sum == 0.0f ? INFINITY : top + log2f(sum);
         }
     }
@@ -598,7 +611,11 @@ __global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttentionA
         const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-            if (lane + e * kWave < D) ((T *)a.out)[at * D + lane + e * kWave] = (T)(r[e] * f);
+            if (lane + e * kWave < D) {
+                const T v = (T)(r[e] * f);
+                ((T *)a.out)[at * D + lane + e * kWave] = v;
+                if (a.rest) ((T *)a.rest)[at * D + lane + e * kWave] = (T)(r[e] * f - (float)v);
+            }
         if (a.lse && lane == 0) a.lse[at] = sum == 0.0f ? INFINITY : top + log2f(sum);
     }
 }
@@ -630,12 +647,15 @@ __global__ __launch_bounds__(WAVES * kWave, (kQuerySide<T, DP, DIRECT>)) void at
         if (s.run > 0 && s.run <= a.S) {
             RowPacks<T, DP> mine, dout;
             load_row<T, DP, DIRECT>(dout, (const T *)a.dout + at * D, D, q.exists());
-            load_row<T, DP, DIRECT>(mine, (const T *)a.out + at * D, D, q.exists());
             float delta = 0.0f;
+            for (const void *part : {(const void *)a.out, (const void *)a.rest}) {
+                if (!part) break;
+                load_row<T, DP, DIRECT>(mine, (const T *)part + at * D, D, q.exists());
 #pragma unroll
-            for (int ks = 0; ks < L::kSteps; ++ks)
+                for (int ks = 0; ks < L::kSteps; ++ks)
 #pragma unroll
-                for (int e = 0; e < kPack<T>; ++e) delta = fmaf((float)dout[ks].v[e], (float)mine[ks].v[e], delta);
+                    for (int e = 0; e < kPack<T>; ++e) delta = fmaf((float)dout[ks].v[e], (float)mine[ks].v[e], delta);
+            }
             delta += other_half(delta);
             const float lse = q.exists() ? a.lse[at] : INFINITY;
             if (q.exists() && half == 0) a.delta[at] = delta;

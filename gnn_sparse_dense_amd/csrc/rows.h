@@ -196,6 +196,7 @@ struct AttentionArgs {
     float scale;
     int causal;
     void *out;               // [R, H, D] (backward: read)
+    void *rest;              // [R, H, D] or nullptr: what out's rounding leaves off
     float *lse;              // [R, H] or nullptr: base-2 logarithm of the sum of 2^score, scores in base 2;
                              // infinity where a row sees nothing
     int parts;               // of the keys; above 1:

@@ -485,14 +485,15 @@ struct Heads {
     int64_t S() const { return offsets.size(0) - 1; }
 };
 
-Tensor attended(const Heads &h, const Tensor &lse) {
+// rest and lse: what the backward pass reads, or undefined.
+Tensor attended(const Heads &h, const Tensor &rest, const Tensor &lse) {
     const int64_t R = h.q.size(0), H = h.q.size(1), D = h.q.size(2), K = h.k.size(0), Hk = h.k.size(1);
     int64_t bytes;
     check(spmm_segment_attention_workspace(R, K, h.S(), H, Hk, D, code(h.q), &bytes));
     const Tensor work = scratch(bytes, h.q), out = at::empty(h.q.sizes(), h.q.options());
     check(spmm_segment_attention(ptr(h.q), apart(h.q), ptr(h.k), apart(h.k), ptr(h.v), apart(h.v),
-                                 ptr<int64_t>(h.offsets), ptr<int64_t>(h.key_offsets), ptr(out), ptr<float>(lse), R, K,
-                                 h.S(), H, Hk, D, h.scale, h.causal, code(h.q), ptr(work), bytes, stream_of(h.q)));
+                                 ptr<int64_t>(h.offsets), ptr<int64_t>(h.key_offsets), ptr(out), ptr(rest),
+                                 ptr<float>(lse), R, K, h.S(), H, Hk, D, h.scale, h.causal, code(h.q), ptr(work), bytes, stream_of(h.q)));
     return out;
 }
 
@@ -501,8 +502,9 @@ struct SegmentAttention : torch::autograd::Function<SegmentAttention> {
         const Heads h = {rows_apart(q), rows_apart(k), rows_apart(v), given.offsets, given.key_offsets, given.causal,
                          given.scale};
         const Tensor lse = at::empty({q.size(0), q.size(1)}, q.options().dtype(at::kFloat));
-        const Tensor out = attended(h, lse);
-        ctx->save_for_backward({h.q, h.k, h.v, h.offsets, h.key_offsets, out, lse});
+        const Tensor rest = q.scalar_type() == at::kFloat ? Tensor() : at::empty(q.sizes(), q.options());
+        const Tensor out = attended(h, rest, lse);
+        ctx->save_for_backward({h.q, h.k, h.v, h.offsets, h.key_offsets, out, rest, lse});
         ctx->saved_data["causal"] = h.causal;
         ctx->saved_data["scale"] = h.scale;
         return out;
@@ -513,7 +515,7 @@ struct SegmentAttention : torch::autograd::Function<SegmentAttention> {
         const variable_list saved = ctx->get_saved_variables();
         const Heads h = {saved[0], saved[1], saved[2], saved[3], saved[4], ctx->saved_data["causal"].toBool(),
                          ctx->saved_data["scale"].toDouble()};
-        const Tensor &out = saved[5], &lse = saved[6], dout = grads[0].contiguous();
+        const Tensor &out = saved[5], &rest = saved[6], &lse = saved[7], dout = grads[0].contiguous();
         const int64_t R = h.q.size(0), H = h.q.size(1), D = h.q.size(2), K = h.k.size(0), Hk = h.k.size(1);
         Tensor dq, dk, dv;
         if (ctx->needs_input_grad(0)) dq = at::empty(h.q.sizes(), h.q.options());
@@ -523,7 +525,7 @@ struct SegmentAttention : torch::autograd::Function<SegmentAttention> {
         check(spmm_segment_attention_backward_workspace(R, K, h.S(), H, Hk, D, code(h.q), &bytes));
         const Tensor work = scratch(bytes, h.q);
         check(spmm_segment_attention_backward(ptr(h.q), apart(h.q), ptr(h.k), apart(h.k), ptr(h.v), apart(h.v),
-                                              ptr<int64_t>(h.offsets), ptr<int64_t>(h.key_offsets), ptr(out),
+                                              ptr<int64_t>(h.offsets), ptr<int64_t>(h.key_offsets), ptr(out), ptr(rest),
                                               ptr<float>(lse), ptr(dout), ptr(dq), ptr(dk), ptr(dv), R, K, h.S(), H,
                                               Hk, D, h.scale, h.causal, code(h.q), ptr(work), bytes, stream_of(h.q)));
         return once(grads, {dq, dk, dv, Tensor()}, {{0, 1, 2}, {0, 1, 2}, {0, 1, 2}});
@@ -557,7 +559,7 @@ Tensor segment_attention(const Tensor &q, const Tensor &k, const Tensor &v, cons
     }
     const double by = scale.value_or(1.0 / std::sqrt((double)q.size(2)));
     if (wants_grad(q, k, v)) return SegmentAttention::apply(q, k, v, Heads{{}, {}, {}, offsets, key_offsets, causal, by});
-    return attended({rows_apart(q), rows_apart(k), rows_apart(v), offsets, key_offsets, causal, by}, {});
+    return attended({rows_apart(q), rows_apart(k), rows_apart(v), offsets, key_offsets, causal, by}, {}, {});
 }
 
 // ---- dropout ----

@@ -250,22 +250,26 @@ def _check_heads(q, k, v, offsets, key_offsets):
     return (R, K, S, H, Hk, D), kind
 
 
-def spmm_segment_attention(q, k, v, offsets, key_offsets, out, lse=None, causal: bool = False, scale: float = 1.0) -> None:
+def spmm_segment_attention(q, k, v, offsets, key_offsets, out, lse=None, causal: bool = False, scale: float = 1.0,
+                           rest=None) -> None:
     """out [R, H, D] = attention of q [R, H, D] to k and v [K, Hk, D] within
-    the segments; lse (fp32 [R, H]) is what the backward pass reads."""
+    the segments; lse (fp32 [R, H]) and, of 16-bit rows, rest (as out: what its
+    rounding leaves off) are what the backward pass reads."""
     sizes, kind = _check_heads(q, k, v, offsets, key_offsets)
     R, K, S, H, Hk, D = sizes
     _check_tensor("out", out, (q.dtype,), q.shape, q.device)
     if lse is not None:
         _check_tensor("lse", lse, (torch.float32,), (R, H), q.device)
+    if rest is not None:
+        _check_tensor("rest", rest, (q.dtype,), q.shape, q.device)
     ws, at, n = _workspace(q.device, "spmm_segment_attention_workspace", *sizes, kind)
     _check(_lib.spmm_segment_attention(_ptr(q), H * D, _ptr(k), Hk * D, _ptr(v), Hk * D, _ptr(offsets),
-                                       _ptr(key_offsets), _ptr(out), _ptr(lse), *sizes, float(scale), int(causal),
-                                       kind, at, n, _current_stream(q)))
+                                       _ptr(key_offsets), _ptr(out), _ptr(rest), _ptr(lse), *sizes, float(scale),
+                                       int(causal), kind, at, n, _current_stream(q)))
 
 
 def spmm_segment_attention_backward(q, k, v, offsets, key_offsets, out, lse, dout, dq, dk, dv, causal: bool = False,
-                                    scale: float = 1.0) -> None:
+                                    scale: float = 1.0, rest=None) -> None:
     """Gradients of the attention; any of dq [R, H, D], dk and dv [K, Hk, D]
     may be None."""
     sizes, kind = _check_heads(q, k, v, offsets, key_offsets)
@@ -273,12 +277,14 @@ def spmm_segment_attention_backward(q, k, v, offsets, key_offsets, out, lse, dou
     _check_tensor("out", out, (q.dtype,), q.shape, q.device)
     _check_tensor("lse", lse, (torch.float32,), (R, H), q.device)
     _check_tensor("dout", dout, (q.dtype,), q.shape, q.device)
+    if rest is not None:
+        _check_tensor("rest", rest, (q.dtype,), q.shape, q.device)
     for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
         if t is not None:
             _check_tensor(name, t, (q.dtype,), like.shape, q.device)
     ws, at, n = _workspace(q.device, "spmm_segment_attention_backward_workspace", *sizes, kind)
     _check(_lib.spmm_segment_attention_backward(_ptr(q), H * D, _ptr(k), Hk * D, _ptr(v), Hk * D, _ptr(offsets),
-                                                _ptr(key_offsets), _ptr(out), _ptr(lse), _ptr(dout), _ptr(dq),
+                                                _ptr(key_offsets), _ptr(out), _ptr(rest), _ptr(lse), _ptr(dout), _ptr(dq),
                                                 _ptr(dk), _ptr(dv), *sizes, float(scale), int(causal), kind, at, n,
                                                 _current_stream(q)))
 

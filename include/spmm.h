@@ -570,9 +570,11 @@ int spmm_layer_norm_backward(const void *dy, const void *x, const void *weight, 
  * may reach all of the segment's rows, also those that do not see it).
  * Row r of q starts ldq >= H * D elements behind row r - 1, of k and v
  * ldk, ldv >= Hk * D; out and all gradients are packed.  lse (fp32 [R, H] or
- * NULL) is kept for
+ * NULL) and rest ([R, H, D] or NULL: what out's rounding to `type` leaves off)
+ * are kept for
  *   spmm_segment_attention_backward: dq, dk, dv (any may be NULL) from dout
- *   and the forward pass's out and lse.
+ *   and the forward pass's out, lse and rest (NULL: dq and dk take out as it
+ *   was rounded, which adds half as much to their error in 16 bits again).
  * Probabilities and their gradients are rounded to `type` where they enter a
  * matrix product; sums and softmax statistics are fp32.
  * scale > 0; D <= 128; R * H and K * Hk < 2^31 - 4097, S * Hk < 2^24,
@@ -581,14 +583,14 @@ int spmm_layer_norm_backward(const void *dy, const void *x, const void *weight, 
 int spmm_segment_attention_workspace(int64_t R, int64_t K, int64_t S, int64_t H, int64_t Hk, int64_t D, int type,
                                      int64_t *bytes);
 int spmm_segment_attention(const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv,
-                           const int64_t *offsets, const int64_t *key_offsets, void *out, float *lse, int64_t R,
-                           int64_t K, int64_t S, int64_t H, int64_t Hk, int64_t D, double scale, int causal, int type,
+                           const int64_t *offsets, const int64_t *key_offsets, void *out, void *rest, float *lse,
+                           int64_t R, int64_t K, int64_t S, int64_t H, int64_t Hk, int64_t D, double scale, int causal, int type,
                            void *workspace, int64_t workspace_bytes, void *stream);
 int spmm_segment_attention_backward_workspace(int64_t R, int64_t K, int64_t S, int64_t H, int64_t Hk, int64_t D,
                                               int type, int64_t *bytes);
 int spmm_segment_attention_backward(const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv,
                                     const int64_t *offsets, const int64_t *key_offsets, const void *out,
-                                    const float *lse, const void *dout, void *dq, void *dk, void *dv, int64_t R,
+                                    const void *rest, const float *lse, const void *dout, void *dq, void *dk, void *dv, int64_t R,
                                     int64_t K, int64_t S, int64_t H, int64_t Hk, int64_t D, double scale, int causal,
                                     int type, void *workspace, int64_t workspace_bytes, void *stream);
 
