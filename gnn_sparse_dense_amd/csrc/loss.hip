@@ -93,7 +93,7 @@ __global__ __launch_bounds__(kListThreads) void loss_list_kernel(LossArgs a, int
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         if (in[i]) a.rows[at++] = (int)(mine + i);
-        else if (a.row_loss && mine + i < a.R) a.row_loss[mine + i] = 0.0f;
+        else if (a.per_row && mine + i < a.R) a.row_loss[mine + i] = 0.0f;
     }
     if (blockIdx.x == blocks - 1 && threadIdx.x == 0) *a.count = before + all;
 }
@@ -293,7 +293,7 @@ __global__ __launch_bounds__(kJoinThreads) void loss_join_kernel(LossArgs a, int
                 loss = (top - a.picked[r]) + logf(sum);
                 a.stats[r] = top;
                 a.stats[a.R + r] = 1.0f / sum;
-                if (a.row_loss) a.row_loss[a.rows[r]] = loss;
+                if (a.per_row) a.row_loss[a.rows[r]] = loss;
             }
             if (a.block_loss) {
 #pragma unroll
@@ -778,7 +778,7 @@ hipError_t launch_loss(const LossArgs &args, void *state, void *workspace, int t
     a.tile_sum = a.tile_top + tiles;
     a.picked = a.tile_sum + tiles;
     a.block_count = reinterpret_cast<int *>(a.picked + a.R);
-    if (!a.row_loss) a.block_loss = a.picked + a.R + std::max<int64_t>(1, tiles_of(a.R, kListRows));
+    if (!a.per_row) a.block_loss = a.picked + a.R + std::max<int64_t>(1, tiles_of(a.R, kListRows));
     if (type == SPMM_F32) return forward<float>(a, s);
     if (type == SPMM_BF16) return forward<__bf16>(a, s);
     return forward<_Float16>(a, s);
