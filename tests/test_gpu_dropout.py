@@ -5,11 +5,11 @@ import torch
 pytestmark = pytest.mark.gpu
 
 from tests import rows64  # noqa: E402
+from tests.test_gpu_rows import TYPES, close, guarded, normal, rng  # noqa: E402
 
 if torch.cuda.is_available():
     import gnn_sparse_dense_amd as G
     from tests.gpu_helpers import DEV, log
-    from tests.test_gpu_rows import TYPES, close, guarded, normal, rng
 
 SEEDS = [0, 1, -1, 2 ** 62 + 12345, -2 ** 63]
 

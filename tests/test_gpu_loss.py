@@ -6,12 +6,12 @@ import torch
 pytestmark = pytest.mark.gpu
 
 from tests import rows64  # noqa: E402
+from tests.test_gpu_attention import SLACK, close  # noqa: E402
+from tests.test_gpu_rows import TYPES, guarded, half_step, normal, rng  # noqa: E402
 
 if torch.cuda.is_available():
     import gnn_sparse_dense_amd as G
     from tests.gpu_helpers import DEV, log
-    from tests.test_gpu_attention import SLACK, close
-    from tests.test_gpu_rows import TYPES, guarded, half_step, normal, rng
 
 
 def case(R, I, V, dtype, drop=0.2, seed=0):
