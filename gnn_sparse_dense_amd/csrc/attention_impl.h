@@ -519,6 +519,14 @@ __global__ __launch_bounds__(WAVES * kWave, (kQuerySide<T, DP, DIRECT>)) void at
                     for (int ks = 0; ks < L::kSteps; ++ks)
 #pragma unroll
                         for (int b = 0; b < NB; ++b) multiply<T>(mine[ks], rows.read(ktile[u], b, ks), sc[b]);
+                    if constexpr (sizeof(T) == 2) {      // four reads ahead of the products
+                        __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+#pragma unroll
+                        for (int i = 0; i < L::kSteps * NB; ++i) {
+                            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                        }
+                    }
                     if (j0 + BN > q.seen_least) {
 #pragma unroll
                         for (int b = 0; b < NB; ++b)
@@ -579,44 +587,39 @@ __global__ __launch_bounds__(WAVES * kWave, (kQuerySide<T, DP, DIRECT>)) void at
     }
 }
 
-// Joins the parts of a row, a wave to a row and head.
+// Joins the parts of the rows, four elements of one to a lane.
 constexpr int kJoinThreads = 256;
 
 template <typename T>
 __global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttentionArgs a) {
-    const int lane = threadIdx.x & (kWave - 1), D = (int)a.D;
+    const int D = (int)a.D, quads = (D + 3) / 4;
     const int64_t all = a.R * a.H;
-    for (int64_t at = (int64_t)blockIdx.x * (kJoinThreads / kWave) + threadIdx.x / kWave; at < all;
-         at += (int64_t)gridDim.x * (kJoinThreads / kWave)) {
-        // a lane takes a part's statistics
-        const bool has = lane < a.parts;
-        const float mine = has ? a.partial_sum[lane * all + at] : 0.0f;
-        const float at_top = has && mine != 0.0f ? a.partial_top[lane * all + at] : -INFINITY;
-        float top = at_top;
-#pragma unroll
-        for (int o = kWave / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, kWave));
-        const float weight = at_top == -INFINITY && mine == 0.0f ? 0.0f : exp2_of(at_top - top);
-        float sum = mine * weight;
-#pragma unroll
-        for (int o = kWave / 2; o > 0; o >>= 1) sum += __shfl_xor(sum, o, kWave);
-        float r[2] = {0.0f, 0.0f};
+    for (int64_t i = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x; i < all * quads;
+         i += (int64_t)gridDim.x * kJoinThreads) {
+        const int64_t at = i / quads;
+        const int d = (int)(i - at * quads) * 4;
+        float top = -INFINITY, sum = 0.0f, r[4] = {};
         for (int p = 0; p < a.parts; ++p) {
-            const float w = __shfl(weight, p, kWave);
-            if (__shfl(mine, p, kWave) == 0.0f) continue;
-            const float *from = a.partial + (p * all + at) * D;
+            const float mine = a.partial_sum[p * all + at];
+            if (mine == 0.0f) continue;                  // a part that sees nothing holds nothing
+            const float mine_top = a.partial_top[p * all + at], next = fmaxf(top, mine_top);
+            const float from = next == -INFINITY ? 0.0f : next;
+            const float kept = exp2_of(top - from), weight = exp2_of(mine_top - from);
+            const Pack<float> v = load_pack(a.partial + (p * all + at) * D + d, D - d);
+            sum = fmaf(sum, kept, mine * weight);
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-                if (lane + e * kWave < D) r[e] = fmaf(w, from[lane + e * kWave], r[e]);
+            for (int e = 0; e < 4; ++e) r[e] = fmaf(r[e], kept, v.v[e] * weight);
+            top = next;
         }
         const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-            if (lane + e * kWave < D) {
+        for (int e = 0; e < 4; ++e)
+            if (d + e < D) {
                 const T v = (T)(r[e] * f);
-                ((T *)a.out)[at * D + lane + e * kWave] = v;
-                if (a.rest) ((T *)a.rest)[at * D + lane + e * kWave] = (T)(r[e] * f - (float)v);
+                ((T *)a.out)[at * D + d + e] = v;
+                if (a.rest) ((T *)a.rest)[at * D + d + e] = (T)(r[e] * f - (float)v);
             }
-        if (a.lse && lane == 0) a.lse[at] = sum == 0.0f ? INFINITY : top + log2f(sum);
+        if (a.lse && d == 0) a.lse[at] = sum == 0.0f ? INFINITY : top + log2f(sum);
     }
 }
 
@@ -952,25 +955,29 @@ __global__ __launch_bounds__(WAVES * kWave, (kKeySide<T, DP, DIRECT>)) void atte
                     wait_copies<0>();
                     load(t0 + 1, 1);
                     sums.read(q, qtile[0], 0);
-                    for (int t = t0; t < t1; t += 2) {
+                    auto tile = [&](int t, int u) {
 #pragma unroll
-                        for (int i = 0; i < 2 * NB; ++i) {
-                            const int u = i / NB, b = i % NB, m0 = (t + u) * BN + b * 32;
-                            if (b == 0 && t + u >= t1) break;
-                            auto ahead = [&] {
-                                if (b == NB - 1) {
-                                    // this tile is read out, and the next one here
-                                    wait_copies<0>();
-                                    load(t + u + 2, u);
-                                    sums.read(q, qtile[1 - u], 0);
-                                } else {
-                                    sums.read(q, qtile[u], b + 1);
-                                }
-                            };
+                        for (int b = 0; b < NB; ++b) {
+                            const int m0 = t * BN + b * 32;
                             sums.block(q, qtile[u], dtile[u], lse_of[u], delta_of[u], b, m0 < wave_full, m0, mine_from,
-                                       ahead);
+                                       [&] {
+                                           if (b == NB - 1) {
+                                               // this tile is read out, and the next one here
+                                               wait_copies<0>();
+                                               load(t + 2, u);
+                                               sums.read(q, qtile[1 - u], 0);
+                                           } else {
+                                               sums.read(q, qtile[u], b + 1);
+                                           }
+                                       });
                         }
+                    };
+                    int t = t0;
+                    for (; t + 1 < t1; t += 2) {
+                        tile(t, 0);
+                        tile(t + 1, 1);
                     }
+                    if (t < t1) tile(t, 0);
                     wait_copies<0>();
                 }
             } else {
@@ -1065,8 +1072,13 @@ template <typename T, int DP, int WAVES, bool DIRECT>
 hipError_t forward_launch(const AttentionArgs &a, hipStream_t s) {
     const unsigned total = slots(a.R * a.G.d, a.S, 32 * WAVES) * (unsigned)(a.Hk * a.parts);
     const unsigned blocks = (unsigned)std::min<int64_t>(total, kMaxBlocks);
-    if (WAVES == 1 && a.short_keys) attention_kernel<T, DP, WAVES, DIRECT, 1><<<blocks, WAVES * kWave, 0, s>>>(a, total);
-    else attention_kernel<T, DP, WAVES, DIRECT, 2><<<blocks, WAVES * kWave, 0, s>>>(a, total);
+    if constexpr (WAVES == 1) {
+        if (a.short_keys) {
+            attention_kernel<T, DP, WAVES, DIRECT, 1><<<blocks, WAVES * kWave, 0, s>>>(a, total);
+            return hipGetLastError();
+        }
+    }
+    attention_kernel<T, DP, WAVES, DIRECT, 2><<<blocks, WAVES * kWave, 0, s>>>(a, total);
     return hipGetLastError();
 }
 
@@ -1111,7 +1123,7 @@ hipError_t launch_attention_pass(const AttentionArgs &a, AttentionPass pass, boo
 
 template <typename T>
 hipError_t launch_attention_join(const AttentionArgs &a, hipStream_t s) {
-    const int64_t waves = kJoinThreads / kWave, blocks = (a.R * a.H + waves - 1) / waves;
+    const int64_t blocks = (a.R * a.H * ((a.D + 3) / 4) + kJoinThreads - 1) / kJoinThreads;
     attention_join_kernel<T><<<(unsigned)std::min(blocks, kMaxBlocks), kJoinThreads, 0, s>>>(a);
     return hipGetLastError();
 }
