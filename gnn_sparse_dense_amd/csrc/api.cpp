@@ -2059,7 +2059,7 @@ SPMM_API int spmm_segment_attention_workspace(int64_t R, int64_t K, int64_t S, i
                                               int type, int64_t *bytes) {
     if (!bytes) return fail(SPMM_E_INVALID_ARG, "output is NULL");
     if (const int st = check_attention(R, K, S, H, Hk, D, type)) return st;
-    *bytes = attention_workspace_floats(R, K, S, H, Hk, D) * (int64_t)sizeof(float);
+    *bytes = attention_workspace_floats(R, K, S, H, Hk, D, type) * (int64_t)sizeof(float);
     return succeed();
 }
 
@@ -2073,7 +2073,7 @@ SPMM_API int spmm_segment_attention(const void *q, int64_t ldq, const void *k, i
     if (const int st = check_rows_apart("ldq", ldq, H, D)) return st;
     if (const int st = check_rows_apart("ldk", ldk, Hk, D)) return st;
     if (const int st = check_rows_apart("ldv", ldv, Hk, D)) return st;
-    const int64_t need = attention_workspace_floats(R, K, S, H, Hk, D) * (int64_t)sizeof(float);
+    const int64_t need = attention_workspace_floats(R, K, S, H, Hk, D, type) * (int64_t)sizeof(float);
     if (const int st = check_workspace(need, workspace_bytes)) return st;
     if (R == 0) return succeed();
     const int64_t size = type_size(type);
@@ -2118,7 +2118,7 @@ SPMM_API int spmm_segment_attention_backward_workspace(int64_t R, int64_t K, int
                                                        int64_t D, int type, int64_t *bytes) {
     if (!bytes) return fail(SPMM_E_INVALID_ARG, "output is NULL");
     if (const int st = check_attention(R, K, S, H, Hk, D, type)) return st;
-    *bytes = attention_backward_workspace_floats(R, K, S, H, Hk, D) * (int64_t)sizeof(float);
+    *bytes = attention_backward_workspace_floats(R, K, S, H, Hk, D, type) * (int64_t)sizeof(float);
     return succeed();
 }
 
@@ -2135,7 +2135,7 @@ SPMM_API int spmm_segment_attention_backward(const void *q, int64_t ldq, const v
     if (const int st = check_rows_apart("ldk", ldk, Hk, D)) return st;
     if (const int st = check_rows_apart("ldv", ldv, Hk, D)) return st;
     if (!dq && !dk && !dv) return fail(SPMM_E_INVALID_ARG, "dq, dk and dv are all NULL");
-    const int64_t need = attention_backward_workspace_floats(R, K, S, H, Hk, D) * (int64_t)sizeof(float);
+    const int64_t need = attention_backward_workspace_floats(R, K, S, H, Hk, D, type) * (int64_t)sizeof(float);
     if (const int st = check_workspace(need, workspace_bytes)) return st;
     if (R == 0 && K == 0) return succeed();
     const int64_t size = type_size(type), queries = R * H * D * size, keys = K * Hk * D * size;

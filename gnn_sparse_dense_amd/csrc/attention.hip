@@ -29,21 +29,28 @@ bool direct_rows(const void *p, int64_t ld, int64_t D, int size) {
 }
 
 // Tiles of 128 rows by four waves that share their keys, or of 32 by one: by the
-// mean length of a segment, since the device alone knows each.
-bool large_tiles(int64_t rows, int64_t S) { return rows > 64 * S; }
+// mean length of a segment, since the device alone knows each.  With gradients, 8
+// heads, four waves and one: bf16, 64 elements, 256 segments of 64 rows 111 and 92 us,
+// 128 of 128 117 and 102, of 256 216 and 222; 128 elements 227 and 174, 244 and 205, 506
+// and 575; fp32, 32 elements 159 and 121, 208 and 171, 512 and 452.
+bool large_tiles(int64_t rows, int64_t S, int size) { return rows > (size == 4 ? 256 : 128) * S; }
 
-// Parts of a segment's keys (rows) that are worked on side by side and joined
-// afterwards, where there are too few tiles to fill the chip: about `want` blocks,
-// at least 256 keys (rows) to a part of a segment of mean length.
-int64_t parts_of(int64_t blocks, int64_t want, int64_t length, int64_t S, int64_t most) {
-    return std::max<int64_t>(1, std::min({want / std::max<int64_t>(1, blocks), length / std::max<int64_t>(1, S) / 256, most}));
+// Parts of a segment's keys that are worked on side by side and joined afterwards,
+// where there are too few tiles to fill the chip: about `want` blocks, at least
+// `least` keys to a part of a segment of mean length.  One row each, 32 heads of 128
+// over 8, bf16: 4 segments of 8,000 keys, 256 to a part 37 us, 128 43, 512 39; 32 of
+// 1,000 33, 37 and 47; one of 65,536, at most 64 parts 59 us, 128 66, 256 88.  128-row
+// tiles: 3,001 rows to 5,003 keys in 9, 256 keys to a part 30 us, 512 (one part) 27.
+int64_t parts_of(int64_t blocks, int64_t want, int64_t keys, int64_t S, int64_t least) {
+    const int64_t length = keys / std::max<int64_t>(1, S);
+    return std::max<int64_t>(1, std::min({want / std::max<int64_t>(1, blocks), length / least, int64_t(64)}));
 }
 
 int64_t tiles(int64_t rows, int64_t S, bool large) { return rows / (large ? 128 : 32) + std::min(rows, S); }
 
-int query_parts(int64_t R, int64_t K, int64_t S, int64_t H, int64_t Hk) {
-    const bool large = large_tiles(R * (H / Hk), S);
-    return (int)parts_of(tiles(R * (H / Hk), S, large) * Hk, large ? 512 : 2048, K, S, 64);
+int query_parts(int64_t R, int64_t K, int64_t S, int64_t H, int64_t Hk, int size) {
+    const bool large = large_tiles(R * (H / Hk), S, size);
+    return (int)parts_of(tiles(R * (H / Hk), S, large) * Hk, large ? 512 : 2048, K, S, large ? 512 : 256);
 }
 
 // Packed rows of a part of a key tile's rows: a third of what a compute unit has to
@@ -52,26 +59,27 @@ int query_parts(int64_t R, int64_t K, int64_t S, int64_t H, int64_t Hk) {
 constexpr int64_t kUnits = 256;
 constexpr int kMostParts = 16;
 
-int64_t part_rows(int64_t R, int64_t K, int64_t S, int64_t H, int64_t Hk) {
+int64_t part_rows(int64_t R, int64_t K, int64_t S, int64_t H, int64_t Hk, int size) {
     const int64_t rows = R * (H / Hk) / std::max<int64_t>(1, S);
-    const int64_t share = tiles(K, S, large_tiles(K, S)) * Hk * rows / (3 * kUnits);
+    const int64_t share = tiles(K, S, large_tiles(K, S, size)) * Hk * rows / (3 * kUnits);
     return std::max<int64_t>(512, share);
 }
 
-int key_parts(int64_t R, int64_t K, int64_t S, int64_t H, int64_t Hk) {
+int key_parts(int64_t R, int64_t K, int64_t S, int64_t H, int64_t Hk, int size) {
     const int64_t rows = R * (H / Hk) / std::max<int64_t>(1, S);      // the longest segment's are taken to be thrice the mean
-    return (int)std::max<int64_t>(1, std::min<int64_t>(kMostParts, 3 * rows / part_rows(R, K, S, H, Hk)));
+    return (int)std::max<int64_t>(1, std::min<int64_t>(kMostParts, 3 * rows / part_rows(R, K, S, H, Hk, size)));
 }
 
 }  // namespace
 
-int64_t attention_workspace_floats(int64_t R, int64_t K, int64_t S, int64_t H, int64_t Hk, int64_t D) {
-    const int64_t parts = query_parts(R, K, S, H, Hk);
+int64_t attention_workspace_floats(int64_t R, int64_t K, int64_t S, int64_t H, int64_t Hk, int64_t D, int type) {
+    const int64_t parts = query_parts(R, K, S, H, Hk, type == SPMM_F32 ? 4 : 2);
     return parts > 1 ? parts * R * H * (D + 2) : 0;
 }
 
-int64_t attention_backward_workspace_floats(int64_t R, int64_t K, int64_t S, int64_t H, int64_t Hk, int64_t D) {
-    const int64_t parts = key_parts(R, K, S, H, Hk);
+int64_t attention_backward_workspace_floats(int64_t R, int64_t K, int64_t S, int64_t H, int64_t Hk, int64_t D,
+                                            int type) {
+    const int64_t parts = key_parts(R, K, S, H, Hk, type == SPMM_F32 ? 4 : 2);
     return R * H + (parts > 1 ? 2 * parts * K * Hk * D : 0);
 }
 
@@ -80,13 +88,13 @@ hipError_t launch_attention(const AttentionArgs &args, float *workspace, int typ
     AttentionArgs a = args;
     const int size = type == SPMM_F32 ? 4 : 2;
     a.G = divisor(a.H / a.Hk);
-    a.parts = query_parts(a.R, a.K, a.S, a.H, a.Hk);
+    a.parts = query_parts(a.R, a.K, a.S, a.H, a.Hk, size);
     if (a.parts > 1) {
         a.partial = workspace;
         a.partial_top = workspace + a.parts * a.R * a.H * a.D;
         a.partial_sum = a.partial_top + a.parts * a.R * a.H;
     }
-    const bool large = large_tiles(a.R * a.G.d, a.S);
+    const bool large = large_tiles(a.R * a.G.d, a.S, size);
     a.short_keys = a.K <= 64 * a.S;
     const bool direct = direct_rows(a.k, a.ldk, a.D, size) && direct_rows(a.v, a.ldv, a.D, size);
     const auto pass = AttentionPass::kForward;
@@ -105,8 +113,8 @@ hipError_t launch_attention_backward(const AttentionArgs &args, float *workspace
     const int size = type == SPMM_F32 ? 4 : 2;
     a.G = divisor(a.H / a.Hk);
     a.parts = 1;
-    a.key_parts = key_parts(a.R, a.K, a.S, a.H, a.Hk);
-    a.part_rows = part_rows(a.R, a.K, a.S, a.H, a.Hk) / (a.causal ? 2 : 1);
+    a.key_parts = key_parts(a.R, a.K, a.S, a.H, a.Hk, size);
+    a.part_rows = part_rows(a.R, a.K, a.S, a.H, a.Hk, size) / (a.causal ? 2 : 1);
     a.delta = workspace;
     a.partial_dk = workspace + a.R * a.H;
     a.partial_dv = a.partial_dk + a.key_parts * a.K * a.Hk * a.D;
@@ -117,15 +125,15 @@ hipError_t launch_attention_backward(const AttentionArgs &args, float *workspace
     };
     if (a.R > 0) {
         const bool direct = direct_rows(a.k, a.ldk, a.D, size) && direct_rows(a.v, a.ldv, a.D, size);
-        if (const hipError_t e = pass(AttentionPass::kQueries, large_tiles(a.R * a.G.d, a.S), direct)) return e;
+        if (const hipError_t e = pass(AttentionPass::kQueries, large_tiles(a.R * a.G.d, a.S, size), direct)) return e;
     }
     if (a.K == 0 || (!a.dk && !a.dv)) return hipSuccess;
     const bool direct = direct_rows(a.q, a.ldq, a.D, size) && direct_rows(a.dout, a.H * a.D, a.D, size);
-    if (const hipError_t e = pass(AttentionPass::kKeys, large_tiles(a.K, a.S), direct)) return e;
+    if (const hipError_t e = pass(AttentionPass::kKeys, large_tiles(a.K, a.S, size), direct)) return e;
     if (a.key_parts == 1) return hipSuccess;
-    return type == SPMM_F32    ? launch_attention_add<float>(a, large_tiles(a.K, a.S), s)
-           : type == SPMM_BF16 ? launch_attention_add<__bf16>(a, large_tiles(a.K, a.S), s)
-                               : launch_attention_add<_Float16>(a, large_tiles(a.K, a.S), s);
+    return type == SPMM_F32    ? launch_attention_add<float>(a, large_tiles(a.K, a.S, size), s)
+           : type == SPMM_BF16 ? launch_attention_add<__bf16>(a, large_tiles(a.K, a.S, size), s)
+                               : launch_attention_add<_Float16>(a, large_tiles(a.K, a.S, size), s);
 }
 
 }  // namespace gspmm

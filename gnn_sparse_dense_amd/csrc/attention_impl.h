@@ -598,18 +598,18 @@ __global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttentionA
          i += (int64_t)gridDim.x * kJoinThreads) {
         const int64_t at = i / quads;
         const int d = (int)(i - at * quads) * 4;
+        // a part that sees nothing has the maximum -infinity and zeros
         float top = -INFINITY, sum = 0.0f, r[4] = {};
+#pragma unroll 8
+        for (int p = 0; p < a.parts; ++p) top = fmaxf(top, a.partial_top[p * all + at]);
+        const float from = top == -INFINITY ? 0.0f : top;
+#pragma unroll 8
         for (int p = 0; p < a.parts; ++p) {
-            const float mine = a.partial_sum[p * all + at];
-            if (mine == 0.0f) continue;                  // a part that sees nothing holds nothing
-            const float mine_top = a.partial_top[p * all + at], next = fmaxf(top, mine_top);
-            const float from = next == -INFINITY ? 0.0f : next;
-            const float kept = exp2_of(top - from), weight = exp2_of(mine_top - from);
+            const float weight = exp2_of(a.partial_top[p * all + at] - from);
             const Pack<float> v = load_pack(a.partial + (p * all + at) * D + d, D - d);
-            sum = fmaf(sum, kept, mine * weight);
+            sum = fmaf(a.partial_sum[p * all + at], weight, sum);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) r[e] = fmaf(r[e], kept, v.v[e] * weight);
-            top = next;
+            for (int e = 0; e < 4; ++e) r[e] = fmaf(v.v[e], weight, r[e]);
         }
         const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll

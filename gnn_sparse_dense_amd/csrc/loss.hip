@@ -252,7 +252,7 @@ __global__ __launch_bounds__(S::kThreads, 2) void loss_logits_kernel(LossArgs a,
 
 constexpr int kJoinThreads = 256, kJoinRows = 32;
 
-// Rows of a block: 32, or 8 where a row has many tiles (128 for 64 rows: 11 -> 5 us).
+// Rows of a block: 32, or 8 where a row has many tiles (256 tiles of 64 rows: 11 -> 5 us).
 int join_rows(int tiles) { return tiles > 32 ? 8 : kJoinRows; }
 
 // Joins the column tiles of ROWS rows, 256 / ROWS tiles at a time.
@@ -329,16 +329,33 @@ __global__ __launch_bounds__(kTotalThreads) void loss_total_kernel(LossArgs a, i
 
 // ---- backward ----
 
-// The power of two above the largest gradient of a row (1 where all are zero).
+// The power of two above the largest gradient of a row (1 where all are zero): the
+// blocks' largest, and theirs where there is more than one block.
+constexpr int kUnitRows = 16384;
+constexpr int64_t kUnitBlocks = 1024;
+
+__device__ inline void store_unit(const LossArgs &a, float most) {
+    *a.unit = most > 0.0f ? ldexpf(1.0f, min(max(ilogbf(most) + 1, -120), 120)) : 1.0f;
+}
+
 __global__ __launch_bounds__(kTotalThreads) void loss_unit_kernel(LossArgs a) {
     const int64_t count = *a.count;
     float most = 0.0f;
-    for (int64_t r = threadIdx.x; r < count; r += kTotalThreads) {
+#pragma unroll 4
+    for (int64_t r = (int64_t)blockIdx.x * kTotalThreads + threadIdx.x; r < count; r += (int64_t)gridDim.x * kTotalThreads) {
         const float g = fabsf(a.dloss[a.rows[r]]);
         most = g <= 3.0e38f ? fmaxf(most, g) : most;     // infinities and NaN: theirs alone
     }
     most = block_all(most, [](float x, float y) { return fmaxf(x, y); });
-    if (threadIdx.x == 0) *a.unit = most > 0.0f ? ldexpf(1.0f, min(max(ilogbf(most) + 1, -120), 120)) : 1.0f;
+    if (threadIdx.x) return;
+    if (gridDim.x > 1) a.unit[1 + blockIdx.x] = most;
+    else store_unit(a, most);
+}
+
+__global__ __launch_bounds__(kTotalThreads) void loss_unit_join_kernel(LossArgs a, int blocks) {
+    const float most = block_all((int)threadIdx.x < blocks ? a.unit[1 + threadIdx.x] : 0.0f,
+                                 [](float x, float y) { return fmaxf(x, y); });
+    if (threadIdx.x == 0) store_unit(a, most);
 }
 
 // x's listed rows next to each other, where some are left out.
@@ -613,24 +630,27 @@ hipError_t dw_launch(const LossArgs &a, int64_t v0, int64_t N, int64_t chunk, hi
     return hipGetLastError();
 }
 
-// Rows off 16 bytes are moved to whole ones first where the products outweigh the
-// copy of w: kPadRows rows.
-constexpr int64_t kPadRows = 256;
+// Rows off 16 bytes are moved to whole ones first where the products (R V) outweigh
+// the copies (R + V) by kPadGain.  1001 elements, fp16, 50,000 classes, with gradients:
+// 256 rows 420 us moved and 366 as they are, 512 567 and 555, 1,024 761 and 934; 50
+// classes, 30,000 rows of 101 91 and 60.
+constexpr int64_t kPadGain = 512;
 
-int64_t padded_width(int64_t R, int64_t I, int size) {
+int64_t padded_width(int64_t R, int64_t I, int64_t V, int size) {
     const int64_t ld = whole(I, 16 / size);
-    return ld != I && R > kPadRows && R * ld * size < (int64_t(1) << 31) && 320 * ld * size < (int64_t(1) << 31) ? ld : I;
+    const bool gains = R * V > kPadGain * (R + V);
+    return ld != I && gains && R * ld * size < (int64_t(1) << 31) && 320 * ld * size < (int64_t(1) << 31) ? ld : I;
 }
 
 // Bytes of both moved arrays, x first.
 int64_t padded_bytes(int64_t R, int64_t I, int64_t V, int size) {
-    const int64_t ld = padded_width(R, I, size);
+    const int64_t ld = padded_width(R, I, V, size);
     return ld == I ? 0 : whole(R * ld * size, 256) + whole(V * ld * size, 256);
 }
 
 template <typename T>
 hipError_t pad(LossArgs &a, hipStream_t s) {
-    a.ld = padded_width(a.R, a.I, sizeof(T));
+    a.ld = padded_width(a.R, a.I, a.V, sizeof(T));
     if (a.ld == a.I) return hipSuccess;
     T *x = (T *)a.padded, *w = x + whole(a.R * a.ld * sizeof(T), 256) / sizeof(T);
     auto blocks = [&](int64_t rows) {
@@ -673,7 +693,11 @@ hipError_t backward(const LossArgs &args, hipStream_t s) {
     if (const hipError_t e = pad<T>(a, s)) return e;
     const bool direct = direct_rows(a.x, a.R, a.ld, size) && direct_rows(a.w, 320, a.ld, size) &&
                         direct_rows(nullptr, 320, a.ldd, size);
-    if (a.per_row) loss_unit_kernel<<<1, kTotalThreads, 0, s>>>(a);
+    if (a.per_row) {
+        const int blocks = (int)std::max<int64_t>(1, std::min(kUnitBlocks, a.R / kUnitRows));
+        loss_unit_kernel<<<(unsigned)blocks, kTotalThreads, 0, s>>>(a);
+        if (blocks > 1) loss_unit_join_kernel<<<1, kTotalThreads, 0, s>>>(a, blocks);
+    }
     const int64_t packs = a.R * tiles_of(a.ld, kPack<T>);
     const unsigned pack_blocks = (unsigned)std::min(std::max<int64_t>(1, packs / kPackThreads), int64_t(1) << 14);
     if (a.dw) loss_pack_kernel<T><<<pack_blocks, kPackThreads, 0, s>>>(a);
@@ -741,6 +765,8 @@ static void state_arrays(LossArgs &a, void *state) {
     a.count = reinterpret_cast<int64_t *>(static_cast<char *>(state) + whole(3 * a.R * 4, 8));
 }
 
+constexpr int64_t kUnitBytes = (kUnitBlocks + 64) * 4;       // the unit, and the blocks' largest gradients
+
 struct BackwardSizes {
     int64_t d, packed, dx_sum, dw_partial, padded;       // bytes, each whole 256s
 };
@@ -749,7 +775,7 @@ static BackwardSizes backward_sizes(int64_t R, int64_t I, int64_t V, int size) {
     const int64_t piece = piece_of(R, V, size);
     BackwardSizes b;
     b.d = whole(R * piece * size, 256);
-    b.packed = whole(R * padded_width(R, I, size) * size, 256);
+    b.packed = whole(R * padded_width(R, I, V, size) * size, 256);
     b.padded = padded_bytes(R, I, V, size);
     // the addresses are not known here: what either way of staging needs
     const int64_t parts = std::max(dx_shape(R, I, std::min(piece, V), size, true).parts,
@@ -765,7 +791,7 @@ static BackwardSizes backward_sizes(int64_t R, int64_t I, int64_t V, int size) {
 
 int64_t loss_backward_workspace_bytes(int64_t R, int64_t I, int64_t V, int type) {
     const BackwardSizes b = backward_sizes(R, I, V, type == SPMM_F32 ? 4 : 2);
-    return 256 + 256 + b.d + b.packed + b.dx_sum + b.dw_partial + b.padded;      // room to start on 256 bytes, and the unit
+    return 256 + kUnitBytes + b.d + b.packed + b.dx_sum + b.dw_partial + b.padded;      // room to start on 256 bytes
 }
 
 hipError_t launch_loss(const LossArgs &args, void *state, void *workspace, int type, hipStream_t s) {
@@ -790,7 +816,7 @@ hipError_t launch_loss_backward(const LossArgs &args, const void *state, void *w
     const BackwardSizes b = backward_sizes(a.R, a.I, a.V, type == SPMM_F32 ? 4 : 2);
     char *at = reinterpret_cast<char *>(whole((int64_t)(uintptr_t)workspace, 256));
     a.unit = reinterpret_cast<float *>(at);
-    a.d = at += 256;
+    a.d = at += kUnitBytes;
     a.packed = at += b.d;
     a.dx_sum = reinterpret_cast<float *>(at += b.packed);
     a.dw_partial = reinterpret_cast<float *>(at += b.dx_sum);

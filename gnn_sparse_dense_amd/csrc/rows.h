@@ -213,8 +213,9 @@ struct AttentionArgs {
     float *partial_dk;       // [key_parts, K, Hk, D]
     float *partial_dv;       // [key_parts, K, Hk, D]
 };
-int64_t attention_workspace_floats(int64_t R, int64_t K, int64_t S, int64_t H, int64_t Hk, int64_t D);
-int64_t attention_backward_workspace_floats(int64_t R, int64_t K, int64_t S, int64_t H, int64_t Hk, int64_t D);
+int64_t attention_workspace_floats(int64_t R, int64_t K, int64_t S, int64_t H, int64_t Hk, int64_t D, int type);
+int64_t attention_backward_workspace_floats(int64_t R, int64_t K, int64_t S, int64_t H, int64_t Hk, int64_t D,
+                                            int type);
 hipError_t launch_attention(const AttentionArgs &a, float *workspace, int type, hipStream_t s);
 hipError_t launch_attention_backward(const AttentionArgs &a, float *workspace, int type, hipStream_t s);
 
@@ -257,7 +258,7 @@ struct LossArgs {
     const float *dloss;
     void *dx;                // [R, I] or nullptr
     void *dw;                // [V, I] or nullptr
-    float *unit;             // per_row: power of two that dloss is held in
+    float *unit;             // per_row: power of two that dloss is held in; then the blocks' largest
     void *d;                 // [R, ldd], a piece's gradient of the logits
     int64_t ldd;
     int64_t ld;              // elements from a row of x, and of w, to the next
