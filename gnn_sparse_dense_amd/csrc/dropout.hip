@@ -8,7 +8,9 @@
 // launches do not enter, so the mask of a call can be made again anywhere.
 //
 // Bound by memory: 8 bytes an fp32 element, 4 (6 with a residual) a 16-bit one.
-// The generator is 20 products of 32 x 32 bits for four elements.
+// The generator is 20 products of 32 x 32 bits for four elements.  1,000,000 x 64 fp32,
+// forward and backward 83 us each (6.1 TB/s), 16,381 x 4096 bf16 67 us with a residual
+// (6.0) and 50 without (5.4).
 #include "rows.h"
 
 #include <algorithm>
