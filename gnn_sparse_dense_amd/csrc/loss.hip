@@ -42,7 +42,7 @@ namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f;
 
-using Narrow = Shape<128, 64, 4, 1>;
+using Narrow = Shape<64, 64, 2, 2>;
 using Flat = Shape<64, 128, 1, 4>;
 
 // ---- the rows with a class ----
@@ -561,8 +561,10 @@ int64_t piece_of(int64_t R, int64_t V, int size) {
     return std::min(fits, whole(V, 16));
 }
 
-// 256 x 256 tiles when there are enough of them to fill the chip; 128 x 64 where
-// no more columns exist.
+// 256 x 256 tiles when there are enough of them to fill the chip; 64 x 64 where no
+// more columns exist: more of them share a unit, and their rounds end closer
+// together than 128 x 64 ones' (1,000,000 rows of 64, half with a class, 40 classes, fp32,
+// 474 -> 470 us; dx in such tiles too, see dx_shape(), 418).
 enum class Tiles { kLarge, kMedium, kNarrow };
 
 Tiles tiles_for(int64_t rows, int64_t cols, int size, bool direct) {
@@ -590,16 +592,19 @@ int64_t dw_chunk(int64_t R, int64_t N, int64_t I) {
 
 // dx: 256 x 256 tiles where a piece has enough classes for their start and end to
 // weigh little, and parts of the classes side by side, added up afterwards, where
-// the tiles do not fill the chip (parts of 1,024 classes at least).
+// the tiles do not fill the chip (parts of 1,024 classes at least; 5,003 x 1001, 49,999
+// classes, fp16: 1,165 us whole in 128 x 128 tiles, 529 in three parts of 256 x 256).  Up
+// to 64 classes: a few steps to a tile, small tiles.
 struct DxShape {
-    bool large;
+    bool large, small;
     int64_t parts, part;
 };
 
 DxShape dx_shape(int64_t R, int64_t I, int64_t N, int size, bool direct) {
     DxShape d;
     d.large = direct && size == 2 && I > 128 && R > 128 && N >= 4096;
-    const int tile = d.large ? 256 : 128;
+    d.small = N <= 64;
+    const int tile = d.large ? 256 : d.small ? 64 : 128;
     const int64_t tiles = tiles_of(R, tile) * tiles_of(I, tile), want = d.large ? kUnits : 2 * kUnits;
     d.parts = std::max<int64_t>(1, std::min({(want + tiles / 2) / std::max<int64_t>(1, tiles), N / 1024, int64_t(64)}));
     d.part = whole(tiles_of(N, (int)d.parts), 64);
@@ -727,6 +732,9 @@ hipError_t backward(const LossArgs &args, hipStream_t s) {
             hipError_t e = hipSuccess;
             if (dx.large) {
                 if constexpr (sizeof(T) == 2) e = dx_launch<T, Large, true>(a, v0, N, summed ? v0 != 0 : -1, s);
+            } else if (dx.small) {
+                e = direct ? dx_launch<T, Narrow, true>(a, v0, N, summed ? v0 != 0 : -1, s)
+                           : dx_launch<T, Narrow, false>(a, v0, N, summed ? v0 != 0 : -1, s);
             } else {
                 e = direct ? dx_launch<T, Medium, true>(a, v0, N, summed ? v0 != 0 : -1, s)
                            : dx_launch<T, Medium, false>(a, v0, N, summed ? v0 != 0 : -1, s);
