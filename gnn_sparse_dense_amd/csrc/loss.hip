@@ -32,8 +32,8 @@
 // 1,662 (69%), against 1.21 PFLOP/s of a large library product; a tile of the
 // logits sums over 2,048 elements, too few to cover its start and its exponentials.
 // 64 rows x 2048, 32,768 classes: 26 us, w's 134 MB at 5.2 TB/s.  150,000 rows with a
-// class of 300,007 x 128, 47 classes, fp32: 37 + 40 us for the tiles' two passes, dx 48,
-// dw 34, 50 for packing rows and clearing the others: eight passes over the rows.
+// class of 300,007 x 128, 47 classes, fp32: 36 + 38 us for the tiles' two passes, dx 40,
+// dw 34, 49 for packing rows and clearing the others: eight passes over the rows.
 #include "tile_product.h"
 
 namespace gspmm {
@@ -428,6 +428,35 @@ __global__ __launch_bounds__(kPackThreads) void loss_rest_kernel(LossArgs a, boo
     }
 }
 
+// A tile's sums over K: fp32 rows in runs of kRun that are added up at their ends,
+// since one chain over all of K rounds to the size of its largest term at each step
+// (6,000 rows of 1024, 8,000 classes: dx 1.6e-6 off and 3,051 us in one chain, 1.1e-6
+// and 3,072 us in runs of 4,096, 8e-7 and 3,072 us of 2,048).  16-bit results are
+// rounded far above that, and rows off 16 bytes come here with few classes or in parts.
+constexpr int64_t kRun = 2048;
+
+template <typename T, typename S, bool A_ROWS, bool DIRECT>
+__device__ inline void long_sums(const Stages &lds, const Operand<T> &a, const Operand<T> &b, int64_t K, Sums<S> &sums) {
+    if constexpr (sizeof(T) == 2 || !DIRECT) {
+        tile_sums<T, S, A_ROWS, false, DIRECT>(lds, a, b, K, sums);
+    } else {
+        for (int64_t k = 0; k < K; k += kRun) {
+            const int64_t n = min(kRun, K - k);
+            Operand<T> A = a, B = b;
+            A.ptr += A_ROWS ? k : k * a.ld;
+            (A_ROWS ? A.inner : A.outer) = n;
+            B.ptr += k * b.ld;
+            B.outer = min(n, b.outer - k);
+            Sums<S> run = {};
+            tile_sums<T, S, A_ROWS, false, DIRECT>(lds, A, B, n, run);
+#pragma unroll
+            for (int i = 0; i < S::MI; ++i)
+#pragma unroll
+                for (int j = 0; j < S::NI; ++j) sums.at[i][j] += run.at[i][j];
+        }
+    }
+}
+
 // A tile of dx = d w over a part of a piece's classes: ADD is -1 where it is the
 // whole of dx, 0 and 1 for the first and the other pieces of the fp32 sums.
 template <typename T, typename S, bool DIRECT, int ADD>
@@ -456,7 +485,7 @@ __global__ __launch_bounds__(S::kThreads, 2) void loss_dx_kernel(LossArgs a, int
         __syncthreads();
         Sums<S> sums = {};
         f32x16 (&acc)[S::MI][S::NI] = sums.at;
-        tile_sums<T, S, true, false, DIRECT>(lds, A, B, K, sums);
+        long_sums<T, S, true, DIRECT>(lds, A, B, K, sums);
         if constexpr (ADD < 0) {
             const float f = loss_unit(a) / kHeld<T>;
 #pragma unroll
@@ -497,7 +526,7 @@ __global__ __launch_bounds__(S::kThreads, 2) void loss_dw_kernel(LossArgs a, int
         __syncthreads();
         Sums<S> sums = {};
         f32x16 (&acc)[S::MI][S::NI] = sums.at;
-        tile_sums<T, S, false, false, DIRECT>(lds, A, B, n, sums);
+        long_sums<T, S, false, DIRECT>(lds, A, B, n, sums);
         if (chunk) {
             tile_store_fp32<S, false>(sums, a.dw_partial + (part * N + row) * a.I + col, a.I, A.inner, B.inner);
             continue;

@@ -567,7 +567,8 @@ int spmm_layer_norm_backward(const void *dy, const void *x, const void *weight, 
  *   out[i] = sum_j p_ij v[j],  p_ij = exp(scale q[i].k[j]) / sum_j exp(..)
  * and zero where there are none (also for rows outside the segments, whose
  * contents reach nothing; within a segment an infinity or NaN of a row or key
- * may reach all of the segment's rows, also those that do not see it).
+ * may reach all of the segment's rows, also those that do not see it; a row
+ * whose scores are all -infinity counts as one that sees nothing).
  * Row r of q starts ldq >= H * D elements behind row r - 1, of k and v
  * ldk, ldv >= Hk * D; out and all gradients are packed.  lse (fp32 [R, H] or
  * NULL) and rest ([R, H, D] or NULL: what out's rounding to `type` leaves off)

@@ -70,6 +70,13 @@ def test_parts_and_large_tiles(R, I, V, kind):
     compare(R, I, V, kind, "mean", 0.1)
 
 
+@pytest.mark.parametrize("R,I,V", [(2061, 2048, 4099), (2048, 2048, 4096)])
+def test_long_fp32_sums(R, I, V):
+    """dx in two parts of the classes and dw over all rows at once, each longer than
+    a run of 2,048 that is summed in one chain, or as long."""
+    compare(R, I, V, "fp32", "mean", 0.0)
+
+
 @pytest.mark.parametrize("kind", sorted(TYPES))
 @pytest.mark.parametrize("drop", [0.0, 1.0, 0.97])
 def test_all_no_and_few_rows_with_a_class(drop, kind):
