@@ -32,7 +32,7 @@
 // 1,662 (69%), against 1.21 PFLOP/s of a large library product; a tile of the
 // logits sums over 2,048 elements, too few to cover its start and its exponentials.
 // 64 rows x 2048, 32,768 classes: 26 us, w's 134 MB at 5.2 TB/s.  150,000 rows with a
-// class of 300,007 x 128, 47 classes, fp32: 36 + 38 us for the tiles' two passes, dx 40,
+// class of 300,007 x 128, 47 classes, fp32: 36 + 38 us for the tiles' two passes, dx 41,
 // dw 34, 49 for packing rows and clearing the others: eight passes over the rows.
 #include "tile_product.h"
 
