@@ -46,6 +46,10 @@ int64_t parts_of(int64_t blocks, int64_t want, int64_t keys, int64_t S, int64_t 
     return std::max<int64_t>(1, std::min({want / std::max<int64_t>(1, blocks), length / least, int64_t(64)}));
 }
 
+int query_rows(int64_t R, int64_t S, int64_t H, int64_t Hk, int size) {
+    return large_tiles(R * (H / Hk), S, size) ? 128 : 32;
+}
+
 int64_t tiles(int64_t rows, int64_t S, bool large) { return rows / (large ? 128 : 32) + std::min(rows, S); }
 
 int query_parts(int64_t R, int64_t K, int64_t S, int64_t H, int64_t Hk, int size) {
@@ -77,10 +81,17 @@ int64_t attention_workspace_floats(int64_t R, int64_t K, int64_t S, int64_t H, i
     return parts > 1 ? parts * R * H * (D + 2) : 0;
 }
 
+// delta, and in fp16 lse once more and two floats of each wave of dq's blocks.
+static int64_t row_floats(int64_t R, int64_t S, int64_t H, int64_t Hk, int type) {
+    if (type != SPMM_F16) return R * H;
+    const int64_t rows = query_rows(R, S, H, Hk, 2);
+    return 2 * R * H + 2 * (R * (H / Hk) / rows + S + 2) * Hk * (rows / 32);
+}
+
 int64_t attention_backward_workspace_floats(int64_t R, int64_t K, int64_t S, int64_t H, int64_t Hk, int64_t D,
                                             int type) {
     const int64_t parts = key_parts(R, K, S, H, Hk, type == SPMM_F32 ? 4 : 2);
-    return R * H + (parts > 1 ? 2 * parts * K * Hk * D : 0);
+    return row_floats(R, S, H, Hk, type) + (parts > 1 ? 2 * parts * K * Hk * D : 0);
 }
 
 hipError_t launch_attention(const AttentionArgs &args, float *workspace, int type, hipStream_t s) {
@@ -115,8 +126,11 @@ hipError_t launch_attention_backward(const AttentionArgs &args, float *workspace
     a.parts = 1;
     a.key_parts = key_parts(a.R, a.K, a.S, a.H, a.Hk, size);
     a.part_rows = part_rows(a.R, a.K, a.S, a.H, a.Hk, size) / (a.causal ? 2 : 1);
+    a.query_rows = query_rows(a.R, a.S, a.H, a.Hk, size);
     a.delta = workspace;
-    a.partial_dk = workspace + a.R * a.H;
+    a.held_lse = workspace + a.R * a.H;
+    a.sizes = a.held_lse + a.R * a.H;
+    a.partial_dk = workspace + row_floats(a.R, a.S, a.H, a.Hk, type);
     a.partial_dv = a.partial_dk + a.key_parts * a.K * a.Hk * a.D;
     auto pass = [&](AttentionPass p, bool large, bool direct) {
         return type == SPMM_F32    ? launch_attention_pass<float>(a, p, large, direct, s)

@@ -23,7 +23,11 @@
 // bytes per lane, chunks placed so that both ways of reading meet no bank twice.
 //
 // Sums and statistics are fp32.  Probabilities and ds are rounded to the rows'
-// type where they enter a matrix instruction (16-bit types).
+// type where they enter a matrix instruction (16-bit types).  fp16 has 2^-14 to 2^16
+// for them, so the gradients' kernels hold them times powers of two that are taken
+// out of the sums again: p times 2^12, and ds, a share of 1 / keys of dout.v, times
+// what brings a row's largest so far to 2^11 or more (dq, HeldGradients) or what
+// bounds a key's to 2^15 (dk, KeySums::hold).
 //
 // dk and dv are computed apart from dq, which takes two products more than one
 // kernel for all three would: added up in dq's order or dk's, one of them would need
@@ -280,6 +284,70 @@ __device__ inline int register_row(int i) {
     return 8 * (i >> 2) + 4 * ((threadIdx.x & (kWave - 1)) >> 5) + (i & 3);
 }
 
+// Types that hold probabilities times 2^kHeldBits, and ds, in the gradients' products.
+template <typename T>
+constexpr bool kHolds = __is_same(T, _Float16);
+template <typename T>
+constexpr float kHeldBits = kHolds<T> ? 12.0f : 0.0f;
+
+// ds of a lane's row, held times a power of two `by` where fp16 takes it.  By the
+// running largest, like a softmax's maximum: from 2^15 on, which is below fp16's
+// largest, it is brought to 2^11 to 2^12 and the sums so far follow, exactly.  What is
+// smaller than the largest by up to 2^25 keeps its eleven bits.  Starts at 2^60: times
+// the largest there can be (2^12 p, 128 products of 2^16 by 2^16, twice) it stays finite,
+// and what does not reach 2^15 then has gradients below fp16's smallest number.  8,192
+// causal rows, 16 heads of 128 over 4: dq 187 -> 204 us.
+template <typename T>
+struct HeldGradients {
+    float by = kHolds<T> ? 0x1p60f : 1.0f;
+
+    template <int BLOCKS>
+    __device__ inline void follow(f32x16 &ds, f32x16 (&sums)[BLOCKS]) {
+        if constexpr (kHolds<T>) {
+            float most = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) most = fmaxf(most, fabsf(ds[i]));
+            // rare: the sums stay where the matrix instructions have them
+            if (__builtin_expect(__any(most >= 0x1p15f), 0)) {
+                most = fmaxf(most, other_half(most));
+                // infinities (their row's gradients are infinite or NaN) leave `by` alone
+                const int e = most >= 0x1p15f && most < INFINITY ? 12 - __builtin_amdgcn_frexp_expf(most) : 0;
+                const float f = ldexpf(1.0f, e);
+                by *= f;
+                ds *= f;
+#pragma unroll
+                for (int b = 0; b < BLOCKS; ++b) sums[b] *= f;
+            }
+        }
+    }
+};
+
+template <int CTRL>
+__device__ inline float most_of_lanes(float v) {
+    return fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf,
+                                                                          false)));
+}
+
+// The largest v of the wave's lanes: within quads, quads of 8, halves of 16, then rows of
+// 16 through scalar registers.
+__device__ inline float wave_most(float v) {
+    v = most_of_lanes<0x4E>(most_of_lanes<0xB1>(v));
+    v = most_of_lanes<0x140>(most_of_lanes<0x141>(v));
+    auto lane = [&](int l) { return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), l)); };
+    return fmaxf(fmaxf(lane(0), lane(16)), fmaxf(lane(32), lane(48)));
+}
+
+// The length of the lane's row, its halves in both half waves.
+template <typename T, int STEPS>
+__device__ inline float length_of(const Pack<T> (&r)[STEPS]) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int ks = 0; ks < STEPS; ++ks)
+#pragma unroll
+        for (int e = 0; e < kPack<T>; ++e) sum = fmaf((float)r[ks].v[e], (float)r[ks].v[e], sum);
+    return sqrtf(sum + other_half(sum));
+}
+
 template <typename T>
 __device__ inline Pack<T> group_of(const f32x16 &s, int group) {
     Pack<T> p;
@@ -340,6 +408,12 @@ __device__ inline void store_rest(T *row, f32x16 (&acc)[BLOCKS], float f, int D)
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[b][i] = acc[b][i] * f - (float)(T)(acc[b][i] * f);
     store_row<WHOLE>(row, acc, 1.0f, D);
+}
+
+// What takes the powers of two out of the sums of ds again.
+template <typename T>
+__device__ inline float held_scale(float scale, float by) {
+    return kHolds<T> ? scale * (0x1p-12f / by) : scale;
 }
 
 // What both query-side kernels know of a tile of packed rows.
@@ -662,6 +736,7 @@ __global__ __launch_bounds__(WAVES * kWave, (kQuerySide<T, DP, DIRECT>)) void at
         q.locate(a, s, hk, s.tile * BM, wave * 32);
         const int64_t at = q.row * a.H + q.head;
         f32x16 acc[L::kBlocks] = {};
+        HeldGradients<T> held;
         if (s.run > 0 && s.run <= a.S) {
             RowPacks<T, DP> mine, dout;
             load_row<T, DP, DIRECT>(dout, (const T *)a.dout + at * D, D, q.exists());
@@ -675,8 +750,20 @@ __global__ __launch_bounds__(WAVES * kWave, (kQuerySide<T, DP, DIRECT>)) void at
                     for (int e = 0; e < kPack<T>; ++e) delta = fmaf((float)dout[ks].v[e], (float)mine[ks].v[e], delta);
             }
             delta += other_half(delta);
-            const float lse = q.exists() ? a.lse[at] : INFINITY;
+            const float lse = q.exists() ? a.lse[at] - kHeldBits<T> : INFINITY;
             if (q.exists() && half == 0) a.delta[at] = delta;
+            if constexpr (kHolds<T>) {
+                // what dk's kernel bounds its ds by; a row that is not finite bounds nothing
+                const float length = length_of(dout), size = fabsf(delta);
+                const float longest = wave_most(q.exists() && length < INFINITY ? length : 0.0f);
+                const float largest = wave_most(q.exists() && size < INFINITY ? size : 0.0f);
+                if ((threadIdx.x & (kWave - 1)) == 0) {
+                    float *to = a.sizes + 2 * ((int64_t)id * WAVES + wave);
+                    to[0] = longest;
+                    to[1] = largest;
+                }
+                if (q.exists() && half == 0) a.held_lse[at] = lse;
+            }
             if (a.dq) {
                 load_row<T, DP, DIRECT>(mine, (const T *)a.q + q.row * a.ldq + q.head * D, D, q.exists());
                 const int tiles = (seen_by_tile<BM>(a, s, q.keys) + BN - 1) / BN;
@@ -716,7 +803,9 @@ __global__ __launch_bounds__(WAVES * kWave, (kQuerySide<T, DP, DIRECT>)) void at
                                     if (j0 + b * 32 + register_row(i) >= q.seen) sc[i] = 0.0f;
                             }
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) sc[i] *= dp[i] - delta;
+                            for (int i = 0; i < 16; ++i)
+                                sc[i] *= kHolds<T> ? fmaf(dp[i], held.by, -delta * held.by) : dp[i] - delta;
+                            held.follow(sc, acc);
 #pragma unroll
                             for (int g = 0; g < L::kGroups; ++g) {
                                 const Pack<T> ds = group_of<T>(sc, g);
@@ -730,7 +819,8 @@ __global__ __launch_bounds__(WAVES * kWave, (kQuerySide<T, DP, DIRECT>)) void at
         } else if (q.exists() && half == 0) {
             a.delta[at] = 0.0f;
         }
-        if (a.dq && q.exists()) store_row<DIRECT>((T *)a.dq + at * D, acc, a.scale, D);
+        if (a.dq && q.exists())
+            store_row<DIRECT>((T *)a.dq + at * D, acc, held_scale<T>(a.scale, held.by), D);
     }
 }
 
@@ -807,10 +897,10 @@ struct RowTiles {
             const int64_t from = (row0 + i0) * a.H + hk * a.G.d;
             const int at = (int)((i - i0) * a.H) + m - i * a.G.d;
             if constexpr (DIRECT) {
-                copy_floats(lse_of, a.lse + from, at, in);
+                copy_floats(lse_of, (kHolds<T> ? a.held_lse : a.lse) + from, at, in);
                 copy_floats(delta_of, a.delta + from, at, in);
             } else {
-                lse = in ? a.lse[from + at] : 0.0f;
+                lse = in ? (kHolds<T> ? a.held_lse : a.lse)[from + at] : 0.0f;
                 delta = in ? a.delta[from + at] : 0.0f;
             }
         }
@@ -841,6 +931,29 @@ struct KeySums {
     RowReader<T, DP> rows;
     TurnedReader<T, DP> turned;
     float c;
+    float by = 1.0f;
+
+    // ds of the lane's key is held times a power of two `by` in fp16: |ds| <= |dout| |v| +
+    // |dout.out| over the rows of the segment is brought to 2^15 at most (2^12 p among it).
+    // By a bound and not by the largest so far, whose branch parts the products from the
+    // reads ahead of them (8,192 causal rows, 16 heads of 128 over 4: 448 us, 368 with the
+    // bound, 341 with ds as it is).  ds of 2^-29 of the bound keep eleven bits: of even
+    // weights over 32,768 keys, rows with a thousandth of the longest dout.
+    __device__ inline void hold(const AttentionArgs &a, int run, int hk, int64_t row0, int packed) {
+        if constexpr (kHolds<T>) {
+            // dq's waves of the segment's rows: those of its tiles, slot by slot
+            const int waves = a.query_rows / 32, tiles = (packed + a.query_rows - 1) / a.query_rows;
+            const int64_t slot = row0 * a.G.d / a.query_rows + run;
+            float longest = 0.0f, largest = 0.0f;
+            for (int i = threadIdx.x & (kWave - 1); i < tiles * waves; i += kWave) {
+                const float *at = a.sizes + 2 * (((slot + i / waves) * a.Hk + hk) * waves + i % waves);
+                longest = fmaxf(longest, at[0]);
+                largest = fmaxf(largest, at[1]);
+            }
+            const float most = wave_most(longest) * length_of(v) + wave_most(largest);
+            if (most > 0.0f && most < INFINITY) by = ldexpf(1.0f, 3 - __builtin_amdgcn_frexp_expf(most));
+        }
+    }
 
     __device__ inline void read(RowPacks<T, DP> &r, LdsByte *tile, int b) const {
 #pragma unroll
@@ -867,6 +980,12 @@ struct KeySums {
         const f32x16 lse = register_floats(lse_of, b);
 #pragma unroll
         for (int i = 0; i < 16; ++i) sc[i] = exp2_of(fmaf(sc[i], c, -lse[i]));
+    }
+    // ds from the probabilities and dp
+    __device__ inline void gradients(f32x16 &dp, const f32x16 &sc, const f32x16 &delta) const {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) dp[i] = sc[i] * (dp[i] - delta[i]);
+        if constexpr (kHolds<T>) dp *= by;
     }
     static __device__ inline void add(f32x16 (&to)[L::kBlocks], const Pack<T> (&w)[L::kGroups], const TurnedRows &r) {
 #pragma unroll
@@ -898,9 +1017,7 @@ struct KeySums {
         __builtin_amdgcn_sched_barrier(0);
         read(qturned, qt, b);
         add(dv, w.p, dturned);
-        const f32x16 delta = register_floats(delta_of, b);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) dp[i] = sc[i] * (dp[i] - delta[i]);
+        gradients(dp, sc, register_floats(delta_of, b));
 #pragma unroll
         for (int g = 0; g < L::kGroups; ++g) w.ds[g] = group_of<T>(dp, g);
         spread();
@@ -960,6 +1077,7 @@ __global__ __launch_bounds__(WAVES * kWave, (kKeySide<T, DP, DIRECT>)) void atte
             const int64_t key = (int64_t)s.row0 + min(j, s.rows - 1);
             load_row<T, DP, DIRECT>(sums.k, (const T *)a.k + key * a.ldk + hk * D, D, exists);
             load_row<T, DP, DIRECT>(sums.v, (const T *)a.v + key * a.ldv + hk * D, D, exists);
+            sums.hold(a, s.run, hk, by.row0, by.packed);
             RowTiles<T, DP, BN, WAVES, DIRECT> tiles(a, by.row0, hk, by.packed, wave);
             __syncthreads();
             if constexpr (kAhead) {
@@ -1012,9 +1130,7 @@ __global__ __launch_bounds__(WAVES * kWave, (kKeySide<T, DP, DIRECT>)) void atte
                             }
                             if (m0 < wave_full) K::hide(sc, m0, mine_from);
                             sums.probabilities(sc, lse_of[u], b);
-                            const f32x16 delta = register_floats(delta_of[u], b);
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) dp[i] = sc[i] * (dp[i] - delta[i]);
+                            sums.gradients(dp, sc, register_floats(delta_of[u], b));
 #pragma unroll
                             for (int g = 0; g < L::kGroups; ++g) {
                                 const Pack<T> p = group_of<T>(sc, g), ds = group_of<T>(dp, g);
@@ -1029,12 +1145,13 @@ __global__ __launch_bounds__(WAVES * kWave, (kKeySide<T, DP, DIRECT>)) void atte
             }
         }
         const int64_t at = (((int64_t)s.row0 + j) * a.Hk + hk) * D, shift = part * a.K * a.Hk * a.D;
+        const float fk = held_scale<T>(a.scale, sums.by), fv = kHolds<T> ? 0x1p-12f : 1.0f;
         if (exists && parts > 1) {
-            if (a.dk) store_row<DIRECT>(a.partial_dk + shift + at, sums.dk, a.scale, D);
-            if (a.dv) store_row<DIRECT>(a.partial_dv + shift + at, sums.dv, 1.0f, D);
+            if (a.dk) store_row<DIRECT>(a.partial_dk + shift + at, sums.dk, fk, D);
+            if (a.dv) store_row<DIRECT>(a.partial_dv + shift + at, sums.dv, fv, D);
         } else if (exists) {
-            if (a.dk) store_row<DIRECT>((T *)a.dk + at, sums.dk, a.scale, D);
-            if (a.dv) store_row<DIRECT>((T *)a.dv + at, sums.dv, 1.0f, D);
+            if (a.dk) store_row<DIRECT>((T *)a.dk + at, sums.dk, fk, D);
+            if (a.dv) store_row<DIRECT>((T *)a.dv + at, sums.dv, fv, D);
         }
     }
 }

@@ -205,6 +205,9 @@ struct AttentionArgs {
     float *partial_sum;      // [parts, R, H]
     const void *dout;        // [R, H, D]
     float *delta;            // [R, H]
+    float *held_lse;         // [R, H], fp16: lse less the power of two that p is held times
+    float *sizes;            // fp16: of each wave of dq's blocks, the longest dout and largest |delta|
+    int query_rows;          // packed rows of a block of dq
     void *dq;                // [R, H, D] or nullptr
     void *dk;                // [K, Hk, D] or nullptr
     void *dv;                // [K, Hk, D] or nullptr
