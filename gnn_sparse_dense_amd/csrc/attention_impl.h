@@ -24,10 +24,11 @@
 //
 // Sums and statistics are fp32.  Probabilities and ds are rounded to the rows'
 // type where they enter a matrix instruction (16-bit types).  fp16 has 2^-14 to 2^16
-// for them, so the gradients' kernels hold them times powers of two that are taken
-// out of the sums again: p times 2^12, and ds, a share of 1 / keys of dout.v, times
-// what brings a row's largest so far to 2^11 or more (dq, HeldGradients) or what
-// bounds a key's to 2^15 (dk, KeySums::hold).
+// for them, so they are held times powers of two that are taken out of the sums
+// again: p times 2^12 (forward: the running maximum's, so that 60,000 keys of 2^-22 of
+// the largest weight still add up), and in the gradients ds, a share of 1 / keys of
+// dout.v, times what brings a row's largest so far to 2^11 or more (dq, HeldGradients) or
+// what bounds a key's to 2^15 (dk, KeySums::hold).
 //
 // dk and dv are computed apart from dq, which takes two products more than one
 // kernel for all three would: added up in dq's order or dk's, one of them would need
@@ -284,11 +285,16 @@ __device__ inline int register_row(int i) {
     return 8 * (i >> 2) + 4 * ((threadIdx.x & (kWave - 1)) >> 5) + (i & 3);
 }
 
-// Types that hold probabilities times 2^kHeldBits, and ds, in the gradients' products.
+// Types that hold probabilities times 2^kHeldBits, and ds, in the products.
 template <typename T>
 constexpr bool kHolds = __is_same(T, _Float16);
 template <typename T>
 constexpr float kHeldBits = kHolds<T> ? 12.0f : 0.0f;
+
+// By how many powers of two a forward weight may pass the maximum that it is taken
+// against: what is held stays below 2^15 in fp16.
+template <typename T>
+constexpr float kGrowth = kHolds<T> ? 3.0f : 8.0f;
 
 // ds of a lane's row, held times a power of two `by` where fp16 takes it.  By the
 // running largest, like a softmax's maximum: from 2^15 on, which is below fp16's
@@ -577,7 +583,7 @@ __global__ __launch_bounds__(WAVES * kWave, (kQuerySide<T, DP, DIRECT>)) void at
         Queries<T> q;
         q.locate(a, s, hk, s.tile * BM, wave * 32);
         f32x16 acc[L::kBlocks] = {};
-        float top = -INFINITY, sum = 0.0f;
+        float top = -INFINITY, sum = 0.0f;               // (top: less what weights are held times)
         if (s.run > 0 && s.run <= a.S) {
             const int tiles = (seen_by_tile<BM>(a, s, q.keys) + BN - 1) / BN;
             const int per = (tiles + a.parts - 1) / a.parts;
@@ -628,11 +634,11 @@ __global__ __launch_bounds__(WAVES * kWave, (kQuerySide<T, DP, DIRECT>)) void at
                     for (int b = 0; b < NB; ++b)
 #pragma unroll
                         for (int i = 0; i < 16; ++i) most = fmaxf(most, sc[b][i]);
-                    most = fmaxf(most, other_half(most)) * c;
+                    most = fmaxf(most, other_half(most)) * c - kHeldBits<T>;
                     // The sums keep the maximum they were taken against until it
-                    // grows by 2^8: weights up to 256 lose nothing in any of the
-                    // types, and most tiles rescale nothing.
-                    if (__any(most > top + 8.0f)) {
+                    // grows by 2^8 (fp16: 2^3): weights up to 256 (8, held times 2^12)
+                    // lose nothing, and most tiles rescale nothing.
+                    if (__any(most > top + kGrowth<T>)) {
                         const float next = fmaxf(top, most);
                         const float f = next == -INFINITY ? 1.0f : exp2_of(top - next);
                         top = next;

@@ -577,8 +577,8 @@ int spmm_layer_norm_backward(const void *dy, const void *x, const void *weight, 
  *   and the forward pass's out, lse and rest (NULL: dq and dk take out as it
  *   was rounded, which adds half as much to their error in 16 bits again).
  * Probabilities and the scores' gradients are rounded to `type` where they enter a
- * matrix product (the gradients' in fp16 times powers of two that keep them clear of
- * its ends); sums and softmax statistics are fp32.
+ * matrix product (in fp16 times powers of two that keep them clear of its ends); sums
+ * and softmax statistics are fp32.
  * scale > 0; D <= 128; R * H and K * Hk < 2^31 - 4097, S * Hk < 2^24,
  * H < 2^16.
  */

@@ -141,6 +141,19 @@ def test_gradients_of_values_of_small_weight(monkeypatch, m, D):
     run(monkeypatch, q, k, v, dout, scale=1.0, names=("out", "dv"))
 
 
+def test_weights_far_below_the_largest(monkeypatch):
+    """Every 256th key has nearly all the weight and no value; the others weigh about
+    2^-22.7 of it and make up all of out."""
+    g, m = rng(77), 65536
+    k = torch.zeros(m, 1, 8, dtype=F16)
+    k[::256, 0, 0] = 22.7 * 0.6931                     # 22.7 in base 2
+    q = torch.zeros(1, 2, 8, dtype=F16)
+    q[..., 0] = 1.0
+    v = (1024.0 * (1.0 + 0.1 * normal(g, m, 1, 8))).to(F16)
+    v[::256] = 0.0
+    run(monkeypatch, q, k, v, normal(g, 1, 2, 8, dtype=F16), scale=1.0, names=("out",))
+
+
 @pytest.mark.parametrize("n,m", [(20, 25), (90, 120), (300, 310), (700, 900)])
 @pytest.mark.parametrize("D", [24, 40, 64, 72, 128])
 @pytest.mark.parametrize("order", ["rising", "falling", "mixed"])
