@@ -431,13 +431,14 @@ __global__ __launch_bounds__(kPackThreads) void loss_rest_kernel(LossArgs a, boo
 // A tile's sums over K: fp32 rows in runs of kRun that are added up at their ends,
 // since one chain over all of K rounds to the size of its largest term at each step
 // (6,000 rows of 1024, 8,000 classes: dx 1.6e-6 off and 3,051 us in one chain, 1.1e-6
-// and 3,072 us in runs of 4,096, 8e-7 and 3,072 us of 2,048).  16-bit results are
-// rounded far above that, and rows off 16 bytes come here with few classes or in parts.
+// and 3,072 us in runs of 4,096, 8e-7 and 3,072 us of 2,048; sums of like terms, 65,536
+// rows through registers: 9.8e-4 off in one chain, 3.2e-5 in runs).  16-bit results are
+// rounded far above that, and dx in small tiles (rows by rows) sums over 64 classes at most.
 constexpr int64_t kRun = 2048;
 
 template <typename T, typename S, bool A_ROWS, bool DIRECT>
 __device__ inline void long_sums(const Stages &lds, const Operand<T> &a, const Operand<T> &b, int64_t K, Sums<S> &sums) {
-    if constexpr (sizeof(T) == 2 || !DIRECT) {
+    if constexpr (sizeof(T) == 2 || (A_ROWS && S::BM == Narrow::BM)) {
         tile_sums<T, S, A_ROWS, false, DIRECT>(lds, a, b, K, sums);
     } else {
         for (int64_t k = 0; k < K; k += kRun) {
