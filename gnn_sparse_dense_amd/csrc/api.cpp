@@ -2033,13 +2033,15 @@ SPMM_API int spmm_layer_norm_backward(const void *dy, const void *x, const void 
 static int check_attention(int64_t R, int64_t K, int64_t S, int64_t H, int64_t Hk, int64_t D, int type) {
     if (R < 0 || K < 0) return fail(SPMM_E_INVALID_ARG, "negative size");
     if (S < 1 || H < 1 || Hk < 1 || D < 1) return fail(SPMM_E_INVALID_ARG, "S, H, Hk and D must be positive");
-    if (H % Hk) return fail(SPMM_E_INVALID_ARG, "H (%lld) must be a multiple of Hk (%lld)", (long long)H, (long long)Hk);
+    if (H % Hk)
+        return fail(SPMM_E_INVALID_ARG, "H (%lld) must be a multiple of Hk (%lld)", (long long)H, (long long)Hk);
     if (D > kAttentionMaxWidth)
         return fail(SPMM_E_UNSUPPORTED, "heads of at most %d elements (got %lld)", kAttentionMaxWidth, (long long)D);
     const int64_t most = INT_MAX - 4096;
     if (R >= most || K >= most || S >= (1 << 24) || H >= (1 << 16) || R * H >= most || K * Hk >= most ||
         S * Hk >= (1 << 24))
-        return fail(SPMM_E_UNSUPPORTED, "R * H and K * Hk must be below 2^31 - 4097, S * Hk below 2^24 and H below 2^16");
+        return fail(SPMM_E_UNSUPPORTED,
+                    "R * H and K * Hk must be below 2^31 - 4097, S * Hk below 2^24 and H below 2^16");
     return check_types(type, false, 0);
 }
 
@@ -2065,8 +2067,9 @@ SPMM_API int spmm_segment_attention_workspace(int64_t R, int64_t K, int64_t S, i
 
 SPMM_API int spmm_segment_attention(const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv,
                                     const int64_t *offsets, const int64_t *key_offsets, void *out, void *rest,
-                                    float *lse, int64_t R, int64_t K, int64_t S, int64_t H, int64_t Hk, int64_t D, double scale,
-                                    int causal, int type, void *workspace, int64_t workspace_bytes, void *stream) {
+                                    float *lse, int64_t R, int64_t K, int64_t S, int64_t H, int64_t Hk, int64_t D,
+                                    double scale, int causal, int type, void *workspace, int64_t workspace_bytes,
+                                    void *stream) {
     if (const int st = check_attention(R, K, S, H, Hk, D, type)) return st;
     if (!((float)scale * 1.44269504f > 0.0f && std::isfinite((float)scale * 1.44269504f)))
         return fail(SPMM_E_INVALID_ARG, "scale must be positive and finite in fp32 (got %g)", scale);
@@ -2125,8 +2128,8 @@ SPMM_API int spmm_segment_attention_backward_workspace(int64_t R, int64_t K, int
 SPMM_API int spmm_segment_attention_backward(const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v,
                                              int64_t ldv, const int64_t *offsets, const int64_t *key_offsets,
                                              const void *out, const void *rest, const float *lse, const void *dout,
-                                             void *dq, void *dk, void *dv, int64_t R, int64_t K, int64_t S, int64_t H, int64_t Hk,
-                                             int64_t D, double scale, int causal, int type, void *workspace,
+                                             void *dq, void *dk, void *dv, int64_t R, int64_t K, int64_t S, int64_t H,
+                                             int64_t Hk, int64_t D, double scale, int causal, int type, void *workspace,
                                              int64_t workspace_bytes, void *stream) {
     if (const int st = check_attention(R, K, S, H, Hk, D, type)) return st;
     if (!((float)scale * 1.44269504f > 0.0f && std::isfinite((float)scale * 1.44269504f)))

@@ -70,7 +70,8 @@ int64_t part_rows(int64_t R, int64_t K, int64_t S, int64_t H, int64_t Hk, int si
 }
 
 int key_parts(int64_t R, int64_t K, int64_t S, int64_t H, int64_t Hk, int size) {
-    const int64_t rows = R * (H / Hk) / std::max<int64_t>(1, S);      // the longest segment's are taken to be thrice the mean
+    // the longest segment's rows are taken to be thrice the mean
+    const int64_t rows = R * (H / Hk) / std::max<int64_t>(1, S);
     return (int)std::max<int64_t>(1, std::min<int64_t>(kMostParts, 3 * rows / part_rows(R, K, S, H, Hk, size)));
 }
 

@@ -35,15 +35,16 @@
 // atomics, whose order changes results.
 //
 // Bound by the matrix cores and the exponentials between them, each about as long;
-// medians of the kernels alone under the profiler, 128-element heads, causal, bf16:
-// 12,001 rows in 5 segments, 32 heads over 8, 354 us in a loop of its own (880
-// TFLOP/s; matrix cores 40%, vector units 39% busy, no LDS bank conflicts).  8,192
-// rows in 3, 16 over 4: forward 159 us (640), dq 187 (810 over its three products),
-// dk and dv 347 + 27 for the parts' sum (582 over four; one wave to a SIMD, 28% and
-// 26% busy, a quarter of the units idle at its end).  One row each against 100,003
-// keys in 32 segments: 91 + 8 us, 410 MB at 4.2 TB/s.  4,096 graphs of 24 rows, 4 heads of
-// 32, fp32: 81, 106 and 135 us, fp32 matrix instructions 33 to 41% busy on 32 x 32 tiles
-// of which the graphs fill half.
+// medians of the kernels alone over 20 calls under the profiler, 128-element heads, causal,
+// bf16: 12,001 rows in 5 segments, 32 heads over 8, 430 us (350 to 375 us a call in loops of
+// several hundred without it, 830 to 890 TFLOP/s; matrix cores 40%, vector units 39% busy, no
+// LDS bank conflicts).  8,192 rows in 3, 16 over 4: forward 155 us (655), dq 183 (828 over its
+// three products), dk and dv 338 + 27 for the parts' sum (598 over four; one wave to a SIMD,
+// 28% and 26% busy, a quarter of the units idle at its end).  One row each against 100,003
+// keys in 32 segments: 89 + 8 us, 410 MB at 4.2 TB/s.  4,096 graphs of 24 rows, 4 heads of
+// 32, fp32: 81, 106 and 134 us, fp32 matrix instructions 33 to 41% busy on 32 x 32 tiles
+// of which the graphs fill half.  All by segments of like length: the launches go by the
+// mean (attention.hip).
 #pragma once
 
 #include "tile_product.h"
@@ -129,8 +130,8 @@ struct TurnedReader {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int place = (d * 8) ^ ((j >> L::kDrop) << 2) ^ (2 * group & 3);
-                r.v[j] = *(__attribute__((address_space(3))) float *)(tile + ((at ^ (place << 4)) +
-                                                                              (block * 32 + 8 * group + j) * L::kPitch));
+                const int row = (block * 32 + 8 * group + j) * L::kPitch;
+                r.v[j] = *(__attribute__((address_space(3))) float *)(tile + ((at ^ (place << 4)) + row));
             }
             return r;
         }
@@ -202,8 +203,9 @@ struct Fill {
 #pragma unroll
             for (int i = 0; i < kCopies; ++i) {
                 const uint32_t from = row_of(i, wave) < rows.left ? off[i] : kNowhere;
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                    rsrc, (__attribute__((address_space(3))) void *)(lds + (i * WAVES + wave) * 1024), 16, from, 0, 0, 0);
+                LdsByte *to = lds + (i * WAVES + wave) * 1024;
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (__attribute__((address_space(3))) void *)to, 16, from, 0, 0,
+                                                         0);
             }
         } else {
 #pragma unroll
@@ -232,7 +234,8 @@ struct Runs {
     const int64_t *offsets;
     int S, rows, scale;
 
-    __device__ inline Runs(const int64_t *o, int64_t s, int64_t r, int by) : offsets(o), S((int)s), rows((int)r), scale(by) {}
+    __device__ inline Runs(const int64_t *o, int64_t s, int64_t r, int by)
+        : offsets(o), S((int)s), rows((int)r), scale(by) {}
 
     __device__ inline int bound(int v) const {
         if (v <= 0) return 0;
@@ -339,7 +342,8 @@ __device__ inline float most_of_lanes(float v) {
 __device__ inline float wave_most(float v) {
     v = most_of_lanes<0x4E>(most_of_lanes<0xB1>(v));
     v = most_of_lanes<0x140>(most_of_lanes<0x141>(v));
-    auto lane = [&](int l) { return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), l)); };
+    const int bits = __builtin_bit_cast(int, v);
+    auto lane = [&](int l) { return __builtin_bit_cast(float, __builtin_amdgcn_readlane(bits, l)); };
     return fmaxf(fmaxf(lane(0), lane(16)), fmaxf(lane(32), lane(48)));
 }
 
@@ -564,7 +568,8 @@ __device__ inline void walk(int t0, int t1, LoadAll load, PutAll put, Use use) {
 // ---- forward ----
 
 template <typename T, int DP, int WAVES, bool DIRECT, int STAGES>
-__global__ __launch_bounds__(WAVES * kWave, (kQuerySide<T, DP, DIRECT>)) void attention_kernel(AttentionArgs a, unsigned total) {
+__global__ __launch_bounds__(WAVES * kWave, (kQuerySide<T, DP, DIRECT>)) void attention_kernel(AttentionArgs a,
+                                                                                              unsigned total) {
     using L = Tile<T, DP>;
     constexpr int BM = 32 * WAVES, BN = kTileRows<T, WAVES>, NB = BN / 32;
     TILE_PAIRS(ktile, vtile, BN * L::kPitch, STAGES);
@@ -722,7 +727,8 @@ __global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttentionA
 
 // dq, and delta = dout.out of every row, which dk and dv take from here.
 template <typename T, int DP, int WAVES, bool DIRECT>
-__global__ __launch_bounds__(WAVES * kWave, (kQuerySide<T, DP, DIRECT>)) void attention_dq_kernel(AttentionArgs a, unsigned total) {
+__global__ __launch_bounds__(WAVES * kWave, (kQuerySide<T, DP, DIRECT>)) void attention_dq_kernel(AttentionArgs a,
+                                                                                                 unsigned total) {
     using L = Tile<T, DP>;
     constexpr int BM = 32 * WAVES, BN = kTileRows<T, WAVES>, NB = BN / 32;
     TILE_PAIRS(ktile, vtile, BN * L::kPitch, kStagesOf<WAVES>);
@@ -1004,8 +1010,8 @@ struct KeySums {
     // of the next one's operand and the arithmetic that does not wait for it.
     // ahead() reads q of the block after it; border: see hide().
     template <typename Ahead>
-    __device__ inline void block(RowPacks<T, DP> &q, LdsByte *qt, LdsByte *dt, LdsByte *lse_of, LdsByte *delta_of, int b,
-                                 bool border, int m0, int from, Ahead ahead) {
+    __device__ inline void block(RowPacks<T, DP> &q, LdsByte *qt, LdsByte *dt, LdsByte *lse_of, LdsByte *delta_of,
+                                 int b, bool border, int m0, int from, Ahead ahead) {
         RowPacks<T, DP> d;
         TurnedRows dturned, qturned;
         f32x16 sc, dp;
@@ -1052,7 +1058,8 @@ struct KeySums {
 // 64 elements), it reads ahead: a block's turned rows while its exponentials run,
 // and the next block's rows while the products with the turned ones run.
 template <typename T, int DP, int WAVES, bool DIRECT>
-__global__ __launch_bounds__(WAVES * kWave, (kKeySide<T, DP, DIRECT>)) void attention_dkdv_kernel(AttentionArgs a, unsigned total) {
+__global__ __launch_bounds__(WAVES * kWave, (kKeySide<T, DP, DIRECT>)) void attention_dkdv_kernel(AttentionArgs a,
+                                                                                                 unsigned total) {
     using L = Tile<T, DP>;
     using K = KeySums<T, DP>;
     constexpr int BM = 32 * WAVES, BN = kTileRows<T, WAVES>, NB = BN / 32;

@@ -1,7 +1,10 @@
 // Device-side helpers and argument structs of the row operators: the routed
 // exchange (rows sorted by expert and back), the segment product, the layer
-// norm, attention within segments, dropout and a classifier's loss.  Rows are packed row-major in fp32, bf16 or fp16; arithmetic is
-// fp32 throughout and every output is rounded once, when it is stored.
+// norm, attention within segments, dropout and a classifier's loss.  Rows are
+// packed row-major in fp32, bf16 or fp16; sums and statistics are fp32 and every
+// output is rounded once, when it is stored.  What stands between two matrix
+// products of 16-bit rows (attention's probabilities and gradients of scores, the
+// loss's gradient of the logits) is rounded to the rows' type there.
 #pragma once
 
 #include <hip/hip_runtime.h>

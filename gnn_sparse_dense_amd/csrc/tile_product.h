@@ -136,8 +136,10 @@ struct Copy {
             at = row * row_bytes + chunk * 16;
             if constexpr (GATHER) {
 #pragma unroll
-                for (int i = 0; i < kCopies; ++i)
-                    listed[i] = (uint32_t)o.rows[min(int64_t(row + i * kRowsPerCopy), o.outer - 1)] * row_bytes + chunk * 16;
+                for (int i = 0; i < kCopies; ++i) {
+                    const int64_t r = min(int64_t(row + i * kRowsPerCopy), o.outer - 1);
+                    listed[i] = (uint32_t)o.rows[r] * row_bytes + chunk * 16;
+                }
             }
         } else {
             constexpr int kRow = B * (int)sizeof(T);

@@ -493,7 +493,8 @@ Tensor attended(const Heads &h, const Tensor &rest, const Tensor &lse) {
     const Tensor work = scratch(bytes, h.q), out = at::empty(h.q.sizes(), h.q.options());
     check(spmm_segment_attention(ptr(h.q), apart(h.q), ptr(h.k), apart(h.k), ptr(h.v), apart(h.v),
                                  ptr<int64_t>(h.offsets), ptr<int64_t>(h.key_offsets), ptr(out), ptr(rest),
-                                 ptr<float>(lse), R, K, h.S(), H, Hk, D, h.scale, h.causal, code(h.q), ptr(work), bytes, stream_of(h.q)));
+                                 ptr<float>(lse), R, K, h.S(), H, Hk, D, h.scale, h.causal, code(h.q), ptr(work), bytes,
+                                 stream_of(h.q)));
     return out;
 }
 
@@ -558,7 +559,8 @@ Tensor segment_attention(const Tensor &q, const Tensor &k, const Tensor &v, cons
                               ": key_offsets are needed");
     }
     const double by = scale.value_or(1.0 / std::sqrt((double)q.size(2)));
-    if (wants_grad(q, k, v)) return SegmentAttention::apply(q, k, v, Heads{{}, {}, {}, offsets, key_offsets, causal, by});
+    if (wants_grad(q, k, v))
+        return SegmentAttention::apply(q, k, v, Heads{{}, {}, {}, offsets, key_offsets, causal, by});
     return attended({rows_apart(q), rows_apart(k), rows_apart(v), offsets, key_offsets, causal, by}, {}, {});
 }
 

@@ -284,9 +284,9 @@ def spmm_segment_attention_backward(q, k, v, offsets, key_offsets, out, lse, dou
             _check_tensor(name, t, (q.dtype,), like.shape, q.device)
     ws, at, n = _workspace(q.device, "spmm_segment_attention_backward_workspace", *sizes, kind)
     _check(_lib.spmm_segment_attention_backward(_ptr(q), H * D, _ptr(k), Hk * D, _ptr(v), Hk * D, _ptr(offsets),
-                                                _ptr(key_offsets), _ptr(out), _ptr(rest), _ptr(lse), _ptr(dout), _ptr(dq),
-                                                _ptr(dk), _ptr(dv), *sizes, float(scale), int(causal), kind, at, n,
-                                                _current_stream(q)))
+                                                _ptr(key_offsets), _ptr(out), _ptr(rest), _ptr(lse), _ptr(dout),
+                                                _ptr(dq), _ptr(dk), _ptr(dv), *sizes, float(scale), int(causal), kind,
+                                                at, n, _current_stream(q)))
 
 
 def spmm_dropout(x, residual, y, p: float, seed, offset: int = 0) -> None:
@@ -429,7 +429,9 @@ def dropout(x, p: float, seed, offset: int = 0, residual=None):
     is kept, forward and backward alike.  Give each step another seed (the
     tensor may change between the replays of a captured step, but not between
     a forward pass and its backward pass) and each call of a step another
-    offset.  Differentiable in x and residual."""
+    offset.  An int is copied to the GPU by each call (a launch more), and a
+    captured call keeps it: every replay drops the same elements.
+    Differentiable in x and residual (once)."""
     if not isinstance(seed, torch.Tensor):
         seed = torch.full((1,), int(seed), dtype=torch.int64, device=x.device)
     return _rows.dropout(x, p, seed, offset, residual)
@@ -441,5 +443,6 @@ def linear_cross_entropy(x, w, target, reduction: str = "mean"):
     of each row ("none", fp32 [R]), their "sum" or their "mean".  A target
     outside [0, V) means no class: the row has no loss, no gradient and does
     not count in the mean (which is zero over no rows).  Differentiable in x
-    and w."""
+    and w; in fp16 with "none", rows whose incoming gradient is below 2^-16 of
+    the largest lose bits of theirs."""
     return _rows.linear_cross_entropy(x, w, target, reduction)

@@ -586,15 +586,15 @@ int spmm_segment_attention_workspace(int64_t R, int64_t K, int64_t S, int64_t H,
                                      int64_t *bytes);
 int spmm_segment_attention(const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv,
                            const int64_t *offsets, const int64_t *key_offsets, void *out, void *rest, float *lse,
-                           int64_t R, int64_t K, int64_t S, int64_t H, int64_t Hk, int64_t D, double scale, int causal, int type,
-                           void *workspace, int64_t workspace_bytes, void *stream);
+                           int64_t R, int64_t K, int64_t S, int64_t H, int64_t Hk, int64_t D, double scale, int causal,
+                           int type, void *workspace, int64_t workspace_bytes, void *stream);
 int spmm_segment_attention_backward_workspace(int64_t R, int64_t K, int64_t S, int64_t H, int64_t Hk, int64_t D,
                                               int type, int64_t *bytes);
 int spmm_segment_attention_backward(const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv,
                                     const int64_t *offsets, const int64_t *key_offsets, const void *out,
-                                    const void *rest, const float *lse, const void *dout, void *dq, void *dk, void *dv, int64_t R,
-                                    int64_t K, int64_t S, int64_t H, int64_t Hk, int64_t D, double scale, int causal,
-                                    int type, void *workspace, int64_t workspace_bytes, void *stream);
+                                    const void *rest, const float *lse, const void *dout, void *dq, void *dk, void *dv,
+                                    int64_t R, int64_t K, int64_t S, int64_t H, int64_t Hk, int64_t D, double scale,
+                                    int causal, int type, void *workspace, int64_t workspace_bytes, void *stream);
 
 /*
  * Dropout of n elements: y[i] = residual[i] + (kept(i) ? x[i] / (1 - p) : 0)
@@ -622,7 +622,8 @@ int spmm_dropout(const void *x, const void *residual, void *y, int64_t n, double
  *   spmm_linear_cross_entropy_backward: dx [R, I] and dw [V, I] (either may be
  *   NULL) from dloss (fp32 [R] or one) and the forward pass's state.
  * The gradient of the logits is rounded to `type` where it enters a matrix
- * product; sums are fp32.  state (aligned to 8 bytes) is written by the
+ * product (in fp16 times one power of two for all rows, so with a gradient for each
+ * row those below 2^-16 of the largest lose bits); sums are fp32.  state (aligned to 8 bytes) is written by the
  * forward and read by the backward pass; the workspace of the backward pass
  * holds the gradient of the logits for as many classes at a time as fit
  * 512 MB (256 at least).
