@@ -580,7 +580,8 @@ int spmm_layer_norm_backward(const void *dy, const void *x, const void *weight, 
  * matrix product (in fp16 times powers of two that keep them clear of its ends); sums
  * and softmax statistics are fp32.
  * scale > 0; D <= 128; R * H and K * Hk < 2^31 - 4097, S * Hk < 2^24,
- * H < 2^16.
+ * H < 2^16.  Weights are divided by their sum at the end, so a segment's keys times
+ * the largest element of v must stay below 2^120 (fp16 always does).
  */
 int spmm_segment_attention_workspace(int64_t R, int64_t K, int64_t S, int64_t H, int64_t Hk, int64_t D, int type,
                                      int64_t *bytes);

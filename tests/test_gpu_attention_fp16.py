@@ -15,14 +15,16 @@ two:
 All of these are far below half a step of the outputs, so a comparison asks for the
 outputs' own precision; each test makes sure that its bounds are a small share of the
 values."""
+import ctypes
+
 import pytest
 import torch
 
 pytestmark = pytest.mark.gpu
 
 from tests import rows64  # noqa: E402
-from tests.test_gpu_attention import SLACK, on_gpu  # noqa: E402
-from tests.test_gpu_rows import half_step, normal, rng  # noqa: E402
+from tests.test_gpu_attention import SLACK, bounds, on_gpu  # noqa: E402
+from tests.test_gpu_rows import guarded, half_step, normal, rng  # noqa: E402
 
 if torch.cuda.is_available():
     import gnn_sparse_dense_amd as G
@@ -202,3 +204,88 @@ def test_wide_rows_of_joined_parts_follow_the_same_bits():
         leaves[i].requires_grad_()
         out = G.segment_attention(*leaves, o, ko)
         assert torch.equal(torch.autograd.grad(out, leaves[i], dout.to(DEV))[0], got[1 + i])
+
+
+SHAPES = [([1], [1], 1, 1, 8), ([3, 0, 70, 1], None, 6, 2, 40), ([300, 1, 257], None, 4, 1, 72),
+          ([2] * 700, None, 2, 2, 16), ([2100], None, 4, 1, 128), ([2500, 1], [40, 9], 2, 1, 96),
+          ([0, 0], [5, 7], 3, 1, 24), ([1, 1], [3000, 20], 8, 2, 64)]
+
+
+@pytest.mark.parametrize("rows,keys,H,Hk,D", SHAPES)
+def test_workspaces_of_exactly_their_size(rows, keys, H, Hk, D):
+    """The C calls with workspaces of as many bytes as they ask for, guarded: nothing
+    beside them is written, and the results are the binding's."""
+    g = rng(sum(rows), H, D)
+    ro, ko = bounds(rows), bounds(rows if keys is None else keys)
+    R, K, S = ro[-1] + 2, ko[-1] + 3, len(rows)
+    q, k, v, dout = (normal(g, n, h, D, dtype=F16).to(DEV) for n, h in ((R, H), (K, Hk), (K, Hk), (R, H)))
+    o, kof = torch.tensor(ro, device=DEV), torch.tensor(ko, device=DEV)
+    sizes, lib = (R, K, S, H, Hk, D), G.lib()
+
+    def workspace(call):
+        n = ctypes.c_int64()
+        assert getattr(lib, call)(*sizes, G.SPMM_F16, ctypes.byref(n)) == 0
+        whole, untouched = guarded((max(1, n.value // 4),), torch.float32)
+        return whole, n.value, untouched
+
+    at = [t.data_ptr() for t in (q, k, v, o, kof)]
+    heads = [at[0], H * D, at[1], Hk * D, at[2], Hk * D, at[3], at[4]]
+    for causal in (0, 1):
+        out, rest, dq = (torch.empty_like(q) for _ in range(3))
+        lse, dk, dv = torch.empty(R, H, device=DEV), torch.empty_like(k), torch.empty_like(v)
+        work, n, first = workspace("spmm_segment_attention_workspace")
+        back, m, second = workspace("spmm_segment_attention_backward_workspace")
+        stream = torch.cuda.current_stream().cuda_stream
+        how = [*sizes, D ** -0.5, causal, G.SPMM_F16]
+        made = [t.data_ptr() for t in (out, rest, lse)]
+        grads = [t.data_ptr() for t in (dout, dq, dk, dv)]
+        assert lib.spmm_segment_attention(*heads, *made, *how, work.data_ptr(), n, stream) == 0
+        assert lib.spmm_segment_attention_backward(*heads, *made, *grads, *how, back.data_ptr(), m, stream) == 0
+        torch.cuda.synchronize()
+        first(), second()
+        leaves = [t.clone().requires_grad_() for t in (q, k, v)]
+        same = G.segment_attention(*leaves, o, kof, causal=bool(causal))
+        for a, b in zip((out, dq, dk, dv), (same, *torch.autograd.grad(same, leaves, dout))):
+            assert torch.equal(a, b)
+
+
+def test_captured_and_on_two_streams():
+    """Forward and backward captured and replayed with gradients of other sizes and
+    other offsets; two passes at once on two streams."""
+    g = rng(41)
+    shapes = ((400, 4), (400, 2), (400, 2))
+    static = [normal(g, n, h, 64, dtype=F16).to(DEV).requires_grad_() for n, h in shapes]
+    dout, o = normal(g, 400, 4, 64, dtype=F16).to(DEV), torch.tensor([0, 300, 400], device=DEV)
+
+    def run(leaves, o, dout):
+        out = G.segment_attention(*leaves, o, causal=True)
+        return [out, *torch.autograd.grad(out, leaves, dout)]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run(static, o, dout)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side, capture_error_mode="thread_local"):
+        got = run(static, o, dout)
+    for rep, (size, lengths) in enumerate([(1e-4, [0, 399, 400]), (1024.0, [0, 10, 400]), (1.0, [5, 200, 390])]):
+        new = [normal(g, n, h, 64, dtype=F16).to(DEV) for n, h in shapes]
+        with torch.no_grad():
+            for a, b in zip(static, new):
+                a.copy_(b)
+            dout.copy_(normal(g, 400, 4, 64, scale=size).to(F16))
+            o.copy_(torch.tensor(lengths))
+        float(torch.randn(1 << 18, device=DEV).sum())
+        graph.replay()
+        torch.cuda.synchronize()
+        eager = run([t.requires_grad_() for t in new], torch.tensor(lengths, device=DEV), dout.clone())
+        assert all(torch.equal(a, b) for a, b in zip(got, eager)), f"replay {rep}"
+    both, streams = [], [torch.cuda.Stream() for _ in range(2)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            both.append(run([t.detach().clone().requires_grad_() for t in new], torch.tensor(lengths, device=DEV),
+                            dout.clone()))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for pair in zip(*both, eager) for a in pair[:2] for b in pair[2:])
